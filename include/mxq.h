@@ -328,6 +328,144 @@ mxq_status mxq_gemm_noalloc(const void* A, const uint8_t* sA, const void* B, con
                             int fmt, int64_t M, int64_t N, int64_t K, void* C, int out_dtype,
                             void* stream);
 
+/* ---------------------------------------------------------------------------
+ * FP8 with one fp32 scale per block of 128, and the norms in front of it
+ * ---------------------------------------------------------------------------
+ * The other common 8-bit recipe beside MX: E4M3 or E5M2 codes with a plain
+ * fp32 scale for each 1x128 block (activations, gradients) or 128x128 tile
+ * (weights), which no E8M0 exponent can express.
+ *
+ * A block of values v has
+ *   scale = max(amax / fmax, 2^-126)   fmax = 448 (E4M3) or 57344 (E5M2)
+ *   code  = RN_sat(v * (1 / scale))    fp32 division, product and E4M3/E5M2
+ *                                      conversion each rounded to nearest even
+ * and stands for code * scale.  A block that holds a NaN or an infinity has
+ * scale NaN and zero codes.  The last block of a line is shorter when the
+ * line's length is no multiple of 128.
+ *
+ * Code lines of `blocked` elements have a pitch of mxq_fp8_pitch(blocked)
+ * bytes (blocked rounded up to 16); the quantizers write zeros past the end.
+ * Scales:
+ *  MXQ_FP8_LINES: one per line and 128 elements, [ceil(blocked / 128)]
+ *    [lines rounded up to 4] fp32 -- all lines of one K block side by side,
+ *    as the product reads them.  The quantizers write the scale of an
+ *    all-zero block (2^-126) for the padding lines.
+ *  MXQ_FP8_TILES: one per 128x128 tile, [ceil(lines / 128)]
+ *    [ceil(blocked / 128)] fp32.
+ * Codes must be 16-byte aligned, scales 16-byte (lines) or 4-byte (tiles).
+ */
+typedef enum { MXQ_FP8_LINES = 0, MXQ_FP8_TILES = 1 } mxq_fp8_scales;
+
+/* Bytes between two code lines of `blocked` elements (0 on bad arguments). */
+size_t mxq_fp8_pitch(int64_t blocked);
+
+/* Floats of a scale buffer (0 on bad arguments). scales: mxq_fp8_scales. */
+size_t mxq_fp8_scale_count(int64_t lines, int64_t blocked, int scales);
+
+/*
+ * Quantization of a bf16 tensor x [rows][cols] in blocks of 1x128 along the
+ * rows (MXQ_ROWWISE: lines = rows, blocked = cols) or of 128x1 along the
+ * columns, stored transposed (MXQ_COLWISE_T: lines = cols, blocked = rows).
+ * fmt: MXQ_E4M3 or MXQ_E5M2.  Any sizes; rows == 0 or cols == 0 is a no-op.
+ * x must be 16-byte aligned.
+ */
+mxq_status mxq_fp8_quantize(const void* x, int64_t rows, int64_t cols, int layout, int fmt,
+                            void* codes, float* scales, void* stream);
+
+/* Both layouts of mxq_fp8_quantize from one read of x. */
+mxq_status mxq_fp8_quantize_dual(const void* x, int64_t rows, int64_t cols, int fmt_r,
+                                 void* codes_r, float* scales_r, int fmt_c, void* codes_c,
+                                 float* scales_c, void* stream);
+
+/*
+ * Quantization of a bf16 weight x [rows][cols] in 128x128 tiles: its codes and
+ * tile scales, and -- unless codes_t and scales_t are NULL -- the transposed
+ * codes [cols][rows] with the transposed scales (the operand of the input
+ * gradient), from one read of x.
+ */
+mxq_status mxq_fp8_quantize_tiles(const void* x, int64_t rows, int64_t cols, int fmt, void* codes,
+                                  float* scales, void* codes_t, float* scales_t, void* stream);
+
+/*
+ * C[m][n] = sum over K blocks b of  sA[b][m] * sB(n, b) * sum_{k in b} A[m][k] B[n][k]
+ * with the inner sums on the tensor cores in fp32 and the outer one in fp32.
+ * A: codes of M lines of K elements, MXQ_FP8_LINES scales.  B: codes of N lines
+ * of K elements; b_scales says whether sB holds MXQ_FP8_TILES (a weight) or
+ * MXQ_FP8_LINES scales (the weight gradient's second operand).  fmt_a, fmt_b:
+ * MXQ_E4M3 or MXQ_E5M2, independently.  C: [M][N], MXQ_OUT_F32 or
+ * MXQ_OUT_BF16, 16-byte aligned.  Any M, N, K below 2^31: M == 0 or N == 0 is
+ * a no-op, K == 0 writes zeros.  The bytes between K and the pitch are not
+ * read.  No workspace.
+ */
+mxq_status mxq_fp8_gemm(const void* A, const float* sA, int fmt_a, const void* B, const float* sB,
+                        int fmt_b, int b_scales, int64_t M, int64_t N, int64_t K, void* C,
+                        int out_dtype, void* stream);
+
+/*
+ * Layer norm and RMS norm of the rows of x [rows][cols]:
+ *   MXQ_NORM_LAYER  h = (x - mean(x)) * rstd,  rstd = 1 / sqrt(var(x) + eps)
+ *   MXQ_NORM_RMS    h = x * rstd,              rstd = 1 / sqrt(mean(x^2) + eps)
+ *   y = h * weight (+ bias)
+ * with the statistics and h in fp32 and one rounding of y to x's type.
+ */
+typedef enum { MXQ_NORM_LAYER = 0, MXQ_NORM_RMS = 1 } mxq_norm_kind;
+
+/* Arguments of mxq_norm_forward (host memory, read during the call). */
+typedef struct {
+  const void* x;       /* [rows][cols] of x_dtype                              */
+  const void* weight;  /* [cols] of w_dtype                                    */
+  const void* bias;    /* [cols] of w_dtype, or NULL                           */
+  void* y;             /* [rows][cols] of x_dtype, or NULL when codes is set   */
+  float* mean;         /* [rows], or NULL (MXQ_NORM_LAYER only)                */
+  float* rstd;         /* [rows], or NULL                                      */
+  void* codes;         /* NULL, or E4M3/E5M2 codes of y in 1x128 blocks ...    */
+  float* scales;       /* ... with MXQ_FP8_LINES scales, of the fp32 y         */
+  int64_t rows, cols;
+  float eps;
+  int kind;            /* mxq_norm_kind                                        */
+  int x_dtype;         /* MXQ_OUT_F32 or MXQ_OUT_BF16                          */
+  int w_dtype;
+  int fmt;             /* element format of codes                              */
+} mxq_norm_args;
+
+/*
+ * The forward pass; with codes set it also writes (or, y == NULL, only writes)
+ * the product's operand, quantized from the fp32 values by the rule above.
+ * x, weight, bias, y and codes must be 16-byte aligned.  rows == 0 or
+ * cols == 0 is a no-op.
+ */
+mxq_status mxq_norm_forward(const mxq_norm_args* args, void* stream);
+
+/* Arguments of mxq_norm_backward (host memory, read during the call). */
+typedef struct {
+  const void* dy;      /* [rows][cols] of x_dtype                              */
+  const void* x;       /* [rows][cols] of x_dtype                              */
+  const void* weight;  /* [cols] of w_dtype                                    */
+  const float* mean;   /* [rows] (MXQ_NORM_LAYER)                              */
+  const float* rstd;   /* [rows]                                               */
+  void* dx;            /* [rows][cols] of x_dtype                              */
+  float* dweight;      /* [cols]                                               */
+  float* dbias;        /* [cols], or NULL                                      */
+  void* workspace;     /* 256-byte aligned                                     */
+  size_t workspace_bytes;
+  int64_t rows, cols;
+  int kind;
+  int x_dtype;
+  int w_dtype;
+} mxq_norm_grad_args;
+
+/*
+ * The backward pass, from the forward pass's statistics:
+ *   g = dy * weight,  dx = rstd * (g - mean(g) - h * mean(g h))   (RMS: no mean(g))
+ *   dweight = sum over rows of dy * h,  dbias = sum over rows of dy
+ * The row sums are taken in a fixed order: the same inputs give the same bits.
+ * rows == 0 writes zero gradients; cols == 0 is a no-op.
+ */
+mxq_status mxq_norm_backward(const mxq_norm_grad_args* args, void* stream);
+
+/* Bytes of workspace mxq_norm_backward needs (0 on bad arguments or rows == 0). */
+size_t mxq_norm_backward_workspace_size(int64_t rows, int64_t cols);
+
 /*
  * Synchronizes `stream`, then reports and clears device-side errors recorded
  * by earlier calls on any stream (MXQ_ERR_TIMEOUT when a bounded wait inside

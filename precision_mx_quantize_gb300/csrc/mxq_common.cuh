@@ -30,6 +30,11 @@ enum : uint32_t {
   SITE_GEMM_TMEM_EMPTY = 6,
   SITE_GEMM_DRAIN = 7,
   SITE_DEBUG = 8,
+  SITE_FP8_EMPTY = 9,
+  SITE_FP8_FULL = 10,
+  SITE_FP8_TMEM_FULL = 11,
+  SITE_FP8_TMEM_EMPTY = 12,
+  SITE_FP8_DRAIN = 13,
   // bounds checks of the bounds-checked build (MXQ_DEBUG_BOUNDS)
   SITE_B_QUANT_TILE = 16,    // quantizer tile coordinates
   SITE_B_QUANT_TMA = 17,     // quantizer TMA coordinate alignment
@@ -42,6 +47,12 @@ enum : uint32_t {
   SITE_B_GEMM_QSCALE = 24,   // GEMM epilogue stores of output scales
   SITE_B_SF_CHUNKS = 25,     // scale re-layout stores
   SITE_B_GEMM_TMA = 26,      // GEMM TMA coordinates
+  SITE_B_FP8_LOAD = 27,      // block-128 quantizer loads
+  SITE_B_FP8_CODES = 28,     // block-128 quantizer code stores
+  SITE_B_FP8_SCALES = 29,    // block-128 quantizer scale stores
+  SITE_B_FP8_GEMM = 30,      // block-128 GEMM stores of C
+  SITE_B_NORM = 31,          // norm loads and stores
+  SITE_B_NORM_GRAD = 32,     // norm backward partial sums and gradients
 };
 
 MXQ_DEV void record_error(uint32_t* word, uint32_t status, uint32_t site) {

@@ -52,8 +52,17 @@ uint32_t take_quant_error();
 uint32_t take_quant_e5m2_error();
 uint32_t take_ablation_error();
 uint32_t take_gemm_error();
+uint32_t take_fp8_quant_error();
+uint32_t take_fp8_gemm_error();
+uint32_t take_norm_error();
+
+// Block-128 FP8 buffers: code pitch, lines of a scale row.
+inline int64_t fp8_pitch(int64_t blocked) { return (blocked + 15) / 16 * 16; }
+inline int64_t fp8_lines(int64_t lines) { return (lines + 3) / 4 * 4; }
 
 inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+
+inline bool is_fp8(int fmt) { return fmt == MXQ_E4M3 || fmt == MXQ_E5M2; }
 
 inline mxq_status launch_status() {
   return cudaGetLastError() == cudaSuccess ? MXQ_OK : MXQ_ERR_CUDA;

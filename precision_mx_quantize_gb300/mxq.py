@@ -8,6 +8,10 @@ Low-level functions keep the C names (``mxq_quantize`` ...) and take raw
 pointers; the tensor-level helpers follow the names of the method's
 statement: ``mx_quantize``, ``hadamard_mx_quantize``, ``mx_quantize_dual``,
 ``mx_quantize_ablation``, ``mx_dequantize``, ``mx_gemm``, ``mx_gemm_quantize``.
+The FP8 recipe with one fp32 scale per block of 128 has ``fp8_quantize``,
+``fp8_quantize_dual``, ``fp8_quantize_tiles`` and ``fp8_gemm``; the norms in
+front of it ``layer_norm``, ``rms_norm``, their ``_quantize`` and
+``_backward`` forms.
 """
 
 from __future__ import annotations
@@ -32,6 +36,10 @@ SCALES_ROWMAJOR, SCALES_TC = 0, 1
 SCALE_LAYOUTS = {"rowmajor": SCALES_ROWMAJOR, "tc": SCALES_TC,
                  SCALES_ROWMAJOR: SCALES_ROWMAJOR, SCALES_TC: SCALES_TC}
 OUT_F32, OUT_BF16 = 0, 1
+FP8_LINES, FP8_TILES = 0, 1
+B_SCALES = {"line": FP8_LINES, "tile": FP8_TILES, FP8_LINES: FP8_LINES, FP8_TILES: FP8_TILES}
+FP8_FMTS = {"e4m3": E4M3, "e5m2": E5M2, E4M3: E4M3, E5M2: E5M2}
+NORM_LAYER, NORM_RMS = 0, 1
 FMTS = {"e4m3": E4M3, "e2m1": E2M1, "e5m2": E5M2, E4M3: E4M3, E2M1: E2M1, E5M2: E5M2}
 AXES = {"row": ROWWISE, "col": COLWISE_T, ROWWISE: ROWWISE, COLWISE_T: COLWISE_T}
 
@@ -60,6 +68,15 @@ SIGNATURES = [
     ("mxq_gemm_workspace_size", _SZ, [_I64, _I64, _I64, _I]),
     ("mxq_gemm_noalloc", _I, [_P, _P, _P, _P, _I, _I64, _I64, _I64, _P, _I, _P]),
     ("mxq_gemm_grouped", _I, [_P, _I, _I, _P]),
+    ("mxq_fp8_pitch", _SZ, [_I64]),
+    ("mxq_fp8_scale_count", _SZ, [_I64, _I64, _I]),
+    ("mxq_fp8_quantize", _I, [_P, _I64, _I64, _I, _I, _P, _P, _P]),
+    ("mxq_fp8_quantize_dual", _I, [_P, _I64, _I64, _I, _P, _P, _I, _P, _P, _P]),
+    ("mxq_fp8_quantize_tiles", _I, [_P, _I64, _I64, _I, _P, _P, _P, _P, _P]),
+    ("mxq_fp8_gemm", _I, [_P, _P, _I, _P, _P, _I, _I, _I64, _I64, _I64, _P, _I, _P]),
+    ("mxq_norm_forward", _I, [_P, _P]),
+    ("mxq_norm_backward", _I, [_P, _P]),
+    ("mxq_norm_backward_workspace_size", _SZ, [_I64, _I64]),
     ("mxq_check", _I, [_P]),
     ("mxq_set_wait_timeout_ns", None, [_U64]),
     ("mxq_debug_expire_wait", _I, [_U64, _P]),
@@ -70,6 +87,25 @@ class GemmProblem(ctypes.Structure):
     _fields_ = [("A", ctypes.c_void_p), ("sA", ctypes.c_void_p), ("B", ctypes.c_void_p),
                 ("sB", ctypes.c_void_p), ("C", ctypes.c_void_p), ("M", ctypes.c_int64),
                 ("N", ctypes.c_int64), ("K", ctypes.c_int64), ("out_dtype", ctypes.c_int)]
+
+
+class NormArgs(ctypes.Structure):
+    """mxq_norm_args of the C header (field order and types as declared)."""
+    _fields_ = [("x", ctypes.c_void_p), ("weight", ctypes.c_void_p), ("bias", ctypes.c_void_p),
+                ("y", ctypes.c_void_p), ("mean", ctypes.c_void_p), ("rstd", ctypes.c_void_p),
+                ("codes", ctypes.c_void_p), ("scales", ctypes.c_void_p), ("rows", ctypes.c_int64),
+                ("cols", ctypes.c_int64), ("eps", ctypes.c_float), ("kind", ctypes.c_int),
+                ("x_dtype", ctypes.c_int), ("w_dtype", ctypes.c_int), ("fmt", ctypes.c_int)]
+
+
+class NormGradArgs(ctypes.Structure):
+    """mxq_norm_grad_args of the C header (field order and types as declared)."""
+    _fields_ = [("dy", ctypes.c_void_p), ("x", ctypes.c_void_p), ("weight", ctypes.c_void_p),
+                ("mean", ctypes.c_void_p), ("rstd", ctypes.c_void_p), ("dx", ctypes.c_void_p),
+                ("dweight", ctypes.c_void_p), ("dbias", ctypes.c_void_p),
+                ("workspace", ctypes.c_void_p), ("workspace_bytes", ctypes.c_size_t),
+                ("rows", ctypes.c_int64), ("cols", ctypes.c_int64), ("kind", ctypes.c_int),
+                ("x_dtype", ctypes.c_int), ("w_dtype", ctypes.c_int)]
 
 
 _lib = None
@@ -203,6 +239,39 @@ def mxq_gemm_grouped(problems, count, fmt, stream):
 
 def mxq_gemm_workspace_size(M, N, K, fmt):
     return lib().mxq_gemm_workspace_size(M, N, K, fmt)
+
+
+def mxq_fp8_quantize(x, rows, cols, layout, fmt, codes, scales, stream):
+    return lib().mxq_fp8_quantize(x, rows, cols, layout, fmt, codes, scales, stream)
+
+
+def mxq_fp8_quantize_dual(x, rows, cols, fmt_r, codes_r, scales_r, fmt_c, codes_c, scales_c,
+                          stream):
+    return lib().mxq_fp8_quantize_dual(x, rows, cols, fmt_r, codes_r, scales_r, fmt_c, codes_c,
+                                       scales_c, stream)
+
+
+def mxq_fp8_quantize_tiles(x, rows, cols, fmt, codes, scales, codes_t, scales_t, stream):
+    return lib().mxq_fp8_quantize_tiles(x, rows, cols, fmt, codes, scales, codes_t, scales_t,
+                                        stream)
+
+
+def mxq_fp8_gemm(A, sA, fmt_a, B, sB, fmt_b, b_scales, M, N, K, C, out_dtype, stream):
+    return lib().mxq_fp8_gemm(A, sA, fmt_a, B, sB, fmt_b, b_scales, M, N, K, C, out_dtype, stream)
+
+
+def mxq_norm_forward(args, stream):
+    """args: address of a NormArgs structure in host memory."""
+    return lib().mxq_norm_forward(args, stream)
+
+
+def mxq_norm_backward(args, stream):
+    """args: address of a NormGradArgs structure in host memory."""
+    return lib().mxq_norm_backward(args, stream)
+
+
+def mxq_norm_backward_workspace_size(rows, cols):
+    return lib().mxq_norm_backward_workspace_size(rows, cols)
 
 
 def mxq_check(stream=None):
@@ -501,3 +570,210 @@ def mx_gemm_quantize(A, sA, B, sB, fmt, M, N, K, out_fmt="e4m3", out=None, works
                              scales.data_ptr(), SCALE_LAYOUTS[out_scale_layout], ws_ptr, ws_n,
                              _stream(A.device)), "mxq_gemm_quantize_ex")
     return codes, scales
+
+
+# ---- FP8 with one fp32 scale per block of 128 ---------------------------------------
+
+def fp8_shapes(lines: int, blocked: int, scales="line"):
+    """(codes shape, scales shape) of `lines` code lines of `blocked` elements:
+    a line's pitch is `blocked` rounded up to 16; line scales are [ceil(blocked
+    / 128)][lines rounded up to 4], tile scales [ceil(lines / 128)][ceil(blocked
+    / 128)]."""
+    kb = (blocked + 127) // 128
+    ss = (kb, (lines + 3) // 4 * 4) if B_SCALES[scales] == FP8_LINES else ((lines + 127) // 128, kb)
+    return (lines, (blocked + 15) // 16 * 16), ss
+
+
+def _fp8_buffers(lines, blocked, scales, device):
+    cs, ss = fp8_shapes(lines, blocked, scales)
+    return (torch.empty(cs, dtype=torch.uint8, device=device),
+            torch.empty(ss, dtype=torch.float32, device=device))
+
+
+def _need_fp8(codes, scales, lines, blocked, kind, dev, tag=""):
+    """The code and scale buffers of `lines` lines of `blocked` elements."""
+    cs, ss = fp8_shapes(lines, blocked, kind)
+    _need(codes, "codes" + tag, torch.uint8, cs[0] * cs[1], dev)
+    _need(scales, "scales" + tag, torch.float32, ss[0] * ss[1], dev)
+
+
+def fp8_quantize(x: torch.Tensor, axis="row", fmt="e4m3", out=None):
+    """FP8 codes of a contiguous bf16 CUDA tensor [rows, cols] with one fp32
+    scale per 1x128 block along `axis` ("col": stored transposed); returns
+    (codes, scales), shaped as fp8_shapes says."""
+    _need_input(x)
+    R, C = x.shape
+    ax, f = AXES[axis], FP8_FMTS[fmt]
+    lines, blocked = (R, C) if ax == ROWWISE else (C, R)
+    codes, scales = out if out is not None else _fp8_buffers(lines, blocked, "line", x.device)
+    dev = x.get_device()
+    _need_fp8(codes, scales, lines, blocked, "line", dev)
+    _ok(mxq_fp8_quantize(x.data_ptr(), R, C, ax, f, codes.data_ptr(), scales.data_ptr(),
+                         _stream(dev)), "mxq_fp8_quantize")
+    return codes, scales
+
+
+def fp8_quantize_dual(x: torch.Tensor, fmt_r="e4m3", fmt_c="e4m3", out=None):
+    """Both layouts of fp8_quantize from one read of x; returns (codes_r,
+    scales_r, codes_c, scales_c)."""
+    _need_input(x)
+    R, C = x.shape
+    fr, fc = FP8_FMTS[fmt_r], FP8_FMTS[fmt_c]
+    if out is None:
+        out = _fp8_buffers(R, C, "line", x.device) + _fp8_buffers(C, R, "line", x.device)
+    cr, sr, cc, sc = out
+    dev = x.get_device()
+    _need_fp8(cr, sr, R, C, "line", dev, "_r")
+    _need_fp8(cc, sc, C, R, "line", dev, "_c")
+    _ok(mxq_fp8_quantize_dual(x.data_ptr(), R, C, fr, cr.data_ptr(), sr.data_ptr(), fc,
+                              cc.data_ptr(), sc.data_ptr(), _stream(dev)), "mxq_fp8_quantize_dual")
+    return cr, sr, cc, sc
+
+
+def fp8_quantize_tiles(w: torch.Tensor, fmt="e4m3", out=None):
+    """FP8 codes of a bf16 weight [rows, cols] with one fp32 scale per 128x128
+    tile, and the transposed codes and scales; returns (codes, scales, codes_t,
+    scales_t).  In `out`, codes_t and scales_t may be None: not written."""
+    _need_input(w)
+    R, C = w.shape
+    f = FP8_FMTS[fmt]
+    if out is None:
+        out = _fp8_buffers(R, C, "tile", w.device) + _fp8_buffers(C, R, "tile", w.device)
+    codes, scales, codes_t, scales_t = out
+    dev = w.get_device()
+    _need_fp8(codes, scales, R, C, "tile", dev)
+    if codes_t is not None or scales_t is not None:
+        _need_fp8(codes_t, scales_t, C, R, "tile", dev, "_t")
+    _ok(mxq_fp8_quantize_tiles(w.data_ptr(), R, C, f, codes.data_ptr(), scales.data_ptr(),
+                               _ptr(codes_t), _ptr(scales_t), _stream(dev)),
+        "mxq_fp8_quantize_tiles")
+    return codes, scales, codes_t, scales_t
+
+
+def fp8_gemm(A, sA, B, sB, M, N, K, fmt_a="e4m3", fmt_b="e4m3", b_scales="tile",
+             out_dtype=torch.bfloat16, out=None):
+    """C[M, N] = dec(A) @ dec(B)^T of block-128 FP8 codes (K-major lines).
+
+    A: M lines with line scales.  B: N lines with tile scales (b_scales "tile",
+    a weight) or line scales ("line", the weight gradient)."""
+    od = _out_code(out_dtype)
+    fa, fb, bs = FP8_FMTS[fmt_a], FP8_FMTS[fmt_b], B_SCALES[b_scales]
+    M, N, K = int(M), int(N), int(K)
+    _need(A, "A", torch.uint8, 0)
+    dev = A.get_device()
+    _need_fp8(A, sA, M, K, "line", dev, "_A")
+    _need_fp8(B, sB, N, K, bs, dev, "_B")
+    if out is None:
+        out = torch.empty((M, N), dtype=out_dtype, device=A.device)
+    _need(out, "out", out_dtype, M * N, dev)
+    _ok(mxq_fp8_gemm(A.data_ptr(), sA.data_ptr(), fa, B.data_ptr(), sB.data_ptr(), fb, bs, M, N, K,
+                     out.data_ptr(), od, _stream(dev)), "mxq_fp8_gemm")
+    return out
+
+
+# ---- layer norm and RMS norm ---------------------------------------------------------
+
+def _need_norm(x, weight, bias):
+    """x [rows, cols] and the vectors of its norm; returns (device index, code of
+    x's dtype, code of weight's dtype)."""
+    if not isinstance(x, torch.Tensor) or x.dim() != 2:
+        raise ValueError("x must be a 2-D torch.Tensor [rows, cols]")
+    xd = _out_code_of(x, "x")
+    _need(x, "x", None, 0)
+    dev = x.get_device()
+    _need(weight, "weight", None, x.shape[1], dev)
+    wd = _out_code_of(weight, "weight")
+    if bias is not None:
+        _need(bias, "bias", weight.dtype, x.shape[1], dev)
+    return dev, xd, wd
+
+
+def _out_code_of(t, name):
+    if t.dtype is torch.bfloat16:
+        return OUT_BF16
+    if t.dtype is torch.float32:
+        return OUT_F32
+    raise ValueError(f"{name} must be torch.float32 or torch.bfloat16, got {t.dtype}")
+
+
+def _norm_forward(x, weight, bias, eps, kind, fmt, with_y, out):
+    """(y or None, codes or None, scales or None, mean or None, rstd)."""
+    dev, xd, wd = _need_norm(x, weight, bias)
+    R, C = x.shape
+    y = codes = scales = None
+    if with_y:
+        y = torch.empty_like(x) if out is None else out
+        _need(y, "out", x.dtype, R * C, dev)
+    if fmt is not None:
+        codes, scales = _fp8_buffers(R, C, "line", x.device) if out is None else out
+        _need_fp8(codes, scales, R, C, "line", dev)
+        fmt = FP8_FMTS[fmt]
+    stats = torch.empty((2 if kind == NORM_LAYER else 1, R), dtype=torch.float32, device=x.device)
+    rstd = stats[0]
+    mean = stats[1] if kind == NORM_LAYER else None
+    a = NormArgs(x.data_ptr(), weight.data_ptr(), _ptr(bias), _ptr(y), _ptr(mean), rstd.data_ptr(),
+                 _ptr(codes), _ptr(scales), R, C, eps, kind, xd, wd, fmt or 0)
+    _ok(mxq_norm_forward(ctypes.addressof(a), _stream(dev)), "mxq_norm_forward")
+    return y, codes, scales, mean, rstd
+
+
+def layer_norm(x: torch.Tensor, weight, bias=None, eps=1e-5, out=None):
+    """Layer norm of the rows of a contiguous bf16 or fp32 CUDA tensor; weight
+    and bias bf16 or fp32.  Returns (y, mean, rstd), the statistics in fp32."""
+    y, _, _, mean, rstd = _norm_forward(x, weight, bias, eps, NORM_LAYER, None, True, out)
+    return y, mean, rstd
+
+
+def rms_norm(x: torch.Tensor, weight, eps=1e-5, out=None):
+    """RMS norm of the rows of a contiguous bf16 or fp32 CUDA tensor; returns
+    (y, rstd)."""
+    y, _, _, _, rstd = _norm_forward(x, weight, None, eps, NORM_RMS, None, True, out)
+    return y, rstd
+
+
+def layer_norm_quantize(x: torch.Tensor, weight, bias=None, eps=1e-5, fmt="e4m3", out=None):
+    """Layer norm straight to row-wise block-128 FP8 codes of the fp32 values;
+    returns (codes, scales, mean, rstd)."""
+    _, codes, scales, mean, rstd = _norm_forward(x, weight, bias, eps, NORM_LAYER, fmt, False, out)
+    return codes, scales, mean, rstd
+
+
+def rms_norm_quantize(x: torch.Tensor, weight, eps=1e-5, fmt="e4m3", out=None):
+    """RMS norm straight to row-wise block-128 FP8 codes of the fp32 values;
+    returns (codes, scales, rstd)."""
+    _, codes, scales, _, rstd = _norm_forward(x, weight, None, eps, NORM_RMS, fmt, False, out)
+    return codes, scales, rstd
+
+
+def _norm_backward(dy, x, weight, mean, rstd, kind, out, workspace):
+    dev, xd, wd = _need_norm(x, weight, None)
+    R, C = x.shape
+    _need(dy, "dy", x.dtype, R * C, dev)
+    _need(rstd, "rstd", torch.float32, R, dev)
+    if kind == NORM_LAYER:
+        _need(mean, "mean", torch.float32, R, dev)
+    dx = torch.empty_like(x) if out is None else out
+    _need(dx, "out", x.dtype, R * C, dev)
+    if workspace is None:
+        n = mxq_norm_backward_workspace_size(R, C)
+        workspace = torch.empty(max(int(n), 256), dtype=torch.uint8, device=x.device)
+    _need(workspace, "workspace", torch.uint8, 0, dev)   # its size is checked by the library
+    grads = torch.empty((2 if kind == NORM_LAYER else 1, C), dtype=torch.float32, device=x.device)
+    dw = grads[0]
+    db = grads[1] if kind == NORM_LAYER else None
+    a = NormGradArgs(dy.data_ptr(), x.data_ptr(), weight.data_ptr(), _ptr(mean), rstd.data_ptr(),
+                     dx.data_ptr(), dw.data_ptr(), _ptr(db), workspace.data_ptr(),
+                     workspace.numel(), R, C, kind, xd, wd)
+    _ok(mxq_norm_backward(ctypes.addressof(a), _stream(dev)), "mxq_norm_backward")
+    return dx, dw, db
+
+
+def layer_norm_backward(dy, x, weight, mean, rstd, out=None, workspace=None):
+    """Gradients of layer_norm from its statistics; returns (dx, dweight, dbias),
+    dx in x's dtype and the others in fp32."""
+    return _norm_backward(dy, x, weight, mean, rstd, NORM_LAYER, out, workspace)
+
+
+def rms_norm_backward(dy, x, weight, rstd, out=None, workspace=None):
+    """Gradients of rms_norm from its statistics; returns (dx, dweight)."""
+    return _norm_backward(dy, x, weight, None, rstd, NORM_RMS, out, workspace)[:2]
