@@ -14,7 +14,23 @@
 //   warp 1      allocates tensor memory; one lane issues the four MMAs
 //               (kind::f8f6f4, K = 32 each) of every stage;
 //   warps 2-5   epilogue: lane = line of B, T accumulators per thread.
+//
+// Larger products (fp8_gemm_pair): clusters of two CTAs run the pair MMA
+// (cta_group::2) on 256x256 tiles, persistent over tiles.  Two accumulators of
+// 256 columns fill tensor memory: the MMAs of one K block run while the other
+// block's accumulator is read back.
+//   warp 0      (both CTAs) TMA producer: own 128 lines of A and of B;
+//   warp 1      (both CTAs) tensor memory; the leader's lane issues the MMAs;
+//   warps 4-11  (both CTAs) accumulation: a thread owns 128 columns of one row
+//               of C in registers (64 packed fp32 pairs) for the whole K loop,
+//               adds each K block with one packed multiply-add per pair (line
+//               scales of B: one more multiply), and stores the row.
+// The accumulation warps take their registers from the control warps
+// (setmaxnreg), since 128 accumulators and 64 staged values do not fit the
+// even share.
 #include <string.h>
+
+#include <mutex>
 
 #include "fp8_common.cuh"
 #include "mxq_host.h"
@@ -260,6 +276,398 @@ __global__ void __launch_bounds__(L_THREADS)
   if (warp == 1) tmem_dealloc(tmem, L::TMEM);
 }
 
+// ---- 256 x 256 tiles on CTA pairs ------------------------------------------------
+constexpr int P_THREADS = 384;                   // one control and two accumulation warpgroups
+constexpr int P_CTRL_REGS = 56, P_ACC_REGS = 216;
+// the split below is drawn from the registers the block is launched with
+constexpr int P_MIN_REGS = (128 * P_CTRL_REGS + 256 * P_ACC_REGS + P_THREADS - 1) / P_THREADS;
+constexpr int P_OPERAND = 128 * 128;             // a stage's lines of A, or of B, of one CTA
+constexpr int P_STAGE = 2 * P_OPERAND;
+
+template <bool LINES>
+struct Pair {
+  // line scales of B: a warp's 128 columns of a K block, two buffers
+  static constexpr int SCALES = LINES ? 8 * 2 * 128 * 4 : 0;
+  static constexpr int STAGES = LINES ? 6 : 7;
+  static constexpr int SMEM = STAGES * P_STAGE + SCALES + 256 + 1024;
+  static_assert(SMEM <= 227 * 1024, "shared memory of one CTA");
+};
+
+struct PArgs {
+  FArgs f;
+  int32_t n_mp, n_nt, n_tiles;   // 256-row and 256-column tiles
+  int32_t group, group_n;        // tile order (tile_coords)
+  int32_t store;                 // 2: 32-byte stores of C rows, 1: 16-byte, 0: single elements
+};
+
+MXQ_DEV void mma_f8_pair(uint32_t d_tmem, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accum) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "l"(a), "l"(b), "r"(idesc), "r"(accum)
+      : "memory");
+}
+
+// Waits for this thread's tensor-memory loads; the registers pass through, so
+// that no use of them can move above the wait.
+#define MXQ_TMEM_WAIT32(r)                                                                       \
+  asm volatile("tcgen05.wait::ld.sync.aligned;"                                                  \
+               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]),         \
+                 "+r"(r[6]), "+r"(r[7]), "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]),       \
+                 "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15]), "+r"(r[16]), "+r"(r[17]),   \
+                 "+r"(r[18]), "+r"(r[19]), "+r"(r[20]), "+r"(r[21]), "+r"(r[22]), "+r"(r[23]),   \
+                 "+r"(r[24]), "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28]), "+r"(r[29]),   \
+                 "+r"(r[30]), "+r"(r[31])                                                        \
+               :                                                                                 \
+               : "memory")
+
+MXQ_DEV uint64_t pack2(uint32_t lo, uint32_t hi) {
+  uint64_t d;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "r"(lo), "r"(hi));
+  return d;
+}
+
+MXQ_DEV void unpack2(uint64_t v, float& lo, float& hi) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v));
+}
+
+MXQ_DEV uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+  return d;
+}
+
+MXQ_DEV uint64_t mul2(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+
+// acc += s * v over 32 columns (LINES: s * col[j] * v, col the columns' scales
+// in shared memory).
+template <bool LINES>
+MXQ_DEV void accumulate32(uint64_t* acc, const uint32_t (&v)[32], uint64_t s, const float* col) {
+#pragma unroll
+  for (int j = 0; j < 16; j += 2) {
+    uint64_t a = pack2(v[2 * j], v[2 * j + 1]), b = pack2(v[2 * j + 2], v[2 * j + 3]);
+    if constexpr (LINES) {
+      const ulonglong2 c = *reinterpret_cast<const ulonglong2*>(col + 2 * j);
+      a = mul2(a, c.x);
+      b = mul2(b, c.y);
+    }
+    acc[j] = fma2(a, s, acc[j]);
+    acc[j + 1] = fma2(b, s, acc[j + 1]);
+  }
+}
+
+// The first n of the 128 accumulated columns of one output row.
+MXQ_DEV void store_row(const PArgs& p, const uint64_t (&acc)[64], int64_t row, int64_t col0,
+                       int n) {
+  if (p.f.out_bf16) {
+    __nv_bfloat16* c = static_cast<__nv_bfloat16*>(p.f.C) + row * p.f.N + col0;
+    uint32_t w[64];
+#pragma unroll
+    for (int j = 0; j < 64; ++j) {
+      float lo, hi;
+      unpack2(acc[j], lo, hi);
+      const __nv_bfloat162 b = __floats2bfloat162_rn(lo, hi);
+      w[j] = *reinterpret_cast<const uint32_t*>(&b);
+    }
+    if (p.store == 2) {   // N % 16 == 0: whole groups of 16 columns
+#pragma unroll
+      for (int j = 0; j < 64; j += 8)
+        if (2 * j < n)
+          st_global_v8(c + 2 * j, w[j], w[j + 1], w[j + 2], w[j + 3], w[j + 4], w[j + 5], w[j + 6],
+                       w[j + 7]);
+    } else if (p.store == 1) {
+#pragma unroll
+      for (int j = 0; j < 64; j += 4)
+        if (2 * j < n)
+          *reinterpret_cast<uint4*>(c + 2 * j) = make_uint4(w[j], w[j + 1], w[j + 2], w[j + 3]);
+    } else {
+      uint16_t* h = reinterpret_cast<uint16_t*>(c);
+#pragma unroll
+      for (int j = 0; j < 64; ++j) {
+        if (2 * j < n) h[2 * j] = static_cast<uint16_t>(w[j]);
+        if (2 * j + 1 < n) h[2 * j + 1] = static_cast<uint16_t>(w[j] >> 16);
+      }
+    }
+  } else {
+    float* c = static_cast<float*>(p.f.C) + row * p.f.N + col0;
+    float f[128];
+#pragma unroll
+    for (int j = 0; j < 64; ++j) unpack2(acc[j], f[2 * j], f[2 * j + 1]);
+    if (p.store == 2) {   // N % 8 == 0
+#pragma unroll
+      for (int j = 0; j < 128; j += 8)
+        if (j < n)
+          st_global_v8(c + j, __float_as_uint(f[j]), __float_as_uint(f[j + 1]),
+                       __float_as_uint(f[j + 2]), __float_as_uint(f[j + 3]),
+                       __float_as_uint(f[j + 4]), __float_as_uint(f[j + 5]),
+                       __float_as_uint(f[j + 6]), __float_as_uint(f[j + 7]));
+    } else if (p.store == 1) {
+#pragma unroll
+      for (int j = 0; j < 128; j += 4)
+        if (j < n) *reinterpret_cast<float4*>(c + j) = make_float4(f[j], f[j + 1], f[j + 2], f[j + 3]);
+    } else {
+#pragma unroll
+      for (int j = 0; j < 128; ++j)
+        if (j < n) c[j] = f[j];
+    }
+  }
+}
+
+template <bool LINES>
+__global__ void __launch_bounds__(P_THREADS, 1)
+    fp8_gemm_pair(const __grid_constant__ CUtensorMap ta, const __grid_constant__ CUtensorMap tb,
+                  const PArgs p) {
+  using P = Pair<LINES>;
+  constexpr int S = P::STAGES;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                             ~static_cast<uintptr_t>(1023));
+  float* col_scales = reinterpret_cast<float*>(smem + S * P_STAGE);
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + S * P_STAGE + P::SCALES);
+  uint64_t* empty = full + S;
+  uint64_t* acc_full = empty + S;
+  uint64_t* acc_empty = acc_full + 2;   // leader: both CTAs have read the accumulator
+  uint64_t* drain = acc_empty + 2;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  // leader: the K blocks the peer's producer issued, once it has stopped
+  volatile uint32_t* peer_issued = reinterpret_cast<volatile uint32_t*>(abort_flag + 1);
+  constexpr uint32_t kNotYet = 0xFFFFFFFFu;
+
+  const FArgs& a = p.f;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t rank = cluster_rank();
+  const bool leader = rank == 0;
+  if (threadIdx.x == 0) {
+    prefetch_tmap(&ta);
+    prefetch_tmap(&tb);
+    for (int s = 0; s < S; ++s) {
+      mbar_init(smem_u32(&full[s]), 1);   // leader: one arrival, bytes of both CTAs
+      mbar_init(smem_u32(&empty[s]), 1);
+    }
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(smem_u32(&acc_full[b]), 1);
+      mbar_init(smem_u32(&acc_empty[b]), 16);   // 8 warps of each CTA
+    }
+    mbar_init(smem_u32(drain), 1);
+    *abort_flag = 0;
+    *peer_issued = kNotYet;
+    fence_mbar_init();
+  }
+  if (warp == 1) tmem_alloc_pair(smem_u32(tmem_slot), 512);
+  tc_fence_before();
+  cluster_sync();   // barriers of both CTAs exist before anyone signals the peer
+  tc_fence_after();
+  griddep_wait();
+  griddep_launch_dependents();
+  const int cid = blockIdx.x >> 1, ncl = gridDim.x >> 1;
+  const uint32_t tmem = *tmem_slot;
+  const int nk = a.nk, n_tiles = p.n_tiles;
+  const uint64_t tmo = a.timeout_ns;
+
+  if (warp < 4) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(P_CTRL_REGS));
+    if (warp == 0 && lane == 0) {
+      // ---------------- TMA producer (both CTAs) ----------------
+      const uint32_t full0 = map_to_rank(smem_u32(&full[0]), 0);
+      uint32_t s = 0, phase = 0, issued = 0;
+      bool ok = true;
+      for (int t = cid; t < n_tiles && ok; t += ncl) {
+        int mp, nt;
+        tile_coords(t, p, mp, nt);
+        const int ra = (2 * mp + static_cast<int>(rank)) * 128;
+        const int rb = (2 * nt + static_cast<int>(rank)) * 128;
+        for (int kb = 0; kb < nk; ++kb) {
+          if (!gwait(smem_u32(&empty[s]), phase ^ 1, tmo, abort_flag)) {
+            if (!*abort_flag) fabort(abort_flag, SITE_FP8_EMPTY);
+            ok = false;
+            break;
+          }
+          const uint32_t st = smem_u32(smem + s * P_STAGE), bar = full0 + s * 8;
+          if (leader) mbar_arrive_expect_tx(smem_u32(&full[s]), 2 * P_STAGE);
+          tma_load_2d_pair(st, &ta, bar, kb * 128, ra);
+          tma_load_2d_pair(st + P_OPERAND, &tb, bar, kb * 128, rb);
+          ++issued;
+          if (++s == S) { s = 0; phase ^= 1; }
+        }
+      }
+      if (!leader) {
+        st_cluster_u32(map_to_rank(smem_u32(const_cast<uint32_t*>(peer_issued)), 0), issued);
+      } else if (!ok) {
+        // Every copy of both CTAs signals the leader's stage barriers; before
+        // the final cluster barrier the leader waits (bounded) for the copies
+        // of the last stages either CTA issued, and stages only the peer
+        // issued get their expected bytes here.
+        const uint64_t t0 = global_ns();
+        while (*peer_issued == kNotYet && global_ns() - t0 <= 2 * tmo + 1000000) {
+        }
+        uint32_t last = issued;
+        if (*peer_issued != kNotYet && *peer_issued > last) last = *peer_issued;
+        for (uint32_t k = last > S ? last - S : 0; k < last; ++k) {
+          if (k >= issued) mbar_arrive_expect_tx(smem_u32(&full[k % S]), P_STAGE);
+          if (!mbar_wait(smem_u32(&full[k % S]), (k / S) & 1, tmo)) {
+            record_error(&g_err_fp8_gemm, MXQ_ERR_TIMEOUT, SITE_FP8_FULL);
+            break;
+          }
+        }
+      }
+    } else if (warp == 1 && lane == 0 && leader) {
+      // ---------------- pair-MMA issuer (leader CTA) ----------------
+      const uint32_t idesc = idesc_f8(a.idesc_fmt, 256, 256);
+      const uint64_t ad0 = smem_desc(smem_u32(smem), 0, 1024, 2);
+      const uint64_t bd0 = smem_desc(smem_u32(smem) + P_OPERAND, 0, 1024, 2);
+      uint32_t s = 0, phase = 0, it = 0;
+      bool ok = true;
+      for (int t = cid; t < n_tiles && ok; t += ncl) {
+        for (int kb = 0; kb < nk; ++kb, ++it) {
+          const uint32_t b = it & 1;
+          if (!gwait(smem_u32(&acc_empty[b]), ((it >> 1) & 1) ^ 1, tmo, abort_flag)) {
+            if (!*abort_flag) fabort(abort_flag, SITE_FP8_TMEM_EMPTY);
+            ok = false;
+            break;
+          }
+          if (!gwait(smem_u32(&full[s]), phase, tmo, abort_flag)) {
+            if (!*abort_flag) fabort(abort_flag, SITE_FP8_FULL);
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          const uint64_t ad = ad0 + s * (P_STAGE >> 4), bd = bd0 + s * (P_STAGE >> 4);
+          const uint32_t d = tmem + b * 256;
+          mma_f8_pair(d, ad, bd, idesc, 0u);
+          mma_f8_pair(d, ad + 2, bd + 2, idesc, 1u);
+          mma_f8_pair(d, ad + 4, bd + 4, idesc, 1u);
+          mma_f8_pair(d, ad + 6, bd + 6, idesc, 1u);
+          tc_commit_pair_mc(smem_u32(&empty[s]), 0x3);
+          tc_commit_pair_mc(smem_u32(&acc_full[b]), 0x3);
+          if (++s == S) { s = 0; phase ^= 1; }
+        }
+      }
+      tc_commit_pair_mc(smem_u32(drain), 0x1);   // every MMA is complete before teardown
+      if (!mbar_wait(smem_u32(drain), 0, tmo))
+        record_error(&g_err_fp8_gemm, MXQ_ERR_TIMEOUT, SITE_FP8_DRAIN);
+    }
+  } else {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(P_ACC_REGS));
+    // ---------------- accumulation (warps 4..11, both CTAs) ----------------
+    const int quad = warp & 3, colh = (warp - 4) >> 2;
+    const uint32_t empty_leader = map_to_rank(smem_u32(acc_empty), 0);
+    const uint32_t taddr0 = tmem + (static_cast<uint32_t>(quad * 32) << 16) + colh * 128;
+    float* my_cols = col_scales + (warp - 4) * 256;   // [2][128], this warp's
+    uint32_t it = 0;
+    bool ok = true;
+    for (int t = cid; t < n_tiles && ok; t += ncl) {
+      int mp, nt;
+      tile_coords(t, p, mp, nt);
+      const int64_t row = (int64_t(mp) * 2 + rank) * 128 + quad * 32 + lane;
+      const int64_t col0 = int64_t(nt) * 256 + colh * 128;
+      const bool row_in = row < a.M, cols_in = col0 < a.N;
+      const float* pa = a.sA + (row_in ? row : 0);
+      const float* pb = LINES ? a.sB + col0 + 4 * lane : a.sB + (col0 >> 7) * nk;
+      // line scales come in rows of a multiple of 4: a float4 is in or out
+      const bool four_in = LINES && col0 + 4 * lane < a.lines_b;
+      uint64_t acc[64];
+#pragma unroll
+      for (int j = 0; j < 64; ++j) acc[j] = 0ull;
+      float na = row_in ? pa[0] : 0.0f, nb = !LINES && cols_in ? pb[0] : 0.0f;
+      float4 nc = four_in ? *reinterpret_cast<const float4*>(pb) : make_float4(0, 0, 0, 0);
+      for (int kb = 0; kb < nk; ++kb, ++it) {
+        const uint32_t b = it & 1;
+        float s1 = na;
+        if constexpr (LINES) {
+          // two buffers: a lane that writes block kb + 2 has passed the
+          // __syncwarp of block kb + 1, past every lane's reads of block kb
+          *reinterpret_cast<float4*>(my_cols + b * 128 + 4 * lane) = nc;
+          __syncwarp();
+        } else {
+          s1 *= nb;
+        }
+        if (kb + 1 < nk) {   // the next block's scales, under this block's wait
+          if (row_in) na = pa[int64_t(kb + 1) * a.lines_a];
+          if (LINES) {
+            if (four_in) nc = *reinterpret_cast<const float4*>(pb + int64_t(kb + 1) * a.lines_b);
+          } else if (cols_in) {
+            nb = pb[kb + 1];
+          }
+        }
+        const uint32_t sbits = __float_as_uint(s1);
+        const uint64_t s2 = pack2(sbits, sbits);
+        if (!gwait(smem_u32(&acc_full[b]), (it >> 1) & 1, tmo, abort_flag)) {
+          if (lane == 0 && !*abort_flag) fabort(abort_flag, SITE_FP8_TMEM_FULL);
+          ok = false;
+        }
+        if (!__all_sync(~0u, ok)) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        const uint32_t taddr = taddr0 + b * 256;
+        const float* cs = my_cols + b * 128;
+        uint32_t v0[32], v1[32];
+        MXQ_TMEM_LD32(taddr, v0);
+        MXQ_TMEM_WAIT32(v0);
+        MXQ_TMEM_LD32(taddr + 32, v1);
+        accumulate32<LINES>(acc, v0, s2, cs);
+        MXQ_TMEM_WAIT32(v1);
+        MXQ_TMEM_LD32(taddr + 64, v0);
+        accumulate32<LINES>(acc + 16, v1, s2, cs + 32);
+        MXQ_TMEM_WAIT32(v0);
+        MXQ_TMEM_LD32(taddr + 96, v1);
+        accumulate32<LINES>(acc + 32, v0, s2, cs + 64);
+        MXQ_TMEM_WAIT32(v1);
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive_cluster_relaxed(empty_leader + b * 8);
+        accumulate32<LINES>(acc + 48, v1, s2, cs + 96);
+      }
+      if (!ok) break;
+      if (row_in && cols_in &&
+          MXQ_IN_BOUNDS(row < a.M && col0 < a.N && mp < p.n_mp && nt < p.n_nt, &g_err_fp8_gemm,
+                        SITE_B_FP8_GEMM)) {
+        const int n = static_cast<int>(a.N - col0 < 128 ? a.N - col0 : 128);
+        store_row(p, acc, row, col0, n);
+      }
+    }
+  }
+  tc_fence_before();
+  cluster_sync();   // no CTA leaves while its peer may still signal it
+  tc_fence_after();
+  if (warp == 1) tmem_dealloc_pair(tmem, 512);
+}
+
+// Clusters of the pair kernel that fit on the device at once, cached per
+// device; 0 if they cannot be had, or if the kernel was built with fewer
+// registers than its warpgroups share out among themselves.
+template <bool LINES>
+int pair_clusters(cudaLaunchConfig_t cfg) {
+  static std::mutex mu;
+  static int cached[64] = {0};
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 0;
+  std::lock_guard<std::mutex> lock(mu);
+  if (cached[dev] == 0) {
+    cudaFuncAttributes fa;
+    if (cudaFuncGetAttributes(&fa, fp8_gemm_pair<LINES>) != cudaSuccess ||
+        fa.numRegs < P_MIN_REGS) {
+      cudaGetLastError();
+      return 0;
+    }
+    cfg.numAttrs = 1;   // the cluster dimension
+    cfg.gridDim = dim3(static_cast<unsigned>(2 * sm_count()), 1, 1);
+    int n = 0;
+    if (cudaOccupancyMaxActiveClusters(&n, fp8_gemm_pair<LINES>, &cfg) != cudaSuccess || n <= 0) {
+      cudaGetLastError();
+      n = sm_count() / 2;
+    }
+    cached[dev] = n;
+  }
+  return cached[dev];
+}
+
 // The 2-D map of `lines` code lines of K elements, in boxes of 128 x `box`.
 bool code_map(CUtensorMap* map, const void* codes, int64_t lines, int64_t K, int box) {
   return tensor_map_2d(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, codes, static_cast<uint64_t>(K),
@@ -278,6 +686,50 @@ mxq_status launch_lanes(const void* A, const void* B, int64_t K, const FArgs& a,
     return MXQ_ERR_CUDA;
   fp8_gemm_lanes<T><<<dim3(static_cast<unsigned>(gx), static_cast<unsigned>(gy)), L_THREADS,
                       Lanes<T>::SMEM, static_cast<cudaStream_t>(stream)>>>(ta, tb, a);
+  return launch_status();
+}
+
+template <bool LINES>
+mxq_status launch_pair(const void* A, const void* B, int64_t K, const FArgs& f, uint32_t idesc_fmt,
+                       void* stream) {
+  CUtensorMap ta, tb;
+  if (!code_map(&ta, A, f.M, K, 128) || !code_map(&tb, B, f.N, K, 128)) return MXQ_ERR_CUDA;
+  const void* kernel = reinterpret_cast<const void*>(fp8_gemm_pair<LINES>);
+  if (!ensure_dynamic_smem(kernel, Pair<LINES>::SMEM)) return MXQ_ERR_CUDA;
+  PArgs p = {};
+  p.f = f;
+  p.f.idesc_fmt = idesc_fmt;
+  const int64_t n_mp = (f.M + 255) / 256, n_nt = (f.N + 255) / 256;
+  if (n_mp * n_nt >= (int64_t(1) << 31)) return MXQ_ERR_ARG;
+  p.n_mp = static_cast<int32_t>(n_mp);
+  p.n_nt = static_cast<int32_t>(n_nt);
+  p.n_tiles = p.n_mp * p.n_nt;
+  choose_raster(p.n_mp, p.n_nt, double(f.M) * K, double(f.N) * K, 256.0 * K, p.group, p.group_n);
+  const int e = f.out_bf16 ? 2 : 4;
+  const uintptr_t c = reinterpret_cast<uintptr_t>(f.C);
+  p.store = (f.N * e) % 32 == 0 && (c & 31u) == 0 ? 2 : (f.N * e) % 16 == 0 ? 1 : 0;
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = 2;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  // persistent grid: it may start while the previous kernel on the stream
+  // drains, and waits for it in the kernel
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
+  cfg.blockDim = dim3(P_THREADS, 1, 1);
+  cfg.dynamicSmemBytes = Pair<LINES>::SMEM;
+  cfg.stream = static_cast<cudaStream_t>(stream);
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  const int clusters = pair_clusters<LINES>(cfg);
+  if (clusters <= 0) return MXQ_ERR_CUDA;
+  cfg.gridDim = dim3(static_cast<unsigned>(2 * std::min(p.n_tiles, clusters)), 1, 1);
+  if (cudaLaunchKernelEx(&cfg, fp8_gemm_pair<LINES>, ta, tb, p) != cudaSuccess) {
+    cudaGetLastError();
+    return MXQ_ERR_CUDA;
+  }
   return launch_status();
 }
 
@@ -328,9 +780,16 @@ extern "C" mxq_status mxq_fp8_gemm(const void* A, const float* sA, int fmt_a, co
   a.nk = static_cast<int32_t>((K + F_BLOCK - 1) / F_BLOCK);
   a.tiles = b_scales == MXQ_FP8_TILES;
   a.out_bf16 = out_dtype == MXQ_OUT_BF16;
-  // the lines of B are the MMA's rows (its A operand)
-  a.idesc_fmt = (fmt_b == MXQ_E5M2 ? 1u << 7 : 0u) | (fmt_a == MXQ_E5M2 ? 1u << 10 : 0u);
   a.timeout_ns = wait_timeout_ns();
+  const uint32_t e5a = fmt_a == MXQ_E5M2, e5b = fmt_b == MXQ_E5M2;
+  const int64_t tiles = ((M + 255) / 256) * ((N + 255) / 256);
+  if (M > 128 && tiles >= 24) {
+    const uint32_t types = e5a << 7 | e5b << 10;
+    return a.tiles ? launch_pair<false>(A, B, K, a, types, stream)
+                   : launch_pair<true>(A, B, K, a, types, stream);
+  }
+  // the lines of B are the MMA's rows (its A operand)
+  a.idesc_fmt = e5b << 7 | e5a << 10;
   if (M <= 16) return launch_lanes<16>(A, B, K, a, stream);
   if (M <= 32) return launch_lanes<32>(A, B, K, a, stream);
   if (M <= 64) return launch_lanes<64>(A, B, K, a, stream);

@@ -241,24 +241,6 @@ MXQ_DEV void store_row_codes(const uint32_t (&v)[128], const GArgs& a, int64_t r
   }
 }
 
-// Work item t -> (mp, nt).  Tiles are visited in groups of `group` rows (or
-// columns, when group_n): inside a group the grouped index runs fastest, so
-// the clusters working at one time cover `group` panels of one operand and a
-// few of the other, and the grouped operand's panels stay in L2 while the
-// group sweeps the other dimension.
-MXQ_DEV void tile_coords(int t, const GArgs& a, int& mp, int& nt) {
-  const int n_g = a.group_n ? a.n_nt : a.n_mp;   // grouped dimension
-  const int n_o = a.group_n ? a.n_mp : a.n_nt;   // swept dimension
-  const int per_group = a.group * n_o;
-  const int g = t / per_group;
-  const int first = g * a.group;
-  const int size = min(a.group, n_g - first);
-  const int local = t - g * per_group;
-  const int gi = first + local % size, oi = local / size;
-  mp = a.group_n ? oi : gi;
-  nt = a.group_n ? gi : oi;
-}
-
 // Problem of work item t: p advances monotonically as a role walks its
 // items in increasing order.
 MXQ_DEV int problem_of(const GGroup& g, int t, int p) {
@@ -813,31 +795,8 @@ mxq_status gemm_prepare(const void* A, const uint8_t* sA, const void* B, const u
   // one work item = one 256x256 pair tile (one cluster)
   if (int64_t(a.n_mp) * a.n_nt >= (int64_t(1) << 31)) return MXQ_ERR_ARG;
   a.n_tiles = a.n_mp * a.n_nt;
-  {
-    // Raster: tiles run in groups of `group` panels of one operand (the
-    // grouped one) while the group sweeps all panels of the other.  The
-    // grouped panels are touched by every wave of the group and stay in L2
-    // (budget 64 MB); the swept operand streams from DRAM once per group.
-    // Modeled DRAM bytes: grouped_total + swept_total * n_groups; the
-    // orientation and group size with the fewest bytes win.
-    const double l2_budget = 64.0 * (1 << 20);
-    const double panel = double(2 * G_BM) * double(p.kbytes);
-    const int g_fit = static_cast<int>(std::max(1.0, std::floor(l2_budget / panel)));
-    const double a_bytes = double(p.mp) * p.kbytes, b_bytes = double(p.np) * p.kbytes;
-    double best = -1.0;
-    for (int orient = 0; orient < 2; ++orient) {
-      const int n_g = orient ? a.n_nt : a.n_mp;
-      const double grouped = orient ? b_bytes : a_bytes, swept = orient ? a_bytes : b_bytes;
-      for (int g = 1; g <= std::min(g_fit, n_g); ++g) {
-        const double bytes = grouped + swept * std::ceil(double(n_g) / g);
-        if (best < 0.0 || bytes < best - 1.0) {
-          best = bytes;
-          a.group_n = orient;
-          a.group = g;
-        }
-      }
-    }
-  }
+  choose_raster(a.n_mp, a.n_nt, double(p.mp) * p.kbytes, double(p.np) * p.kbytes,
+                double(2 * G_BM) * double(p.kbytes), a.group, a.group_n);
   a.nk = static_cast<int32_t>((p.kbytes + G_BKB - 1) / G_BKB);
   a.kc_per_row = static_cast<int32_t>(p.kbp / 4);
   a.sfa = tc ? sA : ws;

@@ -1,6 +1,8 @@
 // tcgen05, tensor-memory and cluster helpers shared by the tensor-core GEMMs.
 #pragma once
 
+#include <cmath>
+
 #include "mxq_common.cuh"
 
 namespace mxq {
@@ -132,6 +134,50 @@ MXQ_DEV void tma_load_2d_pair(uint32_t dst, const CUtensorMap* map, uint32_t bar
       " [%0], [%1, {%3, %4}], [%2];" ::"r"(dst),
       "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(x), "r"(y)
       : "memory");
+}
+
+// ---- tile order ---------------------------------------------------------------
+// Work item t -> (mp, nt).  Tiles are visited in groups of `group` rows (or
+// columns, when group_n): inside a group the grouped index runs fastest, so
+// the clusters working at one time cover `group` panels of one operand and a
+// few of the other, and the grouped operand's panels stay in L2 while the
+// group sweeps the other dimension.
+template <typename Args>
+MXQ_DEV void tile_coords(int t, const Args& a, int& mp, int& nt) {
+  const int n_g = a.group_n ? a.n_nt : a.n_mp;   // grouped dimension
+  const int n_o = a.group_n ? a.n_mp : a.n_nt;   // swept dimension
+  const int per_group = a.group * n_o;
+  const int g = t / per_group;
+  const int first = g * a.group;
+  const int size = min(a.group, n_g - first);
+  const int local = t - g * per_group;
+  const int gi = first + local % size, oi = local / size;
+  mp = a.group_n ? oi : gi;
+  nt = a.group_n ? gi : oi;
+}
+
+// Group size and orientation of tile_coords.  The grouped panels (`panel`
+// bytes each) are touched by every wave of the group and stay in L2 (budget
+// 64 MB); the swept operand streams from DRAM once per group.  Modeled DRAM
+// bytes: grouped_total + swept_total * n_groups; the orientation and group
+// size with the fewest bytes win.
+inline void choose_raster(int n_mp, int n_nt, double a_bytes, double b_bytes, double panel,
+                          int32_t& group, int32_t& group_n) {
+  const double l2_budget = 64.0 * (1 << 20);
+  const int g_fit = static_cast<int>(std::max(1.0, std::floor(l2_budget / panel)));
+  double best = -1.0;
+  for (int orient = 0; orient < 2; ++orient) {
+    const int n_g = orient ? n_nt : n_mp;
+    const double grouped = orient ? b_bytes : a_bytes, swept = orient ? a_bytes : b_bytes;
+    for (int g = 1; g <= std::min(g_fit, n_g); ++g) {
+      const double bytes = grouped + swept * std::ceil(double(n_g) / g);
+      if (best < 0.0 || bytes < best - 1.0) {
+        best = bytes;
+        group_n = orient;
+        group = g;
+      }
+    }
+  }
 }
 
 }  // namespace mxq

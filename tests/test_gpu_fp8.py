@@ -170,6 +170,23 @@ def test_product_of_mixed_formats(shape, fmts, kind):
     _check(ops, m, n, k, *fmts, kind, torch.float32)
 
 
+# enough 256x256 tiles for the CTA-pair kernel: ragged rows and columns, odd N,
+# rows of C that allow 32-byte, 16-byte and single-element stores, one K block
+PAIRS = [(1500, 1296, 200), (257, 6200, 100), (2000, 1001, 130), (900, 1672, 300),
+         (6200, 260, 520), (1792, 1028, 1111), (1600, 1024, 1)]
+
+
+@pytest.mark.parametrize("kind", ["tile", "line"])
+@pytest.mark.parametrize("shape", PAIRS, ids=lambda s: "x".join(map(str, s)))
+def test_product_of_many_tiles(shape, kind):
+    m, n, k = shape
+    ops = _operands(m, n, k, "e4m3", "e4m3", kind, m + n + k)
+    for out_dtype in (torch.float32, torch.bfloat16):
+        _check(ops, m, n, k, "e4m3", "e4m3", kind, out_dtype)
+    ops = _operands(m, n, k, "e5m2", "e4m3", kind, m)
+    _check(ops, m, n, k, "e5m2", "e4m3", kind, torch.float32)
+
+
 def test_bytes_past_k_are_not_read():
     m, n, k = 70, 150, 200
     ops = list(_operands(m, n, k, "e4m3", "e4m3", "tile", 2))
