@@ -21,13 +21,11 @@
 // block's accumulator is read back.
 //   warp 0      (both CTAs) TMA producer: own 128 lines of A and of B;
 //   warp 1      (both CTAs) tensor memory; the leader's lane issues the MMAs;
+//   warp 2      (both CTAs) scales of the coming K blocks into shared memory;
 //   warps 4-11  (both CTAs) accumulation: a thread owns 128 columns of one row
-//               of C in registers (64 packed fp32 pairs) for the whole K loop,
-//               adds each K block with one packed multiply-add per pair (line
-//               scales of B: one more multiply), and stores the row.
-// The accumulation warps take their registers from the control warps
-// (setmaxnreg), since 128 accumulators and 64 staged values do not fit the
-// even share.
+//               of C in registers for the whole K loop, adds each K block
+//               with one multiply-add per element (line scales of B: one more
+//               multiply), and stores the row.
 #include <string.h>
 
 #include <mutex>
@@ -54,6 +52,41 @@ struct FArgs {
   uint32_t idesc_fmt;          // element types of the instruction descriptor
   uint64_t timeout_ns;
 };
+
+// The warp's index, known to be the same in all of its lanes.
+MXQ_DEV int warp_index() { return __shfl_sync(~0u, static_cast<int>(threadIdx.x >> 5), 0); }
+
+// True in one lane of a converged warp.
+MXQ_DEV bool elect_one() {
+  uint32_t p;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "elect.sync _|p, 0xFFFFFFFF;\n\t"
+      "selp.b32 %0, 1, 0, p;\n\t}\n"
+      : "=r"(p));
+  return p != 0;
+}
+
+// A bounded wait that also gives up once another role of this CTA has aborted.
+// CTA scope: what the phase guards is tensor memory, or shared memory that
+// only the tensor cores and the copy engine touch, so no wait has to order
+// other CTAs' ordinary stores.  The timer is read once in 64 polls.  A poll
+// that succeeds at once costs 54 cycles in this form and 172 as a nested loop.
+MXQ_DEV bool fwait_more(uint32_t bar, uint32_t parity, uint64_t limit,
+                        volatile int* abort_flag) {
+  uint64_t t0 = 0;
+  for (uint32_t n = 1; !mbar_try_wait(bar, parity); ++n) {
+    if ((n & 63u) != 0) continue;
+    const uint64_t t = global_ns();
+    if (t0 == 0) t0 = t;
+    if (*abort_flag || t - t0 > limit) return false;
+  }
+  return true;
+}
+
+MXQ_DEV bool fwait(uint32_t bar, uint32_t parity, uint64_t limit, volatile int* abort_flag) {
+  return mbar_try_wait(bar, parity) || fwait_more(bar, parity, limit, abort_flag);
+}
 
 MXQ_DEV void fabort(volatile int* abort_flag, uint32_t site) {
   *abort_flag = 1;
@@ -100,6 +133,36 @@ MXQ_DEV void tmem_dealloc(uint32_t taddr, uint32_t cols) {
         "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), \
         "=r"(r[14]), "=r"(r[15])                                                                 \
       : "r"(taddr))
+
+// The wait of a role that runs on to its end whatever happens: when the limit
+// runs out it records the error, and every later wait of the CTA passes at
+// once.  Its warps then need no vote on a result before each warp-wide
+// instruction (a vote and its branch cost as much as the wait).
+MXQ_DEV void fwait_or_abort(uint32_t bar, uint32_t parity, uint64_t limit,
+                            volatile int* abort_flag, uint32_t site) {
+  if (mbar_try_wait(bar, parity)) return;
+  if (*abort_flag) return;
+  if (!fwait_more(bar, parity, limit, abort_flag) && !*abort_flag) fabort(abort_flag, site);
+}
+
+// Arrivals of one lane, predicated instead of branched around.
+MXQ_DEV void arrive_if(bool p, uint32_t bar) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %1, 0;\n\t"
+      "@p mbarrier.arrive.shared::cta.b64 _, [%0];\n\t}" ::"r"(bar),
+      "r"(static_cast<uint32_t>(p))
+      : "memory");
+}
+
+// On a barrier that may live in another CTA; relaxed, as the accumulator's
+// loads are complete and nothing else is ordered by it.
+MXQ_DEV void arrive_remote_if(bool p, uint32_t cluster_bar) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %1, 0;\n\t"
+      "@p mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];\n\t}" ::"r"(cluster_bar),
+      "r"(static_cast<uint32_t>(p))
+      : "memory");
+}
 
 // ---- 128 lines of B x T lines of A per CTA --------------------------------------
 constexpr int L_THREADS = 192;
@@ -164,7 +227,7 @@ __global__ void __launch_bounds__(L_THREADS)
       uint32_t s = 0, phase = 0, issued = 0;
       bool ok = true;
       for (int kb = 0; kb < nk; ++kb) {
-        if (!gwait(smem_u32(&empty[s]), phase ^ 1, tmo, abort_flag)) {
+        if (!fwait(smem_u32(&empty[s]), phase ^ 1, tmo, abort_flag)) {
           if (!*abort_flag) fabort(abort_flag, SITE_FP8_EMPTY);
           ok = false;
           break;
@@ -186,11 +249,11 @@ __global__ void __launch_bounds__(L_THREADS)
       uint32_t s = 0, phase = 0;
       for (int kb = 0; kb < nk; ++kb) {
         const int b = kb % NB;
-        if (!gwait(smem_u32(&acc_empty[b]), ((kb / NB) & 1) ^ 1, tmo, abort_flag)) {
+        if (!fwait(smem_u32(&acc_empty[b]), ((kb / NB) & 1) ^ 1, tmo, abort_flag)) {
           if (!*abort_flag) fabort(abort_flag, SITE_FP8_TMEM_EMPTY);
           break;
         }
-        if (!gwait(smem_u32(&full[s]), phase, tmo, abort_flag)) {
+        if (!fwait(smem_u32(&full[s]), phase, tmo, abort_flag)) {
           if (!*abort_flag) fabort(abort_flag, SITE_FP8_FULL);
           break;
         }
@@ -236,7 +299,7 @@ __global__ void __launch_bounds__(L_THREADS)
       next_a = scale_a(kb + 1);
       next_b = scale_b(kb + 1);
       asm volatile("bar.sync 1, 128;" ::: "memory");
-      if (ok && !gwait(smem_u32(&acc_full[b]), (kb / NB) & 1, tmo, abort_flag)) {
+      if (ok && !fwait(smem_u32(&acc_full[b]), (kb / NB) & 1, tmo, abort_flag)) {
         if (!*abort_flag) fabort(abort_flag, SITE_FP8_TMEM_FULL);
         ok = false;
       }
@@ -278,7 +341,7 @@ __global__ void __launch_bounds__(L_THREADS)
 
 // ---- 256 x 256 tiles on CTA pairs ------------------------------------------------
 constexpr int P_THREADS = 384;                   // one control and two accumulation warpgroups
-constexpr int P_CTRL_REGS = 56, P_ACC_REGS = 216;
+constexpr int P_CTRL_REGS = 88, P_ACC_REGS = 208;
 // the split below is drawn from the registers the block is launched with
 constexpr int P_MIN_REGS = (128 * P_CTRL_REGS + 256 * P_ACC_REGS + P_THREADS - 1) / P_THREADS;
 constexpr int P_OPERAND = 128 * 128;             // a stage's lines of A, or of B, of one CTA
@@ -286,10 +349,13 @@ constexpr int P_STAGE = 2 * P_OPERAND;
 
 template <bool LINES>
 struct Pair {
-  // line scales of B: a warp's 128 columns of a K block, two buffers
-  static constexpr int SCALES = LINES ? 8 * 2 * 128 * 4 : 0;
-  static constexpr int STAGES = LINES ? 6 : 7;
-  static constexpr int SMEM = STAGES * P_STAGE + SCALES + 256 + 1024;
+  // a K block's scales: [128] rows and [256] columns, or the two products of
+  // row and tile scale [2][128]
+  static constexpr int SLOT = LINES ? 384 : 256;          // floats
+  static constexpr int SLOTS = 16;                        // two groups of eight
+  static constexpr int SCALES = SLOTS * SLOT * 4;
+  static constexpr int STAGES = 6;
+  static constexpr int SMEM = STAGES * P_STAGE + SCALES + 512 + 1024;
   static_assert(SMEM <= 227 * 1024, "shared memory of one CTA");
 };
 
@@ -310,109 +376,95 @@ MXQ_DEV void mma_f8_pair(uint32_t d_tmem, uint64_t a, uint64_t b, uint32_t idesc
 
 // Waits for this thread's tensor-memory loads; the registers pass through, so
 // that no use of them can move above the wait.
-#define MXQ_TMEM_WAIT32(r)                                                                       \
+#define MXQ_TMEM_WAIT16(r)                                                                       \
   asm volatile("tcgen05.wait::ld.sync.aligned;"                                                  \
                : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]),         \
                  "+r"(r[6]), "+r"(r[7]), "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]),       \
-                 "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15]), "+r"(r[16]), "+r"(r[17]),   \
-                 "+r"(r[18]), "+r"(r[19]), "+r"(r[20]), "+r"(r[21]), "+r"(r[22]), "+r"(r[23]),   \
-                 "+r"(r[24]), "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28]), "+r"(r[29]),   \
-                 "+r"(r[30]), "+r"(r[31])                                                        \
+                 "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15])                              \
                :                                                                                 \
                : "memory")
 
-MXQ_DEV uint64_t pack2(uint32_t lo, uint32_t hi) {
-  uint64_t d;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "r"(lo), "r"(hi));
-  return d;
+MXQ_DEV float lds32(uint32_t addr) {
+  float v;
+  asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
+  return v;
 }
 
-MXQ_DEV void unpack2(uint64_t v, float& lo, float& hi) {
-  asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v));
+MXQ_DEV void lds128(uint32_t addr, float (&v)[4]) {
+  asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];"
+               : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3])
+               : "r"(addr)
+               : "memory");
 }
 
-MXQ_DEV uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
-  uint64_t d;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
-  return d;
-}
-
-MXQ_DEV uint64_t mul2(uint64_t a, uint64_t b) {
-  uint64_t d;
-  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
-  return d;
-}
-
-// acc += s * v over 32 columns (LINES: s * col[j] * v, col the columns' scales
+// acc += s * v over 16 columns (LINES: s * col[j] * v, col the columns' scales
 // in shared memory).
 template <bool LINES>
-MXQ_DEV void accumulate32(uint64_t* acc, const uint32_t (&v)[32], uint64_t s, const float* col) {
+MXQ_DEV void accumulate16(float* acc, const uint32_t (&v)[16], float s, uint32_t col) {
 #pragma unroll
-  for (int j = 0; j < 16; j += 2) {
-    uint64_t a = pack2(v[2 * j], v[2 * j + 1]), b = pack2(v[2 * j + 2], v[2 * j + 3]);
+  for (int j = 0; j < 16; j += 4) {
+    float c[4] = {1.0f, 1.0f, 1.0f, 1.0f};
     if constexpr (LINES) {
-      const ulonglong2 c = *reinterpret_cast<const ulonglong2*>(col + 2 * j);
-      a = mul2(a, c.x);
-      b = mul2(b, c.y);
+      lds128(col + 4 * j, c);
     }
-    acc[j] = fma2(a, s, acc[j]);
-    acc[j + 1] = fma2(b, s, acc[j + 1]);
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      float x = __uint_as_float(v[j + u]);
+      if constexpr (LINES) x = __fmul_rn(x, c[u]);
+      acc[j + u] = __fmaf_rn(x, s, acc[j + u]);
+    }
   }
 }
 
-// The first n of the 128 accumulated columns of one output row.
-MXQ_DEV void store_row(const PArgs& p, const uint64_t (&acc)[64], int64_t row, int64_t col0,
-                       int n) {
+// The first n of 64 accumulated columns of one output row.
+MXQ_DEV void store64(const PArgs& p, const float* acc, int64_t row, int64_t col0, int n) {
   if (p.f.out_bf16) {
     __nv_bfloat16* c = static_cast<__nv_bfloat16*>(p.f.C) + row * p.f.N + col0;
-    uint32_t w[64];
+    uint32_t w[32];
 #pragma unroll
-    for (int j = 0; j < 64; ++j) {
-      float lo, hi;
-      unpack2(acc[j], lo, hi);
-      const __nv_bfloat162 b = __floats2bfloat162_rn(lo, hi);
+    for (int j = 0; j < 32; ++j) {
+      const __nv_bfloat162 b = __floats2bfloat162_rn(acc[2 * j], acc[2 * j + 1]);
       w[j] = *reinterpret_cast<const uint32_t*>(&b);
     }
     if (p.store == 2) {   // N % 16 == 0: whole groups of 16 columns
 #pragma unroll
-      for (int j = 0; j < 64; j += 8)
+      for (int j = 0; j < 32; j += 8)
         if (2 * j < n)
           st_global_v8(c + 2 * j, w[j], w[j + 1], w[j + 2], w[j + 3], w[j + 4], w[j + 5], w[j + 6],
                        w[j + 7]);
     } else if (p.store == 1) {
 #pragma unroll
-      for (int j = 0; j < 64; j += 4)
+      for (int j = 0; j < 32; j += 4)
         if (2 * j < n)
           *reinterpret_cast<uint4*>(c + 2 * j) = make_uint4(w[j], w[j + 1], w[j + 2], w[j + 3]);
     } else {
       uint16_t* h = reinterpret_cast<uint16_t*>(c);
 #pragma unroll
-      for (int j = 0; j < 64; ++j) {
+      for (int j = 0; j < 32; ++j) {
         if (2 * j < n) h[2 * j] = static_cast<uint16_t>(w[j]);
         if (2 * j + 1 < n) h[2 * j + 1] = static_cast<uint16_t>(w[j] >> 16);
       }
     }
   } else {
     float* c = static_cast<float*>(p.f.C) + row * p.f.N + col0;
-    float f[128];
-#pragma unroll
-    for (int j = 0; j < 64; ++j) unpack2(acc[j], f[2 * j], f[2 * j + 1]);
     if (p.store == 2) {   // N % 8 == 0
 #pragma unroll
-      for (int j = 0; j < 128; j += 8)
+      for (int j = 0; j < 64; j += 8)
         if (j < n)
-          st_global_v8(c + j, __float_as_uint(f[j]), __float_as_uint(f[j + 1]),
-                       __float_as_uint(f[j + 2]), __float_as_uint(f[j + 3]),
-                       __float_as_uint(f[j + 4]), __float_as_uint(f[j + 5]),
-                       __float_as_uint(f[j + 6]), __float_as_uint(f[j + 7]));
+          st_global_v8(c + j, __float_as_uint(acc[j]), __float_as_uint(acc[j + 1]),
+                       __float_as_uint(acc[j + 2]), __float_as_uint(acc[j + 3]),
+                       __float_as_uint(acc[j + 4]), __float_as_uint(acc[j + 5]),
+                       __float_as_uint(acc[j + 6]), __float_as_uint(acc[j + 7]));
     } else if (p.store == 1) {
 #pragma unroll
-      for (int j = 0; j < 128; j += 4)
-        if (j < n) *reinterpret_cast<float4*>(c + j) = make_float4(f[j], f[j + 1], f[j + 2], f[j + 3]);
+      for (int j = 0; j < 64; j += 4)
+        if (j < n)
+          *reinterpret_cast<float4*>(c + j) =
+              make_float4(acc[j], acc[j + 1], acc[j + 2], acc[j + 3]);
     } else {
 #pragma unroll
-      for (int j = 0; j < 128; ++j)
-        if (j < n) c[j] = f[j];
+      for (int j = 0; j < 64; ++j)
+        if (j < n) c[j] = acc[j];
     }
   }
 }
@@ -426,12 +478,14 @@ __global__ void __launch_bounds__(P_THREADS, 1)
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~static_cast<uintptr_t>(1023));
-  float* col_scales = reinterpret_cast<float*>(smem + S * P_STAGE);
+  float* scales = reinterpret_cast<float*>(smem + S * P_STAGE);
   uint64_t* full = reinterpret_cast<uint64_t*>(smem + S * P_STAGE + P::SCALES);
   uint64_t* empty = full + S;
   uint64_t* acc_full = empty + S;
-  uint64_t* acc_empty = acc_full + 2;   // leader: both CTAs have read the accumulator
-  uint64_t* drain = acc_empty + 2;
+  uint64_t* sc_full = acc_full + 4;
+  uint64_t* acc_empty = sc_full + 2;    // leader: both CTAs have read the accumulator
+  uint64_t* sc_empty = acc_empty + 2;
+  uint64_t* drain = sc_empty + 2;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   // leader: the K blocks the peer's producer issued, once it has stopped
@@ -439,19 +493,21 @@ __global__ void __launch_bounds__(P_THREADS, 1)
   constexpr uint32_t kNotYet = 0xFFFFFFFFu;
 
   const FArgs& a = p.f;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = warp_index(), lane = threadIdx.x & 31;
   const uint32_t rank = cluster_rank();
   const bool leader = rank == 0;
   if (threadIdx.x == 0) {
     prefetch_tmap(&ta);
     prefetch_tmap(&tb);
     for (int s = 0; s < S; ++s) {
-      mbar_init(smem_u32(&full[s]), 1);   // leader: one arrival, bytes of both CTAs
+      mbar_init(smem_u32(&full[s]), 1);    // leader: one arrival, bytes of both CTAs
       mbar_init(smem_u32(&empty[s]), 1);
     }
-    for (int b = 0; b < 2; ++b) {
-      mbar_init(smem_u32(&acc_full[b]), 1);
-      mbar_init(smem_u32(&acc_empty[b]), 16);   // 8 warps of each CTA
+    for (int g = 0; g < 4; ++g) mbar_init(smem_u32(&acc_full[g]), 1);
+    for (int b = 0; b < 2; ++b) mbar_init(smem_u32(&acc_empty[b]), 16);   // 8 warps of each CTA
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(smem_u32(&sc_full[i]), 1);
+      mbar_init(smem_u32(&sc_empty[i]), 8);
     }
     mbar_init(smem_u32(drain), 1);
     *abort_flag = 0;
@@ -471,7 +527,12 @@ __global__ void __launch_bounds__(P_THREADS, 1)
 
   if (warp < 4) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(P_CTRL_REGS));
-    if (warp == 0 && lane == 0) {
+    // The control warps run as whole warps and elect a lane for each
+    // instruction, which keeps addresses and descriptors in uniform
+    // registers: the MMAs and commits of a K block then issue in 139 cycles
+    // instead of the 363 they take on one lane of a divergent warp.
+    const bool one = elect_one();
+    if (warp == 0) {
       // ---------------- TMA producer (both CTAs) ----------------
       const uint32_t full0 = map_to_rank(smem_u32(&full[0]), 0);
       uint32_t s = 0, phase = 0, issued = 0;
@@ -480,24 +541,27 @@ __global__ void __launch_bounds__(P_THREADS, 1)
         int mp, nt;
         tile_coords(t, p, mp, nt);
         const int ra = (2 * mp + static_cast<int>(rank)) * 128;
-        const int rb = (2 * nt + static_cast<int>(rank)) * 128;
+        const int rb = nt * 256 + static_cast<int>(rank) * 64;
         for (int kb = 0; kb < nk; ++kb) {
-          if (!gwait(smem_u32(&empty[s]), phase ^ 1, tmo, abort_flag)) {
-            if (!*abort_flag) fabort(abort_flag, SITE_FP8_EMPTY);
+          if (!fwait(smem_u32(&empty[s]), phase ^ 1, tmo, abort_flag)) {
+            if (one && !*abort_flag) fabort(abort_flag, SITE_FP8_EMPTY);
             ok = false;
             break;
           }
           const uint32_t st = smem_u32(smem + s * P_STAGE), bar = full0 + s * 8;
-          if (leader) mbar_arrive_expect_tx(smem_u32(&full[s]), 2 * P_STAGE);
-          tma_load_2d_pair(st, &ta, bar, kb * 128, ra);
-          tma_load_2d_pair(st + P_OPERAND, &tb, bar, kb * 128, rb);
+          if (one) {
+            if (leader) mbar_arrive_expect_tx(smem_u32(&full[s]), 2 * P_STAGE);
+            tma_load_2d_pair(st, &ta, bar, kb * 128, ra);
+            tma_load_2d_pair(st + P_OPERAND, &tb, bar, kb * 128, rb);
+            tma_load_2d_pair(st + P_OPERAND + P_OPERAND / 2, &tb, bar, kb * 128, rb + 128);
+          }
           ++issued;
           if (++s == S) { s = 0; phase ^= 1; }
         }
       }
-      if (!leader) {
+      if (one && !leader) {
         st_cluster_u32(map_to_rank(smem_u32(const_cast<uint32_t*>(peer_issued)), 0), issued);
-      } else if (!ok) {
+      } else if (one && !ok) {
         // Every copy of both CTAs signals the leader's stage barriers; before
         // the final cluster barrier the leader waits (bounded) for the copies
         // of the last stages either CTA issued, and stages only the peer
@@ -515,121 +579,196 @@ __global__ void __launch_bounds__(P_THREADS, 1)
           }
         }
       }
-    } else if (warp == 1 && lane == 0 && leader) {
-      // ---------------- pair-MMA issuer (leader CTA) ----------------
-      const uint32_t idesc = idesc_f8(a.idesc_fmt, 256, 256);
-      const uint64_t ad0 = smem_desc(smem_u32(smem), 0, 1024, 2);
-      const uint64_t bd0 = smem_desc(smem_u32(smem) + P_OPERAND, 0, 1024, 2);
-      uint32_t s = 0, phase = 0, it = 0;
-      bool ok = true;
-      for (int t = cid; t < n_tiles && ok; t += ncl) {
-        for (int kb = 0; kb < nk; ++kb, ++it) {
-          const uint32_t b = it & 1;
-          if (!gwait(smem_u32(&acc_empty[b]), ((it >> 1) & 1) ^ 1, tmo, abort_flag)) {
-            if (!*abort_flag) fabort(abort_flag, SITE_FP8_TMEM_EMPTY);
-            ok = false;
-            break;
+    } else if (warp == 1) {
+      if (leader) {
+        // ---------------- pair-MMA issuer (leader CTA) ----------------
+        const uint32_t idesc = idesc_f8(a.idesc_fmt, 256, 128);
+        const uint64_t ad0 = smem_desc(smem_u32(smem), 0, 1024, 2);
+        uint32_t s = 0, phase = 0, it = 0;
+        bool ok = true;
+        for (int t = cid; t < n_tiles && ok; t += ncl) {
+          for (int kb = 0; kb < nk; ++kb, ++it) {
+            const uint32_t b = it & 1, d = tmem + b * 256;
+            const uint64_t ad = ad0 + s * (P_STAGE >> 4), bd = ad + (P_OPERAND >> 4);
+            if (!fwait(smem_u32(&full[s]), phase, tmo, abort_flag) ||
+                !fwait(smem_u32(&acc_empty[b]), ((it >> 1) & 1) ^ 1, tmo, abort_flag)) {
+              if (one && !*abort_flag) fabort(abort_flag, SITE_FP8_TMEM_EMPTY);
+              ok = false;
+              break;
+            }
+            tc_fence_after();
+            if (one) {
+              mma_f8_pair(d, ad, bd, idesc, 0u);   // columns 0-127 of the tile
+              mma_f8_pair(d, ad + 2, bd + 2, idesc, 1u);
+              mma_f8_pair(d, ad + 4, bd + 4, idesc, 1u);
+              mma_f8_pair(d, ad + 6, bd + 6, idesc, 1u);
+              tc_commit_pair_mc(smem_u32(&acc_full[2 * b]), 0x3);
+              constexpr uint32_t kHalf = (P_OPERAND / 2) >> 4;   // columns 128-255
+              mma_f8_pair(d + 128, ad, bd + kHalf, idesc, 0u);
+              mma_f8_pair(d + 128, ad + 2, bd + kHalf + 2, idesc, 1u);
+              mma_f8_pair(d + 128, ad + 4, bd + kHalf + 4, idesc, 1u);
+              mma_f8_pair(d + 128, ad + 6, bd + kHalf + 6, idesc, 1u);
+              tc_commit_pair_mc(smem_u32(&acc_full[2 * b + 1]), 0x3);
+              tc_commit_pair_mc(smem_u32(&empty[s]), 0x3);
+            }
+            if (++s == S) { s = 0; phase ^= 1; }
           }
-          if (!gwait(smem_u32(&full[s]), phase, tmo, abort_flag)) {
-            if (!*abort_flag) fabort(abort_flag, SITE_FP8_FULL);
-            ok = false;
-            break;
-          }
-          tc_fence_after();
-          const uint64_t ad = ad0 + s * (P_STAGE >> 4), bd = bd0 + s * (P_STAGE >> 4);
-          const uint32_t d = tmem + b * 256;
-          mma_f8_pair(d, ad, bd, idesc, 0u);
-          mma_f8_pair(d, ad + 2, bd + 2, idesc, 1u);
-          mma_f8_pair(d, ad + 4, bd + 4, idesc, 1u);
-          mma_f8_pair(d, ad + 6, bd + 6, idesc, 1u);
-          tc_commit_pair_mc(smem_u32(&empty[s]), 0x3);
-          tc_commit_pair_mc(smem_u32(&acc_full[b]), 0x3);
-          if (++s == S) { s = 0; phase ^= 1; }
+        }
+        if (one) {   // every MMA is complete before teardown
+          tc_commit_pair_mc(smem_u32(drain), 0x1);
+          if (!mbar_wait(smem_u32(drain), 0, tmo))
+            record_error(&g_err_fp8_gemm, MXQ_ERR_TIMEOUT, SITE_FP8_DRAIN);
         }
       }
-      tc_commit_pair_mc(smem_u32(drain), 0x1);   // every MMA is complete before teardown
-      if (!mbar_wait(smem_u32(drain), 0, tmo))
-        record_error(&g_err_fp8_gemm, MXQ_ERR_TIMEOUT, SITE_FP8_DRAIN);
+    } else if (warp == 2) {
+      // ---------------- scales (both CTAs) ----------------
+      // Eight K blocks share a group of slots and its two barriers; BATCH are
+      // loaded at a time (what the registers hold), so that a block's share of
+      // the load latency is below the time of its MMAs.  Groups start anew
+      // with each tile.
+      constexpr int BATCH = LINES ? 2 : 4;
+      uint32_t grp = 0;
+      for (int t = cid; t < n_tiles; t += ncl) {
+        int mp, nt;
+        tile_coords(t, p, mp, nt);
+        const int64_t ra = (int64_t(mp) * 2 + rank) * 128 + 4 * lane, cb = int64_t(nt) * 256;
+        // line scales come in rows of a multiple of 4: a float4 is in or out
+        const bool a_in = ra < a.lines_a;
+        for (int kb8 = 0; kb8 < nk; kb8 += 8, ++grp) {
+          const uint32_t i = grp & 1;
+          fwait_or_abort(smem_u32(&sc_empty[i]), ((grp >> 1) & 1) ^ 1, tmo, abort_flag,
+                         SITE_FP8_SCALES);
+#pragma unroll 1
+          for (int kb0 = kb8; kb0 < min(kb8 + 8, nk); kb0 += BATCH) {
+            float4 va[BATCH], vb[LINES ? BATCH : 1], vc[LINES ? BATCH : 1];
+            float s0[BATCH], s1[BATCH];
+#pragma unroll
+            for (int u = 0; u < BATCH; ++u) {
+              const int64_t kb = kb0 + u;
+              const float4 zero = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+              va[u] = zero;
+              if (kb < nk && a_in)
+                va[u] = *reinterpret_cast<const float4*>(a.sA + kb * a.lines_a + ra);
+              if constexpr (LINES) {
+                const float* sb = a.sB + kb * a.lines_b + cb + 4 * lane;
+                vb[u] = vc[u] = zero;
+                if (kb < nk && cb + 4 * lane < a.lines_b)
+                  vb[u] = *reinterpret_cast<const float4*>(sb);
+                if (kb < nk && cb + 128 + 4 * lane < a.lines_b)
+                  vc[u] = *reinterpret_cast<const float4*>(sb + 128);
+              } else {
+                const float* sb = a.sB + (cb >> 7) * nk + kb;
+                s0[u] = s1[u] = 0.0f;
+                if (kb < nk && cb < a.N) s0[u] = sb[0];
+                if (kb < nk && cb + 128 < a.N) s1[u] = sb[nk];
+              }
+            }
+#pragma unroll
+            for (int u = 0; u < BATCH; ++u) {
+              float* slot = scales + (i * 8 + (kb0 & 7) + u) * P::SLOT + 4 * lane;
+              const float4 x = va[u];
+              if constexpr (LINES) {
+                *reinterpret_cast<float4*>(slot) = x;
+                *reinterpret_cast<float4*>(slot + 128) = vb[u];
+                *reinterpret_cast<float4*>(slot + 256) = vc[u];
+              } else {
+                const float p0 = s0[u], p1 = s1[u];
+                *reinterpret_cast<float4*>(slot) =
+                    make_float4(x.x * p0, x.y * p0, x.z * p0, x.w * p0);
+                *reinterpret_cast<float4*>(slot + 128) =
+                    make_float4(x.x * p1, x.y * p1, x.z * p1, x.w * p1);
+              }
+            }
+          }
+          __syncwarp();
+          if (lane == 0) mbar_arrive(smem_u32(&sc_full[i]));
+        }
+      }
     }
   } else {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(P_ACC_REGS));
     // ---------------- accumulation (warps 4..11, both CTAs) ----------------
-    const int quad = warp & 3, colh = (warp - 4) >> 2;
+    // Warps 4-7 own the columns of half 0, warps 8-11 those of half 1.  The
+    // loop keeps few values beside its 160 accumulators and staged columns:
+    // every shared address is an offset from one register.
+    const int quad = warp & 3, h = (warp - 4) >> 2;
+    const uint32_t bars = smem_u32(acc_full), sc = smem_u32(scales);
     const uint32_t empty_leader = map_to_rank(smem_u32(acc_empty), 0);
-    const uint32_t taddr0 = tmem + (static_cast<uint32_t>(quad * 32) << 16) + colh * 128;
-    float* my_cols = col_scales + (warp - 4) * 256;   // [2][128], this warp's
-    uint32_t it = 0;
-    bool ok = true;
-    for (int t = cid; t < n_tiles && ok; t += ncl) {
+    const uint32_t taddr0 = tmem + (static_cast<uint32_t>(quad * 32) << 16) + h * 128;
+    const uint32_t row_at = 4 * ((LINES ? 0 : h * 128) + quad * 32 + lane);
+    const uint32_t col_at = 4 * (128 + h * 128);
+    uint32_t it = 0, grp = 0;
+    for (int t = cid; t < n_tiles; t += ncl) {
+      float acc[128];
+#pragma unroll
+      for (int j = 0; j < 128; ++j) acc[j] = 0.0f;
+      // Of block 0 the scale group, the scale and the MMAs are waited for here,
+      // of every other block under the last additions of the block before.
+      uint32_t at = sc + (grp & 1) * (32 * P::SLOT);
+      fwait_or_abort(bars + 32 + 8 * (grp & 1), (grp >> 1) & 1, a.timeout_ns, abort_flag,
+                     SITE_FP8_SCALES);   // sc_full follows acc_full[4]
+      float s1 = lds32(at + row_at);
+      fwait_or_abort(bars + 8 * h + 16 * (it & 1), (it >> 1) & 1, a.timeout_ns, abort_flag,
+                     SITE_FP8_TMEM_FULL);
+#pragma unroll 1
+      for (int kb = 0; kb < nk; ++kb) {
+        __syncwarp();
+        tc_fence_after();
+        const uint32_t b = it & 1, taddr = taddr0 + b * 256;
+        const uint32_t cols = at + col_at;
+        // 16 columns in flight while 16 are added
+        uint32_t v[2][16];
+        MXQ_TMEM_LD16(taddr, v[0]);
+#pragma unroll
+        for (int c = 0; c < 7; ++c) {
+          MXQ_TMEM_WAIT16(v[c & 1]);
+          MXQ_TMEM_LD16(taddr + 16 * c + 16, v[(c + 1) & 1]);
+          accumulate16<LINES>(acc + 16 * c, v[c & 1], s1, cols + 64 * c);
+        }
+        MXQ_TMEM_WAIT16(v[1]);
+        // everything is read: hand the accumulator back
+        tc_fence_before();
+        __syncwarp();
+        arrive_remote_if(lane == 0, empty_leader + b * 8);
+        ++it;
+        const uint32_t full_next = bars + 8 * h + 16 * (it & 1), full_phase = (it >> 1) & 1;
+        const bool more = kb + 1 < nk;
+        float s_next = 0.0f;
+        bool ready = true;
+        if (more && ((kb + 1) & 7) != 0) {
+          at += 4 * P::SLOT;
+          s_next = lds32(at + row_at);
+          ready = mbar_try_wait(full_next, full_phase);
+        }
+        accumulate16<LINES>(acc + 112, v[1], s1, cols + 448);
+        if (!more || ((kb + 1) & 7) == 0) {   // the group's last block
+          __syncwarp();
+          arrive_if(lane == 0, bars + 64 + 8 * (grp & 1));   // sc_empty
+          ++grp;
+          if (more) {
+            at = sc + (grp & 1) * (32 * P::SLOT);
+            fwait_or_abort(bars + 32 + 8 * (grp & 1), (grp >> 1) & 1, a.timeout_ns, abort_flag,
+                           SITE_FP8_SCALES);
+            s_next = lds32(at + row_at);
+            ready = false;
+          }
+        }
+        if (!ready)
+          fwait_or_abort(full_next, full_phase, a.timeout_ns, abort_flag, SITE_FP8_TMEM_FULL);
+        s1 = s_next;
+      }
+      if (__any_sync(~0u, *abort_flag)) break;
       int mp, nt;
       tile_coords(t, p, mp, nt);
       const int64_t row = (int64_t(mp) * 2 + rank) * 128 + quad * 32 + lane;
-      const int64_t col0 = int64_t(nt) * 256 + colh * 128;
-      const bool row_in = row < a.M, cols_in = col0 < a.N;
-      const float* pa = a.sA + (row_in ? row : 0);
-      const float* pb = LINES ? a.sB + col0 + 4 * lane : a.sB + (col0 >> 7) * nk;
-      // line scales come in rows of a multiple of 4: a float4 is in or out
-      const bool four_in = LINES && col0 + 4 * lane < a.lines_b;
-      uint64_t acc[64];
+      const int64_t col0 = int64_t(nt) * 256 + h * 128;
+      if (row < a.M && col0 < a.N &&
+          MXQ_IN_BOUNDS(mp < p.n_mp && nt < p.n_nt, &g_err_fp8_gemm, SITE_B_FP8_GEMM)) {
 #pragma unroll
-      for (int j = 0; j < 64; ++j) acc[j] = 0ull;
-      float na = row_in ? pa[0] : 0.0f, nb = !LINES && cols_in ? pb[0] : 0.0f;
-      float4 nc = four_in ? *reinterpret_cast<const float4*>(pb) : make_float4(0, 0, 0, 0);
-      for (int kb = 0; kb < nk; ++kb, ++it) {
-        const uint32_t b = it & 1;
-        float s1 = na;
-        if constexpr (LINES) {
-          // two buffers: a lane that writes block kb + 2 has passed the
-          // __syncwarp of block kb + 1, past every lane's reads of block kb
-          *reinterpret_cast<float4*>(my_cols + b * 128 + 4 * lane) = nc;
-          __syncwarp();
-        } else {
-          s1 *= nb;
+        for (int u = 0; u < 2; ++u) {
+          const int64_t left = a.N - col0 - u * 64;
+          if (left > 0) store64(p, acc + 64 * u, row, col0 + u * 64, left < 64 ? int(left) : 64);
         }
-        if (kb + 1 < nk) {   // the next block's scales, under this block's wait
-          if (row_in) na = pa[int64_t(kb + 1) * a.lines_a];
-          if (LINES) {
-            if (four_in) nc = *reinterpret_cast<const float4*>(pb + int64_t(kb + 1) * a.lines_b);
-          } else if (cols_in) {
-            nb = pb[kb + 1];
-          }
-        }
-        const uint32_t sbits = __float_as_uint(s1);
-        const uint64_t s2 = pack2(sbits, sbits);
-        if (!gwait(smem_u32(&acc_full[b]), (it >> 1) & 1, tmo, abort_flag)) {
-          if (lane == 0 && !*abort_flag) fabort(abort_flag, SITE_FP8_TMEM_FULL);
-          ok = false;
-        }
-        if (!__all_sync(~0u, ok)) {
-          ok = false;
-          break;
-        }
-        tc_fence_after();
-        const uint32_t taddr = taddr0 + b * 256;
-        const float* cs = my_cols + b * 128;
-        uint32_t v0[32], v1[32];
-        MXQ_TMEM_LD32(taddr, v0);
-        MXQ_TMEM_WAIT32(v0);
-        MXQ_TMEM_LD32(taddr + 32, v1);
-        accumulate32<LINES>(acc, v0, s2, cs);
-        MXQ_TMEM_WAIT32(v1);
-        MXQ_TMEM_LD32(taddr + 64, v0);
-        accumulate32<LINES>(acc + 16, v1, s2, cs + 32);
-        MXQ_TMEM_WAIT32(v0);
-        MXQ_TMEM_LD32(taddr + 96, v1);
-        accumulate32<LINES>(acc + 32, v0, s2, cs + 64);
-        MXQ_TMEM_WAIT32(v1);
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive_cluster_relaxed(empty_leader + b * 8);
-        accumulate32<LINES>(acc + 48, v1, s2, cs + 96);
-      }
-      if (!ok) break;
-      if (row_in && cols_in &&
-          MXQ_IN_BOUNDS(row < a.M && col0 < a.N && mp < p.n_mp && nt < p.n_nt, &g_err_fp8_gemm,
-                        SITE_B_FP8_GEMM)) {
-        const int n = static_cast<int>(a.N - col0 < 128 ? a.N - col0 : 128);
-        store_row(p, acc, row, col0, n);
       }
     }
   }
@@ -693,7 +832,7 @@ template <bool LINES>
 mxq_status launch_pair(const void* A, const void* B, int64_t K, const FArgs& f, uint32_t idesc_fmt,
                        void* stream) {
   CUtensorMap ta, tb;
-  if (!code_map(&ta, A, f.M, K, 128) || !code_map(&tb, B, f.N, K, 128)) return MXQ_ERR_CUDA;
+  if (!code_map(&ta, A, f.M, K, 128) || !code_map(&tb, B, f.N, K, 64)) return MXQ_ERR_CUDA;
   const void* kernel = reinterpret_cast<const void*>(fp8_gemm_pair<LINES>);
   if (!ensure_dynamic_smem(kernel, Pair<LINES>::SMEM)) return MXQ_ERR_CUDA;
   PArgs p = {};
