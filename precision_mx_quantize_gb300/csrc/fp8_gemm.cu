@@ -363,7 +363,8 @@ struct PArgs {
   FArgs f;
   int32_t n_mp, n_nt, n_tiles;   // 256-row and 256-column tiles
   int32_t group, group_n;        // tile order (tile_coords)
-  int32_t store;                 // 2: 32-byte stores of C rows, 1: 16-byte, 0: single elements
+  int32_t store;                 // tiles: 2, 32-byte stores of C rows, 1, 16-byte, 0, elements;
+                                 // lines: 1, two columns at a time (N even), 0, elements
 };
 
 MXQ_DEV void mma_f8_pair(uint32_t d_tmem, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accum) {
@@ -390,28 +391,74 @@ MXQ_DEV float lds32(uint32_t addr) {
   return v;
 }
 
-MXQ_DEV void lds128(uint32_t addr, float (&v)[4]) {
-  asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];"
-               : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3])
-               : "r"(addr)
-               : "memory");
+// Sixteen accumulator words of this thread: tiles, 16 columns of its row;
+// lines, the 16 x 256-bit fragments of 32 columns -- rows lane / 4 and 8 more,
+// columns 2 (lane % 4) and the next of each group of 8.
+template <bool LINES>
+MXQ_DEV void load16(uint32_t taddr, uint32_t (&v)[16]) {
+  if constexpr (LINES)
+    asm volatile(
+        "tcgen05.ld.sync.aligned.16x256b.x4.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, "
+        "%11, %12, %13, %14, %15}, [%16];"
+        : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]),
+          "=r"(v[7]), "=r"(v[8]), "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]),
+          "=r"(v[14]), "=r"(v[15])
+        : "r"(taddr));
+  else
+    MXQ_TMEM_LD16(taddr, v);
 }
 
-// acc += s * v over 16 columns (LINES: s * col[j] * v, col the columns' scales
-// in shared memory).
+// Tensor-memory address offset of step c of a half tile.
 template <bool LINES>
-MXQ_DEV void accumulate16(float* acc, const uint32_t (&v)[16], float s, uint32_t col) {
+MXQ_DEV uint32_t step16(int c) {
+  return LINES ? (c >> 1) * 32 + (static_cast<uint32_t>((c & 1) * 16) << 16) : 16 * c;
+}
+
+// acc += s * v for a row of tile scales.
+MXQ_DEV void add16(float* acc, const uint32_t (&v)[16], float s) {
 #pragma unroll
-  for (int j = 0; j < 16; j += 4) {
-    float c[4] = {1.0f, 1.0f, 1.0f, 1.0f};
-    if constexpr (LINES) {
-      lds128(col + 4 * j, c);
+  for (int j = 0; j < 16; ++j) acc[j] = __fmaf_rn(__uint_as_float(v[j]), s, acc[j]);
+}
+
+// acc += row * col * v for a fragment: two rows, the columns' scales in col.
+MXQ_DEV void add16(float* acc, const uint32_t (&v)[16], float lo, float hi, const float (&col)[8]) {
+#pragma unroll
+  for (int j = 0; j < 16; ++j) {
+    const float x = __fmul_rn(__uint_as_float(v[j]), col[2 * (j >> 2) + (j & 1)]);
+    acc[j] = __fmaf_rn(x, (j & 2) ? hi : lo, acc[j]);
+  }
+}
+
+// This thread's scales of 32 columns: 2 (lane % 4) and the next of each group
+// of 8.
+MXQ_DEV void load_cols(uint32_t addr, float (&col)[8]) {
+#pragma unroll
+  for (int q = 0; q < 4; ++q)
+    asm volatile("ld.shared.v2.f32 {%0, %1}, [%2];"
+                 : "=f"(col[2 * q]), "=f"(col[2 * q + 1])
+                 : "r"(addr + 32 * q)
+                 : "memory");
+}
+
+// Stores two neighbouring columns of a row, as far as they lie in C.
+MXQ_DEV void store2(const PArgs& p, int64_t row, int64_t col, float x, float y) {
+  if (row >= p.f.M || col >= p.f.N) return;
+  const int64_t at = row * p.f.N + col;
+  if (p.f.out_bf16) {
+    __nv_bfloat16* c = static_cast<__nv_bfloat16*>(p.f.C) + at;
+    if (p.store) {   // N is even: both columns, aligned
+      *reinterpret_cast<__nv_bfloat162*>(c) = __floats2bfloat162_rn(x, y);
+    } else {
+      c[0] = __float2bfloat16_rn(x);
+      if (col + 1 < p.f.N) c[1] = __float2bfloat16_rn(y);
     }
-#pragma unroll
-    for (int u = 0; u < 4; ++u) {
-      float x = __uint_as_float(v[j + u]);
-      if constexpr (LINES) x = __fmul_rn(x, c[u]);
-      acc[j + u] = __fmaf_rn(x, s, acc[j + u]);
+  } else {
+    float* c = static_cast<float*>(p.f.C) + at;
+    if (p.store) {
+      *reinterpret_cast<float2*>(c) = make_float2(x, y);
+    } else {
+      c[0] = x;
+      if (col + 1 < p.f.N) c[1] = y;
     }
   }
 }
@@ -695,73 +742,68 @@ __global__ void __launch_bounds__(P_THREADS, 1)
     const uint32_t bars = smem_u32(acc_full), sc = smem_u32(scales);
     const uint32_t empty_leader = map_to_rank(smem_u32(acc_empty), 0);
     const uint32_t taddr0 = tmem + (static_cast<uint32_t>(quad * 32) << 16) + h * 128;
-    const uint32_t row_at = 4 * ((LINES ? 0 : h * 128) + quad * 32 + lane);
-    const uint32_t col_at = 4 * (128 + h * 128);
+    const uint32_t row_at = 4 * ((LINES ? 0 : h * 128) + quad * 32 + (LINES ? lane >> 2 : lane));
+    const uint32_t col_at = 4 * (128 + h * 128 + 2 * (lane & 3));
     uint32_t it = 0, grp = 0;
     for (int t = cid; t < n_tiles; t += ncl) {
       float acc[128];
 #pragma unroll
       for (int j = 0; j < 128; ++j) acc[j] = 0.0f;
-      // Of block 0 the scale group, the scale and the MMAs are waited for here,
-      // of every other block under the last additions of the block before.
-      uint32_t at = sc + (grp & 1) * (32 * P::SLOT);
-      fwait_or_abort(bars + 32 + 8 * (grp & 1), (grp >> 1) & 1, a.timeout_ns, abort_flag,
-                     SITE_FP8_SCALES);   // sc_full follows acc_full[4]
-      float s1 = lds32(at + row_at);
-      fwait_or_abort(bars + 8 * h + 16 * (it & 1), (it >> 1) & 1, a.timeout_ns, abort_flag,
-                     SITE_FP8_TMEM_FULL);
 #pragma unroll 1
-      for (int kb = 0; kb < nk; ++kb) {
+      for (int kb = 0; kb < nk; ++kb, ++it) {
+        if ((kb & 7) == 0)   // sc_full follows acc_full[4]
+          fwait_or_abort(bars + 32 + 8 * (grp & 1), (grp >> 1) & 1, a.timeout_ns, abort_flag,
+                         SITE_FP8_SCALES);
+        const uint32_t at = sc + ((grp & 1) * 8 + (kb & 7)) * (4 * P::SLOT), b = it & 1;
+        float s1[LINES ? 4 : 1];   // lines: rows lane / 4 + 8 i of the warp's 32
+#pragma unroll
+        for (int i = 0; i < (LINES ? 4 : 1); ++i) s1[i] = lds32(at + row_at + 32 * i);
+        fwait_or_abort(bars + 8 * h + 16 * b, (it >> 1) & 1, a.timeout_ns, abort_flag,
+                       SITE_FP8_TMEM_FULL);
         __syncwarp();
         tc_fence_after();
-        const uint32_t b = it & 1, taddr = taddr0 + b * 256;
-        const uint32_t cols = at + col_at;
-        // 16 columns in flight while 16 are added
+        const uint32_t taddr = taddr0 + b * 256;
+        // 16 words in flight while 16 are added
         uint32_t v[2][16];
-        MXQ_TMEM_LD16(taddr, v[0]);
+        float col[8];
+        load16<LINES>(taddr, v[0]);
 #pragma unroll
-        for (int c = 0; c < 7; ++c) {
+        for (int c = 0; c < 8; ++c) {
           MXQ_TMEM_WAIT16(v[c & 1]);
-          MXQ_TMEM_LD16(taddr + 16 * c + 16, v[(c + 1) & 1]);
-          accumulate16<LINES>(acc + 16 * c, v[c & 1], s1, cols + 64 * c);
+          if (c < 7) {
+            load16<LINES>(taddr + step16<LINES>(c + 1), v[(c + 1) & 1]);
+          } else {   // everything is read: hand the accumulator back first
+            tc_fence_before();
+            __syncwarp();
+            arrive_remote_if(lane == 0, empty_leader + b * 8);
+          }
+          if constexpr (LINES) {
+            if ((c & 1) == 0) load_cols(at + col_at + 64 * c, col);
+            add16(acc + 16 * c, v[c & 1], s1[2 * (c & 1)], s1[2 * (c & 1) + 1], col);
+          } else {
+            add16(acc + 16 * c, v[c & 1], s1[0]);
+          }
         }
-        MXQ_TMEM_WAIT16(v[1]);
-        // everything is read: hand the accumulator back
-        tc_fence_before();
-        __syncwarp();
-        arrive_remote_if(lane == 0, empty_leader + b * 8);
-        ++it;
-        const uint32_t full_next = bars + 8 * h + 16 * (it & 1), full_phase = (it >> 1) & 1;
-        const bool more = kb + 1 < nk;
-        float s_next = 0.0f;
-        bool ready = true;
-        if (more && ((kb + 1) & 7) != 0) {
-          at += 4 * P::SLOT;
-          s_next = lds32(at + row_at);
-          ready = mbar_try_wait(full_next, full_phase);
-        }
-        accumulate16<LINES>(acc + 112, v[1], s1, cols + 448);
-        if (!more || ((kb + 1) & 7) == 0) {   // the group's last block
+        if ((kb & 7) == 7 || kb + 1 == nk) {   // the group's last block
           __syncwarp();
           arrive_if(lane == 0, bars + 64 + 8 * (grp & 1));   // sc_empty
           ++grp;
-          if (more) {
-            at = sc + (grp & 1) * (32 * P::SLOT);
-            fwait_or_abort(bars + 32 + 8 * (grp & 1), (grp >> 1) & 1, a.timeout_ns, abort_flag,
-                           SITE_FP8_SCALES);
-            s_next = lds32(at + row_at);
-            ready = false;
-          }
         }
-        if (!ready)
-          fwait_or_abort(full_next, full_phase, a.timeout_ns, abort_flag, SITE_FP8_TMEM_FULL);
-        s1 = s_next;
       }
       if (__any_sync(~0u, *abort_flag)) break;
       int mp, nt;
       tile_coords(t, p, mp, nt);
-      const int64_t row = (int64_t(mp) * 2 + rank) * 128 + quad * 32 + lane;
+      const int64_t row0 = (int64_t(mp) * 2 + rank) * 128 + quad * 32;
       const int64_t col0 = int64_t(nt) * 256 + h * 128;
+      if constexpr (LINES) {
+        if (!MXQ_IN_BOUNDS(mp < p.n_mp && nt < p.n_nt, &g_err_fp8_gemm, SITE_B_FP8_GEMM)) continue;
+#pragma unroll
+        for (int j = 0; j < 128; j += 2)
+          store2(p, row0 + ((j >> 4) & 1) * 16 + ((j >> 1) & 1) * 8 + (lane >> 2),
+                 col0 + (j >> 5) * 32 + ((j >> 2) & 3) * 8 + 2 * (lane & 3), acc[j], acc[j + 1]);
+        continue;
+      }
+      const int64_t row = row0 + lane;
       if (row < a.M && col0 < a.N &&
           MXQ_IN_BOUNDS(mp < p.n_mp && nt < p.n_nt, &g_err_fp8_gemm, SITE_B_FP8_GEMM)) {
 #pragma unroll
@@ -847,6 +889,7 @@ mxq_status launch_pair(const void* A, const void* B, int64_t K, const FArgs& f, 
   const int e = f.out_bf16 ? 2 : 4;
   const uintptr_t c = reinterpret_cast<uintptr_t>(f.C);
   p.store = (f.N * e) % 32 == 0 && (c & 31u) == 0 ? 2 : (f.N * e) % 16 == 0 ? 1 : 0;
+  if (LINES) p.store = f.N % 2 == 0;
   cudaLaunchConfig_t cfg = {};
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeClusterDimension;
