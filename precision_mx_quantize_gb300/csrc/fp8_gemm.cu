@@ -341,7 +341,7 @@ __global__ void __launch_bounds__(L_THREADS)
 
 // ---- 256 x 256 tiles on CTA pairs ------------------------------------------------
 constexpr int P_THREADS = 384;                   // one control and two accumulation warpgroups
-constexpr int P_CTRL_REGS = 88, P_ACC_REGS = 208;
+constexpr int P_CTRL_REGS = 104, P_ACC_REGS = 200;
 // the split below is drawn from the registers the block is launched with
 constexpr int P_MIN_REGS = (128 * P_CTRL_REGS + 256 * P_ACC_REGS + P_THREADS - 1) / P_THREADS;
 constexpr int P_OPERAND = 128 * 128;             // a stage's lines of A, or of B, of one CTA
@@ -354,8 +354,11 @@ struct Pair {
   static constexpr int SLOT = LINES ? 384 : 256;          // floats
   static constexpr int SLOTS = 16;                        // two groups of eight
   static constexpr int SCALES = SLOTS * SLOT * 4;
-  static constexpr int STAGES = 6;
-  static constexpr int SMEM = STAGES * P_STAGE + SCALES + 512 + 1024;
+  // Four stages run as fast as six (a K block takes longer than a quarter of a
+  // stage's turnaround), and leave room for the tiles on their way out.
+  static constexpr int STAGES = 4;
+  static constexpr int OUT = 2 * 32768;                   // per half tile, 32 KB
+  static constexpr int SMEM = STAGES * P_STAGE + OUT + SCALES + 512 + 1024;
   static_assert(SMEM <= 227 * 1024, "shared memory of one CTA");
 };
 
@@ -363,8 +366,7 @@ struct PArgs {
   FArgs f;
   int32_t n_mp, n_nt, n_tiles;   // 256-row and 256-column tiles
   int32_t group, group_n;        // tile order (tile_coords)
-  int32_t store;                 // tiles: 2, 32-byte stores of C rows, 1, 16-byte, 0, elements;
-                                 // lines: 1, two columns at a time (N even), 0, elements
+  int32_t tma_out;               // rows of C are 16-byte multiples: tiles leave by TMA
 };
 
 MXQ_DEV void mma_f8_pair(uint32_t d_tmem, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accum) {
@@ -440,93 +442,104 @@ MXQ_DEV void load_cols(uint32_t addr, float (&col)[8]) {
                  : "memory");
 }
 
-// Stores two neighbouring columns of a row, as far as they lie in C.
-MXQ_DEV void store2(const PArgs& p, int64_t row, int64_t col, float x, float y) {
-  if (row >= p.f.M || col >= p.f.N) return;
-  const int64_t at = row * p.f.N + col;
-  if (p.f.out_bf16) {
-    __nv_bfloat16* c = static_cast<__nv_bfloat16*>(p.f.C) + at;
-    if (p.store) {   // N is even: both columns, aligned
-      *reinterpret_cast<__nv_bfloat162*>(c) = __floats2bfloat162_rn(x, y);
-    } else {
-      c[0] = __float2bfloat16_rn(x);
-      if (col + 1 < p.f.N) c[1] = __float2bfloat16_rn(y);
+// Place in a half tile of this thread's accumulator j: tiles, one row of 128
+// columns; lines, the fragments of load16.
+template <bool LINES>
+MXQ_DEV int acc_row(int j, int lane) {
+  return LINES ? ((j >> 4) & 1) * 16 + ((j >> 1) & 1) * 8 + (lane >> 2) : lane;
+}
+template <bool LINES>
+MXQ_DEV int acc_col(int j, int lane) {
+  return LINES ? (j >> 5) * 32 + ((j >> 2) & 3) * 8 + 2 * (lane & 3) + (j & 1) : j;
+}
+
+MXQ_DEV void sts(uint32_t addr, uint32_t a) {
+  asm volatile("st.shared.u32 [%0], %1;" ::"r"(addr), "r"(a) : "memory");
+}
+MXQ_DEV void sts(uint32_t addr, uint32_t a, uint32_t b) {
+  asm volatile("st.shared.v2.u32 [%0], {%1, %2};" ::"r"(addr), "r"(a), "r"(b) : "memory");
+}
+MXQ_DEV void sts(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+  asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(a), "r"(b), "r"(c),
+               "r"(d)
+               : "memory");
+}
+
+MXQ_DEV uint32_t bf16x2(float a, float b) {
+  const __nv_bfloat162 t = __floats2bfloat162_rn(a, b);
+  return *reinterpret_cast<const uint32_t*>(&t);
+}
+
+// Writes a half tile, rounded to C's type, as boxes of 128 rows x 128 bytes
+// with the 128-byte swizzle of the output's tensor map.  fp32 takes two passes
+// of 64 columns.
+template <bool LINES>
+MXQ_DEV void stage_out(const float (&acc)[128], uint32_t out, int quad, int lane, bool bf16,
+                       int pass) {
+  auto place = [&](int row, int byte) {   // byte: within the pass's columns
+    const int r = quad * 32 + row;
+    return out + (byte >> 7) * 16384 + r * 128 + ((byte & 127) ^ ((r & 7) << 4));
+  };
+  if (bf16) {
+#pragma unroll
+    for (int j = 0; j < 128; j += LINES ? 2 : 8) {
+      const uint32_t at = place(acc_row<LINES>(j, lane), 2 * acc_col<LINES>(j, lane));
+      const uint32_t w = bf16x2(acc[j], acc[j + 1]);
+      if constexpr (LINES)
+        sts(at, w);
+      else
+        sts(at, w, bf16x2(acc[j + 2], acc[j + 3]), bf16x2(acc[j + 4], acc[j + 5]),
+            bf16x2(acc[j + 6], acc[j + 7]));
     }
   } else {
-    float* c = static_cast<float*>(p.f.C) + at;
-    if (p.store) {
-      *reinterpret_cast<float2*>(c) = make_float2(x, y);
-    } else {
-      c[0] = x;
-      if (col + 1 < p.f.N) c[1] = y;
+#pragma unroll
+    for (int u = 0; u < 64; u += LINES ? 2 : 4) {
+      // both passes' registers are named at compile time
+      const float a = pass ? acc[64 + u] : acc[u], b = pass ? acc[65 + u] : acc[u + 1];
+      const uint32_t at = place(acc_row<LINES>(u, lane), 4 * acc_col<LINES>(u, lane));
+      if constexpr (LINES)
+        sts(at, __float_as_uint(a), __float_as_uint(b));
+      else
+        sts(at, __float_as_uint(a), __float_as_uint(b),
+            __float_as_uint(pass ? acc[66 + u] : acc[u + 2]),
+            __float_as_uint(pass ? acc[67 + u] : acc[u + 3]));
     }
   }
 }
 
-// The first n of 64 accumulated columns of one output row.
-MXQ_DEV void store64(const PArgs& p, const float* acc, int64_t row, int64_t col0, int n) {
-  if (p.f.out_bf16) {
-    __nv_bfloat16* c = static_cast<__nv_bfloat16*>(p.f.C) + row * p.f.N + col0;
-    uint32_t w[32];
+// A half tile straight from the registers, element by element (rows of C that
+// no tensor map can describe).
+template <bool LINES>
+MXQ_DEV void store_out(const FArgs& a, const float (&acc)[128], int64_t row0, int64_t col0,
+                       int lane) {
 #pragma unroll
-    for (int j = 0; j < 32; ++j) {
-      const __nv_bfloat162 b = __floats2bfloat162_rn(acc[2 * j], acc[2 * j + 1]);
-      w[j] = *reinterpret_cast<const uint32_t*>(&b);
-    }
-    if (p.store == 2) {   // N % 16 == 0: whole groups of 16 columns
-#pragma unroll
-      for (int j = 0; j < 32; j += 8)
-        if (2 * j < n)
-          st_global_v8(c + 2 * j, w[j], w[j + 1], w[j + 2], w[j + 3], w[j + 4], w[j + 5], w[j + 6],
-                       w[j + 7]);
-    } else if (p.store == 1) {
-#pragma unroll
-      for (int j = 0; j < 32; j += 4)
-        if (2 * j < n)
-          *reinterpret_cast<uint4*>(c + 2 * j) = make_uint4(w[j], w[j + 1], w[j + 2], w[j + 3]);
-    } else {
-      uint16_t* h = reinterpret_cast<uint16_t*>(c);
-#pragma unroll
-      for (int j = 0; j < 32; ++j) {
-        if (2 * j < n) h[2 * j] = static_cast<uint16_t>(w[j]);
-        if (2 * j + 1 < n) h[2 * j + 1] = static_cast<uint16_t>(w[j] >> 16);
-      }
-    }
-  } else {
-    float* c = static_cast<float*>(p.f.C) + row * p.f.N + col0;
-    if (p.store == 2) {   // N % 8 == 0
-#pragma unroll
-      for (int j = 0; j < 64; j += 8)
-        if (j < n)
-          st_global_v8(c + j, __float_as_uint(acc[j]), __float_as_uint(acc[j + 1]),
-                       __float_as_uint(acc[j + 2]), __float_as_uint(acc[j + 3]),
-                       __float_as_uint(acc[j + 4]), __float_as_uint(acc[j + 5]),
-                       __float_as_uint(acc[j + 6]), __float_as_uint(acc[j + 7]));
-    } else if (p.store == 1) {
-#pragma unroll
-      for (int j = 0; j < 64; j += 4)
-        if (j < n)
-          *reinterpret_cast<float4*>(c + j) =
-              make_float4(acc[j], acc[j + 1], acc[j + 2], acc[j + 3]);
-    } else {
-#pragma unroll
-      for (int j = 0; j < 64; ++j)
-        if (j < n) c[j] = acc[j];
-    }
+  for (int j = 0; j < 128; ++j) {
+    const int64_t row = row0 + acc_row<LINES>(j, lane), col = col0 + acc_col<LINES>(j, lane);
+    if (row >= a.M || col >= a.N) continue;
+    if (a.out_bf16) static_cast<__nv_bfloat16*>(a.C)[row * a.N + col] = __float2bfloat16_rn(acc[j]);
+    else static_cast<float*>(a.C)[row * a.N + col] = acc[j];
   }
+}
+
+MXQ_DEV void tma_store_2d(const CUtensorMap* map, uint32_t src, int32_t x, int32_t y) {
+  asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.tile.bulk_group [%0, {%2, %3}], [%1];" ::"l"(
+                   reinterpret_cast<uint64_t>(map)),
+               "r"(src), "r"(x), "r"(y)
+               : "memory");
 }
 
 template <bool LINES>
 __global__ void __launch_bounds__(P_THREADS, 1)
     fp8_gemm_pair(const __grid_constant__ CUtensorMap ta, const __grid_constant__ CUtensorMap tb,
-                  const PArgs p) {
+                  const __grid_constant__ CUtensorMap tc, const PArgs p) {
   using P = Pair<LINES>;
   constexpr int S = P::STAGES;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~static_cast<uintptr_t>(1023));
-  float* scales = reinterpret_cast<float*>(smem + S * P_STAGE);
-  uint64_t* full = reinterpret_cast<uint64_t*>(smem + S * P_STAGE + P::SCALES);
+  uint8_t* out = smem + S * P_STAGE;
+  float* scales = reinterpret_cast<float*>(out + P::OUT);
+  uint64_t* full = reinterpret_cast<uint64_t*>(out + P::OUT + P::SCALES);
   uint64_t* empty = full + S;
   uint64_t* acc_full = empty + S;
   uint64_t* sc_full = acc_full + 4;
@@ -546,6 +559,7 @@ __global__ void __launch_bounds__(P_THREADS, 1)
   if (threadIdx.x == 0) {
     prefetch_tmap(&ta);
     prefetch_tmap(&tb);
+    if (p.tma_out) prefetch_tmap(&tc);
     for (int s = 0; s < S; ++s) {
       mbar_init(smem_u32(&full[s]), 1);    // leader: one arrival, bytes of both CTAs
       mbar_init(smem_u32(&empty[s]), 1);
@@ -750,69 +764,79 @@ __global__ void __launch_bounds__(P_THREADS, 1)
 #pragma unroll
       for (int j = 0; j < 128; ++j) acc[j] = 0.0f;
 #pragma unroll 1
-      for (int kb = 0; kb < nk; ++kb, ++it) {
-        if ((kb & 7) == 0)   // sc_full follows acc_full[4]
-          fwait_or_abort(bars + 32 + 8 * (grp & 1), (grp >> 1) & 1, a.timeout_ns, abort_flag,
-                         SITE_FP8_SCALES);
-        const uint32_t at = sc + ((grp & 1) * 8 + (kb & 7)) * (4 * P::SLOT), b = it & 1;
-        float s1[LINES ? 4 : 1];   // lines: rows lane / 4 + 8 i of the warp's 32
+      for (int kb8 = 0; kb8 < nk; kb8 += 8, ++grp) {
+        uint32_t at = sc + (grp & 1) * (32 * P::SLOT);
+        const uint32_t end = at + min(8, nk - kb8) * (4 * P::SLOT);
+        fwait_or_abort(bars + 32 + 8 * (grp & 1), (grp >> 1) & 1, a.timeout_ns, abort_flag,
+                       SITE_FP8_SCALES);   // sc_full follows acc_full[4]
+#pragma unroll 1
+        for (; at != end; at += 4 * P::SLOT, ++it) {
+          const uint32_t b = it & 1;
+          float s1[LINES ? 4 : 1];   // lines: rows lane / 4 + 8 i of the warp's 32
 #pragma unroll
-        for (int i = 0; i < (LINES ? 4 : 1); ++i) s1[i] = lds32(at + row_at + 32 * i);
-        fwait_or_abort(bars + 8 * h + 16 * b, (it >> 1) & 1, a.timeout_ns, abort_flag,
-                       SITE_FP8_TMEM_FULL);
-        __syncwarp();
-        tc_fence_after();
-        const uint32_t taddr = taddr0 + b * 256;
-        // 16 words in flight while 16 are added
-        uint32_t v[2][16];
-        float col[8];
-        load16<LINES>(taddr, v[0]);
-#pragma unroll
-        for (int c = 0; c < 8; ++c) {
-          MXQ_TMEM_WAIT16(v[c & 1]);
-          if (c < 7) {
-            load16<LINES>(taddr + step16<LINES>(c + 1), v[(c + 1) & 1]);
-          } else {   // everything is read: hand the accumulator back first
-            tc_fence_before();
-            __syncwarp();
-            arrive_remote_if(lane == 0, empty_leader + b * 8);
-          }
-          if constexpr (LINES) {
-            if ((c & 1) == 0) load_cols(at + col_at + 64 * c, col);
-            add16(acc + 16 * c, v[c & 1], s1[2 * (c & 1)], s1[2 * (c & 1) + 1], col);
-          } else {
-            add16(acc + 16 * c, v[c & 1], s1[0]);
-          }
-        }
-        if ((kb & 7) == 7 || kb + 1 == nk) {   // the group's last block
+          for (int i = 0; i < (LINES ? 4 : 1); ++i) s1[i] = lds32(at + row_at + 32 * i);
+          fwait_or_abort(bars + 8 * h + 16 * b, (it >> 1) & 1, a.timeout_ns, abort_flag,
+                         SITE_FP8_TMEM_FULL);
           __syncwarp();
-          arrive_if(lane == 0, bars + 64 + 8 * (grp & 1));   // sc_empty
-          ++grp;
+          tc_fence_after();
+          const uint32_t taddr = taddr0 + b * 256;
+          // 16 words in flight while 16 are added
+          uint32_t v[2][16];
+          float col[8];
+          load16<LINES>(taddr, v[0]);
+#pragma unroll
+          for (int c = 0; c < 8; ++c) {
+            MXQ_TMEM_WAIT16(v[c & 1]);
+            if (c < 7) {
+              load16<LINES>(taddr + step16<LINES>(c + 1), v[(c + 1) & 1]);
+            } else {   // everything is read: hand the accumulator back first
+              tc_fence_before();
+              __syncwarp();
+              arrive_remote_if(lane == 0, empty_leader + b * 8);
+            }
+            if constexpr (LINES) {
+              if ((c & 1) == 0) load_cols(at + col_at + 64 * c, col);
+              add16(acc + 16 * c, v[c & 1], s1[2 * (c & 1)], s1[2 * (c & 1) + 1], col);
+            } else {
+              add16(acc + 16 * c, v[c & 1], s1[0]);
+            }
+          }
         }
+        __syncwarp();
+        arrive_if(lane == 0, bars + 64 + 8 * (grp & 1));   // sc_empty
       }
       if (__any_sync(~0u, *abort_flag)) break;
       int mp, nt;
       tile_coords(t, p, mp, nt);
-      const int64_t row0 = (int64_t(mp) * 2 + rank) * 128 + quad * 32;
-      const int64_t col0 = int64_t(nt) * 256 + h * 128;
-      if constexpr (LINES) {
-        if (!MXQ_IN_BOUNDS(mp < p.n_mp && nt < p.n_nt, &g_err_fp8_gemm, SITE_B_FP8_GEMM)) continue;
+      const int row0 = (mp * 2 + static_cast<int>(rank)) * 128, col0 = nt * 256 + h * 128;
+      if (!MXQ_IN_BOUNDS(mp < p.n_mp && nt < p.n_nt, &g_err_fp8_gemm, SITE_B_FP8_GEMM)) continue;
+      if (p.tma_out) {
+        // The half tile goes through shared memory and leaves by TMA, under
+        // the next tile's K loop: stored from the registers it took as long as
+        // three K blocks, and the MMAs only run two ahead.
+        const bool bf16 = a.out_bf16 != 0;
+        const uint32_t mine = smem_u32(out) + h * 32768;
+        const bool first = threadIdx.x % 128 == 0;   // issues and tracks the copies
 #pragma unroll
-        for (int j = 0; j < 128; j += 2)
-          store2(p, row0 + ((j >> 4) & 1) * 16 + ((j >> 1) & 1) * 8 + (lane >> 2),
-                 col0 + (j >> 5) * 32 + ((j >> 2) & 3) * 8 + 2 * (lane & 3), acc[j], acc[j + 1]);
-        continue;
-      }
-      const int64_t row = row0 + lane;
-      if (row < a.M && col0 < a.N &&
-          MXQ_IN_BOUNDS(mp < p.n_mp && nt < p.n_nt, &g_err_fp8_gemm, SITE_B_FP8_GEMM)) {
-#pragma unroll
-        for (int u = 0; u < 2; ++u) {
-          const int64_t left = a.N - col0 - u * 64;
-          if (left > 0) store64(p, acc + 64 * u, row, col0 + u * 64, left < 64 ? int(left) : 64);
+        for (int pass = 0; pass < 2; ++pass) {
+          if (pass && bf16) break;
+          if (first) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+          asm volatile("bar.sync %0, 128;" ::"r"(1 + h) : "memory");
+          stage_out<LINES>(acc, mine, quad, lane, bf16, pass);
+          asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+          asm volatile("bar.sync %0, 128;" ::"r"(1 + h) : "memory");
+          if (first && row0 < a.M) {
+            const int wide = bf16 ? 64 : 32, x = col0 + (bf16 ? 0 : 64 * pass);
+            if (x < a.N) tma_store_2d(&tc, mine, x, row0);
+            if (x + wide < a.N) tma_store_2d(&tc, mine + 16384, x + wide, row0);
+            asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+          }
         }
+      } else {
+        store_out<LINES>(a, acc, row0 + quad * 32, col0, lane);
       }
     }
+    if (threadIdx.x % 128 == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
   }
   tc_fence_before();
   cluster_sync();   // no CTA leaves while its peer may still signal it
@@ -887,9 +911,15 @@ mxq_status launch_pair(const void* A, const void* B, int64_t K, const FArgs& f, 
   p.n_tiles = p.n_mp * p.n_nt;
   choose_raster(p.n_mp, p.n_nt, double(f.M) * K, double(f.N) * K, 256.0 * K, p.group, p.group_n);
   const int e = f.out_bf16 ? 2 : 4;
-  const uintptr_t c = reinterpret_cast<uintptr_t>(f.C);
-  p.store = (f.N * e) % 32 == 0 && (c & 31u) == 0 ? 2 : (f.N * e) % 16 == 0 ? 1 : 0;
-  if (LINES) p.store = f.N % 2 == 0;
+  CUtensorMap tc = {};
+  p.tma_out = f.N * e % 16 == 0;
+  if (p.tma_out &&
+      tensor_map_2d(&tc, f.out_bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
+                                    : CU_TENSOR_MAP_DATA_TYPE_FLOAT32,
+                    f.C, static_cast<uint64_t>(f.N), static_cast<uint64_t>(f.M),
+                    static_cast<uint64_t>(f.N * e), static_cast<uint32_t>(128 / e), 128,
+                    CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_NONE) != CUDA_SUCCESS)
+    return MXQ_ERR_CUDA;
   cudaLaunchConfig_t cfg = {};
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -908,7 +938,7 @@ mxq_status launch_pair(const void* A, const void* B, int64_t K, const FArgs& f, 
   const int clusters = pair_clusters<LINES>(cfg);
   if (clusters <= 0) return MXQ_ERR_CUDA;
   cfg.gridDim = dim3(static_cast<unsigned>(2 * std::min(p.n_tiles, clusters)), 1, 1);
-  if (cudaLaunchKernelEx(&cfg, fp8_gemm_pair<LINES>, ta, tb, p) != cudaSuccess) {
+  if (cudaLaunchKernelEx(&cfg, fp8_gemm_pair<LINES>, ta, tb, tc, p) != cudaSuccess) {
     cudaGetLastError();
     return MXQ_ERR_CUDA;
   }
