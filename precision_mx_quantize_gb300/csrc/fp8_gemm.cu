@@ -48,6 +48,7 @@ struct FArgs {
   int64_t lines_a, lines_b;    // floats between the K blocks of line scales
   int32_t nk;                  // K blocks
   int32_t tiles;               // 1: sB holds tile scales, 0: line scales
+  uint32_t n_nt, split;        // fp8_gemm_lanes: 128-line tiles of B, CTAs that share one
   int32_t out_bf16;
   uint32_t idesc_fmt;          // element types of the instruction descriptor
   uint64_t timeout_ns;
@@ -164,9 +165,20 @@ MXQ_DEV void arrive_remote_if(bool p, uint32_t cluster_bar) {
       : "memory");
 }
 
+// Waits for this thread's tensor-memory loads; the registers pass through, so
+// that no use of them can move above the wait.
+#define MXQ_TMEM_WAIT16(r)                                                                       \
+  asm volatile("tcgen05.wait::ld.sync.aligned;"                                                  \
+               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]),         \
+                 "+r"(r[6]), "+r"(r[7]), "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]),       \
+                 "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15])                              \
+               :                                                                                 \
+               : "memory")
+
 // ---- 128 lines of B x T lines of A per CTA --------------------------------------
 constexpr int L_THREADS = 192;
 constexpr int L_WBYTES = 128 * 128;   // a stage's lines of B
+constexpr int L_MAX_SPLIT = 8;        // CTAs of a cluster that share a tile's K blocks
 
 template <int T>
 struct Lanes {
@@ -176,8 +188,15 @@ struct Lanes {
   static constexpr int STAGES = T == 128 ? 3 : T == 64 ? 4 : 5;   // two CTAs fit in an SM
   static constexpr int SMEM = STAGES * STAGE + 2 * T * 4 + 256 + 1024;
   static_assert(TMEM >= 32 && TMEM <= 256, "two CTAs share an SM's tensor memory");
-  static_assert(STAGE % 1024 == 0 && 2 * SMEM <= 227 * 1024, "swizzle atoms, two CTAs");
+  static_assert(STAGE % 1024 == 0 && 2 * (SMEM + 1024) <= 228 * 1024, "swizzle atoms, two CTAs");
+  static_assert(T * 128 * 4 <= STAGES * STAGE, "partial sums fit in the ring");
 };
+
+MXQ_DEV float ld_cluster(uint32_t addr) {
+  float v;
+  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
+  return v;
+}
 
 template <int T>
 __global__ void __launch_bounds__(L_THREADS)
@@ -197,9 +216,13 @@ __global__ void __launch_bounds__(L_THREADS)
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
 
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int64_t n0 = int64_t(blockIdx.x) * 128, m0 = int64_t(blockIdx.y) * T;
-  const int nk = a.nk;
+  const int warp = warp_index(), lane = threadIdx.x & 31;
+  const uint32_t split = a.split, rank = blockIdx.x % split;
+  const uint32_t tile = blockIdx.x / split;
+  const int64_t n0 = int64_t(tile % a.n_nt) * 128, m0 = int64_t(tile / a.n_nt) * T;
+  // this CTA's K blocks
+  const int kb0 = static_cast<int>(int64_t(a.nk) * rank / split);
+  const int nk = static_cast<int>(int64_t(a.nk) * (rank + 1) / split) - kb0;
   const uint64_t tmo = a.timeout_ns;
   if (threadIdx.x == 0) {
     prefetch_tmap(&ta);
@@ -220,54 +243,62 @@ __global__ void __launch_bounds__(L_THREADS)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
+  griddep_wait();
+  griddep_launch_dependents();
   const uint32_t tmem = *tmem_slot;
+  float acc[T];
 
   if (warp == 0) {
-    if (lane == 0) {
-      uint32_t s = 0, phase = 0, issued = 0;
-      bool ok = true;
-      for (int kb = 0; kb < nk; ++kb) {
-        if (!fwait(smem_u32(&empty[s]), phase ^ 1, tmo, abort_flag)) {
-          if (!*abort_flag) fabort(abort_flag, SITE_FP8_EMPTY);
-          ok = false;
-          break;
-        }
-        const uint32_t st = smem_u32(smem + s * L::STAGE), bar = smem_u32(&full[s]);
+    const bool one = elect_one();
+    uint32_t s = 0, phase = 0, issued = 0;
+    bool ok = true;
+    for (int kb = 0; kb < nk; ++kb) {
+      if (!fwait(smem_u32(&empty[s]), phase ^ 1, tmo, abort_flag)) {
+        if (one && !*abort_flag) fabort(abort_flag, SITE_FP8_EMPTY);
+        ok = false;
+        break;
+      }
+      const uint32_t st = smem_u32(smem + s * L::STAGE), bar = smem_u32(&full[s]);
+      if (one) {
         mbar_arrive_expect_tx(bar, L::STAGE);
-        tma_load_2d(st, &tb, bar, kb * 128, static_cast<int32_t>(n0));
-        tma_load_2d(st + L_WBYTES, &ta, bar, kb * 128, static_cast<int32_t>(m0));
-        ++issued;
-        if (++s == S) { s = 0; phase ^= 1; }
+        tma_load_2d(st, &tb, bar, (kb0 + kb) * 128, static_cast<int32_t>(n0));
+        tma_load_2d(st + L_WBYTES, &ta, bar, (kb0 + kb) * 128, static_cast<int32_t>(m0));
       }
-      if (!ok)   // the copies in flight land before shared memory is released
-        for (uint32_t k = issued > S ? issued - S : 0; k < issued; ++k)
-          if (!mbar_wait(smem_u32(&full[k % S]), (k / S) & 1, tmo)) break;
+      ++issued;
+      if (++s == S) { s = 0; phase ^= 1; }
     }
+    if (one && !ok)   // the copies in flight land before shared memory is released
+      for (uint32_t k = issued > S ? issued - S : 0; k < issued; ++k)
+        if (!mbar_wait(smem_u32(&full[k % S]), (k / S) & 1, tmo)) break;
   } else if (warp == 1) {
-    if (lane == 0) {
-      const uint32_t idesc = idesc_f8(a.idesc_fmt, 128, T);
-      uint32_t s = 0, phase = 0;
-      for (int kb = 0; kb < nk; ++kb) {
-        const int b = kb % NB;
-        if (!fwait(smem_u32(&acc_empty[b]), ((kb / NB) & 1) ^ 1, tmo, abort_flag)) {
-          if (!*abort_flag) fabort(abort_flag, SITE_FP8_TMEM_EMPTY);
-          break;
-        }
-        if (!fwait(smem_u32(&full[s]), phase, tmo, abort_flag)) {
-          if (!*abort_flag) fabort(abort_flag, SITE_FP8_FULL);
-          break;
-        }
-        tc_fence_after();
-        const uint32_t st = smem_u32(smem + s * L::STAGE);
-        const uint64_t wd = smem_desc(st, 0, 1024, 2), xd = smem_desc(st + L_WBYTES, 0, 1024, 2);
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-          mma_f8(tmem + b * T, wd + 2 * j, xd + 2 * j, idesc, j > 0 ? 1u : 0u);
-        tc_commit(smem_u32(&empty[s]));
-        tc_commit(smem_u32(&acc_full[b]));
-        if (++s == S) { s = 0; phase ^= 1; }
+    const bool one = elect_one();
+    const uint32_t idesc = idesc_f8(a.idesc_fmt, 128, T);
+    const uint64_t d0 = smem_desc(smem_u32(smem), 0, 1024, 2);
+    uint32_t s = 0, phase = 0;
+    for (int kb = 0; kb < nk; ++kb) {
+      const int b = kb % NB;
+      const uint64_t wd = d0 + s * (L::STAGE >> 4), xd = wd + (L_WBYTES >> 4);
+      if (!fwait(smem_u32(&acc_empty[b]), ((kb / NB) & 1) ^ 1, tmo, abort_flag)) {
+        if (one && !*abort_flag) fabort(abort_flag, SITE_FP8_TMEM_EMPTY);
+        break;
       }
-      tc_commit(smem_u32(drain));   // every MMA is complete before teardown
+      if (!fwait(smem_u32(&full[s]), phase, tmo, abort_flag)) {
+        if (one && !*abort_flag) fabort(abort_flag, SITE_FP8_FULL);
+        break;
+      }
+      tc_fence_after();
+      if (one) {
+        mma_f8(tmem + b * T, wd, xd, idesc, 0u);
+        mma_f8(tmem + b * T, wd + 2, xd + 2, idesc, 1u);
+        mma_f8(tmem + b * T, wd + 4, xd + 4, idesc, 1u);
+        mma_f8(tmem + b * T, wd + 6, xd + 6, idesc, 1u);
+        tc_commit(smem_u32(&acc_full[b]));
+        tc_commit(smem_u32(&empty[s]));
+      }
+      if (++s == S) { s = 0; phase ^= 1; }
+    }
+    if (one) {   // every MMA is complete before teardown
+      tc_commit(smem_u32(drain));
       if (!mbar_wait(smem_u32(drain), 0, tmo))
         record_error(&g_err_fp8_gemm, MXQ_ERR_TIMEOUT, SITE_FP8_DRAIN);
     }
@@ -276,19 +307,16 @@ __global__ void __launch_bounds__(L_THREADS)
     const int et = threadIdx.x - 64;          // epilogue thread
     const int64_t n = n0 + quad * 32 + lane;  // this thread's line of B
     const int64_t m = m0 + et;                // the line of A whose scale it stages
-    const int64_t n_kb = nk;
     auto scale_a = [&](int kb) {
-      return et < T && m < a.M && kb < nk ? a.sA[kb * a.lines_a + m] : 0.0f;
+      return et < T && m < a.M && kb < nk ? a.sA[(kb0 + kb) * a.lines_a + m] : 0.0f;
     };
     auto scale_b = [&](int kb) {
       if (n >= a.N || kb >= nk) return 0.0f;
-      return a.tiles ? a.sB[(n >> 7) * n_kb + kb] : a.sB[kb * a.lines_b + n];
+      return a.tiles ? a.sB[(n >> 7) * a.nk + kb0 + kb] : a.sB[(kb0 + kb) * a.lines_b + n];
     };
-    float acc[T];
 #pragma unroll
     for (int j = 0; j < T; ++j) acc[j] = 0.0f;
     float next_a = scale_a(0), next_b = scale_b(0);
-    bool ok = true;
     for (int kb = 0; kb < nk; ++kb) {
       const int b = kb % NB;
       // two scale buffers and one barrier a block: a warp that stages block
@@ -299,44 +327,67 @@ __global__ void __launch_bounds__(L_THREADS)
       next_a = scale_a(kb + 1);
       next_b = scale_b(kb + 1);
       asm volatile("bar.sync 1, 128;" ::: "memory");
-      if (ok && !fwait(smem_u32(&acc_full[b]), (kb / NB) & 1, tmo, abort_flag)) {
-        if (!*abort_flag) fabort(abort_flag, SITE_FP8_TMEM_FULL);
-        ok = false;
-      }
-      if (!__all_sync(~0u, ok)) {
-        ok = false;
-        continue;   // keeps the barrier count of the other warps
-      }
+      fwait_or_abort(smem_u32(&acc_full[b]), (kb / NB) & 1, tmo, abort_flag, SITE_FP8_TMEM_FULL);
+      __syncwarp();
       tc_fence_after();
       const uint32_t taddr = tmem + (static_cast<uint32_t>(quad * 32) << 16) + b * T;
 #pragma unroll
       for (int c = 0; c < T; c += 16) {
         uint32_t v[16];
         MXQ_TMEM_LD16(taddr + c, v);
-        tmem_ld_wait();
+        MXQ_TMEM_WAIT16(v);
 #pragma unroll
         for (int j = 0; j < 16; ++j)
-          acc[c + j] = __fmaf_rn(__uint_as_float(v[j]), sb * sa[(kb & 1) * T + c + j], acc[c + j]);
+          acc[c + j] = __fmaf_rn(__fmul_rn(__uint_as_float(v[j]), sb), sa[(kb & 1) * T + c + j],
+                                 acc[c + j]);
       }
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(smem_u32(&acc_empty[b]));
+      arrive_if(lane == 0, smem_u32(&acc_empty[b]));
     }
-    if (ok && n < a.N) {
+  }
+
+  auto store = [&](int64_t row, int64_t col, float v) {
+    if (!MXQ_IN_BOUNDS(row < a.M && col < a.N, &g_err_fp8_gemm, SITE_B_FP8_GEMM)) return;
+    if (a.out_bf16) static_cast<__nv_bfloat16*>(a.C)[row * a.N + col] = __float2bfloat16_rn(v);
+    else static_cast<float*>(a.C)[row * a.N + col] = v;
+  };
+  // [T][128] partial sums, over the ring: every MMA and copy of this CTA is
+  // complete once its last accumulator is
+  float* part = reinterpret_cast<float*>(smem);
+  const int col = (warp & 3) * 32 + lane;
+  if (warp >= 2) {
+    if (split == 1) {
+      if (n0 + col < a.N && !*abort_flag) {
 #pragma unroll
-      for (int j = 0; j < T; ++j) {
-        if (m0 + j >= a.M) break;
-        if (!MXQ_IN_BOUNDS(n < a.N && m0 + j < a.M, &g_err_fp8_gemm, SITE_B_FP8_GEMM)) continue;
-        const int64_t at = (m0 + j) * a.N + n;
-        if (a.out_bf16) static_cast<__nv_bfloat16*>(a.C)[at] = __float2bfloat16_rn(acc[j]);
-        else static_cast<float*>(a.C)[at] = acc[j];
+        for (int j = 0; j < T; ++j)
+          if (m0 + j < a.M) store(m0 + j, n0 + col, acc[j]);
       }
+    } else if (!*abort_flag) {
+#pragma unroll
+      for (int j = 0; j < T; ++j) part[j * 128 + col] = acc[j];
     }
   }
   tc_fence_before();
-  __syncthreads();
+  if (split == 1) __syncthreads();
+  else cluster_sync();
   tc_fence_after();
   if (warp == 1) tmem_dealloc(tmem, L::TMEM);
+  if (split == 1) return;
+  // Each CTA adds up a share of the tile's lines of A, over the CTAs in order.
+  if (warp >= 2 && n0 + col < a.N) {
+    const uint32_t mine = smem_u32(part + col);
+    for (int j = rank; j < T && m0 + j < a.M; j += split) {
+      float v[L_MAX_SPLIT], sum = 0.0f;
+#pragma unroll
+      for (int r = 0; r < L_MAX_SPLIT; ++r)
+        v[r] = r < split ? ld_cluster(map_to_rank(mine + j * 512, r)) : 0.0f;
+#pragma unroll
+      for (int r = 0; r < L_MAX_SPLIT; ++r) sum += v[r];
+      store(m0 + j, n0 + col, sum);
+    }
+  }
+  cluster_sync();   // no CTA leaves while a peer may still read its sums
 }
 
 // ---- 256 x 256 tiles on CTA pairs ------------------------------------------------
@@ -376,16 +427,6 @@ MXQ_DEV void mma_f8_pair(uint32_t d_tmem, uint64_t a, uint64_t b, uint32_t idesc
       "l"(a), "l"(b), "r"(idesc), "r"(accum)
       : "memory");
 }
-
-// Waits for this thread's tensor-memory loads; the registers pass through, so
-// that no use of them can move above the wait.
-#define MXQ_TMEM_WAIT16(r)                                                                       \
-  asm volatile("tcgen05.wait::ld.sync.aligned;"                                                  \
-               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]),         \
-                 "+r"(r[6]), "+r"(r[7]), "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]),       \
-                 "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15])                              \
-               :                                                                                 \
-               : "memory")
 
 MXQ_DEV float lds32(uint32_t addr) {
   float v;
@@ -881,16 +922,48 @@ bool code_map(CUtensorMap* map, const void* codes, int64_t lines, int64_t K, int
                        CU_TENSOR_MAP_L2_PROMOTION_L2_256B) == CUDA_SUCCESS;
 }
 
+// CTAs that share the K blocks of a tile.  A CTA streams its lines of B no
+// faster than its few copies in flight allow, and a product of few tokens has
+// few tiles: splitting K until two CTAs sit on every SM, as long as each keeps
+// four blocks, fills the machine (1x4096x14336: FIXME).
+uint32_t lanes_split(int64_t tiles, int nk) {
+  uint32_t split = 1;
+  while (split < L_MAX_SPLIT && tiles * split < 2 * sm_count() &&
+         nk >= static_cast<int>(8 * split))
+    split *= 2;
+  return split;
+}
+
 template <int T>
-mxq_status launch_lanes(const void* A, const void* B, int64_t K, const FArgs& a, void* stream) {
+mxq_status launch_lanes(const void* A, const void* B, int64_t K, FArgs a, void* stream) {
   CUtensorMap ta, tb;
   if (!code_map(&ta, A, a.M, K, T) || !code_map(&tb, B, a.N, K, 128)) return MXQ_ERR_CUDA;
-  const int64_t gx = (a.N + 127) / 128, gy = (a.M + T - 1) / T;
-  if (gy > 65535) return MXQ_ERR_ARG;
+  const int64_t n_nt = (a.N + 127) / 128, tiles = n_nt * ((a.M + T - 1) / T);
+  a.n_nt = static_cast<uint32_t>(n_nt);
+  a.split = lanes_split(tiles, a.nk);
+  if (tiles * a.split >= (int64_t(1) << 31)) return MXQ_ERR_ARG;
   if (!ensure_dynamic_smem(reinterpret_cast<const void*>(fp8_gemm_lanes<T>), Lanes<T>::SMEM))
     return MXQ_ERR_CUDA;
-  fp8_gemm_lanes<T><<<dim3(static_cast<unsigned>(gx), static_cast<unsigned>(gy)), L_THREADS,
-                      Lanes<T>::SMEM, static_cast<cudaStream_t>(stream)>>>(ta, tb, a);
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = a.split;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  // a CTA starts the dependents only once it runs itself, so the next kernel
+  // never takes the place of CTAs that still have to start
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
+  cfg.gridDim = dim3(static_cast<unsigned>(tiles * a.split), 1, 1);
+  cfg.blockDim = dim3(L_THREADS, 1, 1);
+  cfg.dynamicSmemBytes = Lanes<T>::SMEM;
+  cfg.stream = static_cast<cudaStream_t>(stream);
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  if (cudaLaunchKernelEx(&cfg, fp8_gemm_lanes<T>, ta, tb, a) != cudaSuccess) {
+    cudaGetLastError();
+    return MXQ_ERR_CUDA;
+  }
   return launch_status();
 }
 
