@@ -445,7 +445,7 @@ typedef struct {
   const float* rstd;   /* [rows]                                               */
   void* dx;            /* [rows][cols] of x_dtype                              */
   float* dweight;      /* [cols]                                               */
-  float* dbias;        /* [cols], or NULL                                      */
+  float* dbias;        /* [cols], or NULL (MXQ_NORM_LAYER only)                */
   void* workspace;     /* 256-byte aligned                                     */
   size_t workspace_bytes;
   int64_t rows, cols;

@@ -12,6 +12,8 @@
 // The variance is taken about the mean (two passes over the row), not as a
 // difference of moments, so that a large common offset costs no digits.  Sums
 // over rows run in a fixed order: no atomics.
+#include <type_traits>
+
 #include "fp8_common.cuh"
 #include "mxq_host.h"
 
@@ -76,6 +78,43 @@ MXQ_DEV void store8(float* row, int64_t col, int64_t cols, bool vec, const float
   }
 }
 
+// Eight elements of a row as they lie in memory.
+template <typename XT>
+struct Raw8;
+
+template <>
+struct Raw8<__nv_bfloat16> {
+  uint32_t w[4];
+  MXQ_DEV void load(const __nv_bfloat16* row, int64_t col, int64_t cols, bool vec) {
+    w[0] = w[1] = w[2] = w[3] = 0u;
+    if (col >= cols) return;
+    if (vec) {
+      const uint4 t = *reinterpret_cast<const uint4*>(row + col);
+      w[0] = t.x; w[1] = t.y; w[2] = t.z; w[3] = t.w;
+    } else {
+      const uint16_t* q = reinterpret_cast<const uint16_t*>(row + col);
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        if (col + j < cols) w[j >> 1] |= static_cast<uint32_t>(q[j]) << (16 * (j & 1));
+    }
+  }
+  MXQ_DEV float operator[](int j) const { return j & 1 ? bf16hi(w[j >> 1]) : bf16lo(w[j >> 1]); }
+};
+
+template <>
+struct Raw8<float> {
+  float f[8];
+  MXQ_DEV void load(const float* row, int64_t col, int64_t cols, bool vec) {
+    if (col < cols) {
+      load8(row, col, cols, vec, f);
+    } else {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) f[j] = 0.0f;
+    }
+  }
+  MXQ_DEV float operator[](int j) const { return f[j]; }
+};
+
 MXQ_DEV float warp_sum(float v) {
 #pragma unroll
   for (int d = 16; d; d >>= 1) v += __shfl_xor_sync(~0u, v, d);
@@ -126,12 +165,23 @@ struct NArgs {
   int32_t vec;
 };
 
+// The scale of block kb of row r; the last row also writes those of the
+// padding lines (an all-zero block's).
+MXQ_DEV void store_scale(const NArgs& a, int64_t kb, int64_t r, float scale) {
+  float* s = a.scales + kb * a.lines;
+  s[r] = scale;
+  if (r == a.rows - 1)
+    for (int64_t l = a.rows; l < a.lines; ++l) s[l] = F_TINY;
+}
+
 // One CTA per row, reading the row again for each pass (rows of any length).
 template <typename XT, typename WT, bool LAYER, int FMT>
 __global__ void __launch_bounds__(256) norm_rows(const NArgs a) {
   __shared__ float buf[N_MAX_WARPS];
   const int64_t r = blockIdx.x, cols = a.cols;
   const int64_t n_chunks = (cols + 7) / 8, n_pad = (n_chunks + 15) / 16 * 16;
+  griddep_wait();
+  griddep_launch_dependents();
   const XT* x = static_cast<const XT*>(a.x) + r * cols;
   const WT* w = static_cast<const WT*>(a.weight);
   const WT* b = static_cast<const WT*>(a.bias);
@@ -179,17 +229,91 @@ __global__ void __launch_bounds__(256) norm_rows(const NArgs a) {
       const uint2 q = encode_block<FMT>(f, scale);
       if (8 * c < a.pitch)
         *reinterpret_cast<uint2*>(a.codes + r * a.pitch + 8 * c) = q;
-      if ((c & 15) == 0) a.scales[(c >> 4) * a.lines + r] = scale;
+      if ((c & 15) == 0) store_scale(a, c >> 4, r, scale);
     }
   }
 }
 
-// Scales of the padding lines: those of an all-zero block.
-__global__ void norm_pad_scales(float* scales, int64_t rows, int64_t lines, int64_t kb) {
-  const int64_t n = lines - rows;
-  for (int64_t i = int64_t(blockIdx.x) * blockDim.x + threadIdx.x; i < n * kb;
-       i += int64_t(gridDim.x) * blockDim.x)
-    scales[(i / n) * lines + rows + i % n] = F_TINY;
+// Rows of at most 8 I elements per thread, read once and kept in registers:
+// a warp per row (WARP, eight rows a CTA) or a CTA per row.
+//
+// Bound by HBM.  A row's reductions are two round trips through shared memory
+// (RMS one), hidden by the other rows resident on the SM; weight and bias are
+// loaded before them.
+template <typename XT, typename WT, bool LAYER, int FMT, bool WARP, int I>
+__global__ void __launch_bounds__(WARP ? 256 : 512) norm_regs(const NArgs a) {
+  __shared__ float buf[WARP ? 1 : 2 * N_MAX_WARPS];
+  const int64_t cols = a.cols;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int64_t r = WARP ? int64_t(blockIdx.x) * 8 + warp : blockIdx.x;
+  const int t = WARP ? lane : threadIdx.x, nt = WARP ? 32 : blockDim.x;
+  const bool vec = a.vec != 0;
+  griddep_wait();
+  griddep_launch_dependents();
+  if (r >= a.rows) return;   // whole warps, and only where a warp has its own row
+  const XT* x = static_cast<const XT*>(a.x) + r * cols;
+  Raw8<XT> raw[I];
+  Raw8<WT> w[I], b[I];
+#pragma unroll
+  for (int i = 0; i < I; ++i) raw[i].load(x, 8 * (t + i * nt), cols, vec);
+#pragma unroll
+  for (int i = 0; i < I; ++i) {
+    w[i].load(static_cast<const WT*>(a.weight), 8 * (t + i * nt), cols, vec);
+    if (LAYER && a.bias) b[i].load(static_cast<const WT*>(a.bias), 8 * (t + i * nt), cols, vec);
+  }
+  // Sum over the row; `part` numbers the reduction, each with its own buffer.
+  auto row_sum = [&](float v, int part) {
+    v = warp_sum(v);
+    if constexpr (WARP) return v;
+    const int nw = nt >> 5;
+    float* mine = buf + (WARP ? 0 : part * N_MAX_WARPS);
+    if (lane == 0) mine[warp] = v;
+    __syncthreads();
+    return warp_sum(lane < nw ? mine[lane] : 0.0f);
+  };
+  const float inv_n = 1.0f / static_cast<float>(cols);
+  float mean = 0.0f, s = 0.0f;
+  if constexpr (LAYER) {
+#pragma unroll
+    for (int i = 0; i < I; ++i)
+#pragma unroll
+      for (int j = 0; j < 8; ++j) s += raw[i][j];   // zero past the row's end
+    mean = row_sum(s, 0) * inv_n;
+    s = 0.0f;
+  }
+#pragma unroll
+  for (int i = 0; i < I; ++i) {
+    const int64_t c = 8 * (t + i * nt);
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+      if (vec ? c < cols : c + j < cols) s += (raw[i][j] - mean) * (raw[i][j] - mean);
+  }
+  const float rstd = 1.0f / sqrtf(row_sum(s, 1) * inv_n + a.eps);
+  if (t == 0) {
+    if (LAYER && a.mean) a.mean[r] = mean;
+    if (a.rstd) a.rstd[r] = rstd;
+  }
+#pragma unroll
+  for (int i = 0; i < I; ++i) {
+    const int64_t c = 8 * (t + i * nt);
+    if (8 * ((c >> 3) & ~int64_t(15)) >= cols) break;   // uniform over the 16 lanes of a block
+    float f[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      f[j] = (raw[i][j] - mean) * rstd * w[i][j];
+      if (LAYER && a.bias) f[j] += b[i][j];
+      if (vec ? c >= cols : c + j >= cols) f[j] = 0.0f;
+    }
+    if (a.y && c < cols && MXQ_IN_BOUNDS(r < a.rows, &g_err_norm, SITE_B_NORM))
+      store8(static_cast<XT*>(a.y) + r * cols, c, cols, vec, f);
+    if constexpr (FMT >= 0) {
+      float scale;
+      const uint2 q = encode_block<FMT>(f, scale);
+      if (c < a.pitch && MXQ_IN_BOUNDS(c + 8 <= a.pitch, &g_err_norm, SITE_B_NORM))
+        *reinterpret_cast<uint2*>(a.codes + r * a.pitch + c) = q;
+      if (((c >> 3) & 15) == 0) store_scale(a, c >> 7, r, scale);
+    }
+  }
 }
 
 struct NGrad {
@@ -243,6 +367,121 @@ __global__ void __launch_bounds__(256) norm_grad_rows(const NGrad a) {
   }
 }
 
+// Backward for rows of at most 8 I elements per thread: a warp per row (WARP)
+// or a CTA per row, over every grid-th row.  A thread keeps its columns' sums
+// of dw and db in registers for all its rows, so x and dy are read once; the
+// next row's are loaded under this row's reduction.  The CTA's sums go to
+// `part`, which norm_grad_join adds up in order.
+template <typename XT, typename WT, bool LAYER, bool WARP, int I>
+__global__ void __launch_bounds__(WARP ? 256 : 512) norm_grad_regs(const NGrad a) {
+  extern __shared__ float sums[];          // WARP: [8][8 I 32] for the final join
+  __shared__ float2 buf[WARP ? 1 : 2 * N_MAX_WARPS];
+  const int64_t cols = a.cols;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int t = WARP ? lane : threadIdx.x, nt = WARP ? 32 : blockDim.x;
+  const int64_t first = WARP ? int64_t(blockIdx.x) * 8 + warp : blockIdx.x;
+  const int64_t step = WARP ? int64_t(gridDim.x) * 8 : gridDim.x;
+  const bool vec = a.vec != 0;
+  const float inv_n = 1.0f / static_cast<float>(cols);
+  griddep_wait();
+  griddep_launch_dependents();
+  float dw[I][8], db[I][8];
+#pragma unroll
+  for (int i = 0; i < I; ++i)
+#pragma unroll
+    for (int j = 0; j < 8; ++j) dw[i][j] = db[i][j] = 0.0f;
+  Raw8<WT> w[I];
+#pragma unroll
+  for (int i = 0; i < I; ++i) w[i].load(static_cast<const WT*>(a.weight), 8 * (t + i * nt), cols, vec);
+  Raw8<XT> x[I], dy[I];
+  float mean = 0.0f, rstd = 0.0f;
+  auto load = [&](int64_t r) {
+    if (r >= a.rows) return;
+#pragma unroll
+    for (int i = 0; i < I; ++i) {
+      x[i].load(static_cast<const XT*>(a.x) + r * cols, 8 * (t + i * nt), cols, vec);
+      dy[i].load(static_cast<const XT*>(a.dy) + r * cols, 8 * (t + i * nt), cols, vec);
+    }
+    mean = LAYER ? a.mean[r] : 0.0f;
+    rstd = a.rstd[r];
+  };
+  load(first);
+  int phase = 0;
+  for (int64_t r = first; r < a.rows; r += step, phase ^= 1) {
+    float s1 = 0.0f, s2 = 0.0f;
+    float h[I][8], g[I][8];
+    const float m = mean, rs = rstd;
+#pragma unroll
+    for (int i = 0; i < I; ++i) {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const float d = dy[i][j];               // zero past the row's end
+        h[i][j] = (x[i][j] - m) * rs;
+        dw[i][j] += d * h[i][j];
+        db[i][j] += d;
+        g[i][j] = d * w[i][j];
+        s1 += g[i][j];
+        s2 += g[i][j] * h[i][j];
+      }
+    }
+    load(r + step);
+    s2 = warp_sum(s2);
+    if (LAYER) s1 = warp_sum(s1);
+    if constexpr (!WARP) {
+      // two buffers, one barrier a row: a warp writes row k + 2's sums after
+      // barrier k + 1, which every warp reached after reading row k's
+      float2* mine = buf + phase * N_MAX_WARPS;
+      if (lane == 0) mine[warp] = make_float2(s1, s2);
+      __syncthreads();
+      const float2 v = lane < (nt >> 5) ? mine[lane] : make_float2(0.0f, 0.0f);
+      s2 = warp_sum(v.y);
+      if (LAYER) s1 = warp_sum(v.x);
+    }
+    const float c1 = LAYER ? s1 * inv_n : 0.0f, c2 = s2 * inv_n;
+#pragma unroll
+    for (int i = 0; i < I; ++i) {
+      const int64_t c = 8 * (t + i * nt);
+      if (c >= cols) break;
+      float f[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) f[j] = rs * (g[i][j] - c1 - h[i][j] * c2);
+      if (MXQ_IN_BOUNDS(r < a.rows, &g_err_norm, SITE_B_NORM_GRAD))
+        store8(static_cast<XT*>(a.dx) + r * cols, c, cols, vec, f);
+    }
+  }
+  float* part = a.part + int64_t(blockIdx.x) * 2 * cols;
+  if constexpr (WARP) {
+    // the eight warps' sums, in order
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      if (k == 1 && !LAYER) break;
+      __syncthreads();
+#pragma unroll
+      for (int i = 0; i < I; ++i)
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+          sums[(warp * 8 * I + 8 * i + j) * 32 + lane] = k ? db[i][j] : dw[i][j];
+      __syncthreads();
+      for (int e = threadIdx.x; e < 8 * I * 32; e += 256) {
+        float v = 0.0f;
+#pragma unroll
+        for (int q = 0; q < 8; ++q) v += sums[q * 8 * I * 32 + e];
+        // element e: lane e % 32, chunk and place e / 32
+        const int64_t c = 8 * ((e & 31) + (e >> 8) * 32) + ((e >> 5) & 7);
+        if (c < cols) part[k * cols + c] = v;
+      }
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < I; ++i) {
+      const int64_t c = 8 * (t + i * nt);
+      if (c >= cols) break;
+      store8(part, c, cols, cols % 4 == 0 && vec, dw[i]);
+      if (LAYER) store8(part + cols, c, cols, cols % 4 == 0 && vec, db[i]);
+    }
+  }
+}
+
 // Partial sums of dw and db: a CTA takes 256 columns and every splits-th
 // group of rows, one column per thread.
 template <typename XT, bool LAYER>
@@ -263,44 +502,158 @@ __global__ void __launch_bounds__(256) norm_grad_cols(const NGrad a) {
   p[a.cols + c] = db;
 }
 
-// The partial sums of each column, in the order of the splits.
-__global__ void __launch_bounds__(256) norm_grad_join(const float* part, int64_t cols, int splits,
-                                                      float* dweight, float* dbias) {
-  const int64_t c = int64_t(blockIdx.x) * 256 + threadIdx.x;
-  if (c >= cols) return;
+// The partial sums of each column, in a fixed order: 32 columns a CTA, its
+// eight warps take every eighth split each and are added up in order.
+struct JoinArgs {
+  const float* part;   // [splits][2][cols]
+  int64_t cols;
+  int splits;
+  float* dweight;
+  float* dbias;        // or null
+};
+
+__global__ void __launch_bounds__(256) norm_grad_join(const JoinArgs a) {
+  __shared__ float sums[2][8][32];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int64_t cols = a.cols, c = int64_t(blockIdx.x) * 32 + lane;
+  griddep_wait();
+  griddep_launch_dependents();
   float dw = 0.0f, db = 0.0f;
-  for (int s = 0; s < splits; ++s) {
-    dw += part[int64_t(s) * 2 * cols + c];
-    db += part[int64_t(s) * 2 * cols + cols + c];
+  if (c < cols) {
+#pragma unroll 4
+    for (int s = warp; s < a.splits; s += 8) {
+      const float* p = a.part + int64_t(s) * 2 * cols + c;
+      dw += p[0];
+      if (a.dbias) db += p[cols];
+    }
   }
-  dweight[c] = dw;
-  if (dbias) dbias[c] = db;
+  sums[0][warp][lane] = dw;
+  sums[1][warp][lane] = db;
+  __syncthreads();
+  if (warp < 2 && c < cols) {
+    float* out = warp ? a.dbias : a.dweight;
+    float v = 0.0f;
+#pragma unroll
+    for (int q = 0; q < 8; ++q) v += sums[warp][q][lane];
+    if (out && MXQ_IN_BOUNDS(c < cols, &g_err_norm, SITE_B_NORM_GRAD)) out[c] = v;
+  }
 }
 
-int grad_splits(int64_t rows, int64_t cols) {
-  const int64_t groups = (cols + 255) / 256;
-  const int64_t want = std::max<int64_t>(1, 8 * 152 / groups);
+// How a row is split: a warp per row, or a CTA of nt threads, with i chunks of
+// eight elements per thread; i == 0: the row does not fit the registers.
+struct RowPlan {
+  bool warp;
+  int nt, i;
+};
+
+// Forward.  Up to 1024 columns a warp holds a row (no barrier).  Longer rows
+// take a CTA: with few rows, one chunk a thread (latency: a row spread over
+// more threads); with many, two, which halves the warps of each reduction.
+RowPlan forward_plan(int64_t rows, int64_t cols) {
+  const int64_t chunks = (cols + 7) / 8;
+  if (chunks <= 128) return {true, 256, chunks <= 32 ? 1 : chunks <= 64 ? 2 : 4};
+  const int least = rows >= 4 * sm_count() ? 2 : 1;
+  for (int i = least; i <= 4; i *= 2)
+    if (chunks <= 512 * i)
+      return {false, static_cast<int>(((chunks + i - 1) / i + 31) / 32 * 32), i};
+  return {false, 256, 0};
+}
+
+// Backward.  The sums of dw and db take 16 registers a chunk beside x and dy:
+// four chunks a thread fit for bf16 rows, two for fp32 and for a warp's row.
+RowPlan backward_plan(int64_t cols, int x_dtype) {
+  const int64_t chunks = (cols + 7) / 8;
+  if (chunks <= 64) return {true, 256, chunks <= 32 ? 1 : 2};
+  for (int i = chunks <= 256 ? 1 : 2; i <= (x_dtype == MXQ_OUT_BF16 ? 4 : 2); i *= 2)
+    if (chunks <= 512 * i)
+      return {false, static_cast<int>(((chunks + i - 1) / i + 31) / 32 * 32), i};
+  return {false, 256, 0};
+}
+
+// Sets of partial sums.  Register kernels: one per CTA, as many CTAs as the
+// registers let an SM hold at once (about 768, 512 and 512 threads with one,
+// two and four chunks each).  Longer rows: enough that the column sums fill the
+// device.
+int grad_splits(int64_t rows, int64_t cols, int x_dtype) {
+  const RowPlan p = backward_plan(cols, x_dtype);
+  if (p.i) {
+    const int per_sm = std::max(1, (p.i == 1 ? 768 : 512) / p.nt);
+    const int64_t want = int64_t(per_sm) * sm_count();
+    return static_cast<int>(std::min<int64_t>(p.warp ? (rows + 7) / 8 : rows, want));
+  }
+  const int64_t want = std::max<int64_t>(1, 8 * sm_count() / ((cols + 255) / 256));
   return static_cast<int>(std::min<int64_t>(std::min<int64_t>(rows, want), 512));
+}
+
+// A launch that may start while the previous kernel on the stream drains; the
+// kernels wait for it before their first global access.
+template <typename K, typename A>
+bool launch_early(K kernel, unsigned grid, int threads, size_t smem, cudaStream_t st, const A& a) {
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.gridDim = dim3(grid, 1, 1);
+  cfg.blockDim = dim3(static_cast<unsigned>(threads), 1, 1);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  if (cudaLaunchKernelEx(&cfg, kernel, a) == cudaSuccess) return true;
+  cudaGetLastError();
+  return false;
+}
+
+template <typename XT, typename WT, bool LAYER, int FMT>
+mxq_status launch_forward(const NArgs& a, cudaStream_t st) {
+  const RowPlan p = forward_plan(a.rows, a.cols);
+  const unsigned rows = static_cast<unsigned>(a.rows), groups = (rows + 7) / 8;
+  bool ok;
+  if (p.warp) {
+    ok = p.i == 1   ? launch_early(norm_regs<XT, WT, LAYER, FMT, true, 1>, groups, 256, 0, st, a)
+         : p.i == 2 ? launch_early(norm_regs<XT, WT, LAYER, FMT, true, 2>, groups, 256, 0, st, a)
+                    : launch_early(norm_regs<XT, WT, LAYER, FMT, true, 4>, groups, 256, 0, st, a);
+  } else {
+    ok = p.i == 1   ? launch_early(norm_regs<XT, WT, LAYER, FMT, false, 1>, rows, p.nt, 0, st, a)
+         : p.i == 2 ? launch_early(norm_regs<XT, WT, LAYER, FMT, false, 2>, rows, p.nt, 0, st, a)
+         : p.i == 4 ? launch_early(norm_regs<XT, WT, LAYER, FMT, false, 4>, rows, p.nt, 0, st, a)
+                    : launch_early(norm_rows<XT, WT, LAYER, FMT>, rows, 256, 0, st, a);
+  }
+  return ok ? launch_status() : MXQ_ERR_CUDA;
 }
 
 template <typename XT, typename WT, bool LAYER>
 mxq_status run_forward(const NArgs& a, int fmt, cudaStream_t st) {
-  const unsigned grid = static_cast<unsigned>(a.rows);
-  if (!a.codes) norm_rows<XT, WT, LAYER, -1><<<grid, 256, 0, st>>>(a);
-  else if (fmt == MXQ_E4M3) norm_rows<XT, WT, LAYER, MXQ_E4M3><<<grid, 256, 0, st>>>(a);
-  else norm_rows<XT, WT, LAYER, MXQ_E5M2><<<grid, 256, 0, st>>>(a);
-  if (a.codes && a.lines > a.rows)
-    norm_pad_scales<<<1, 256, 0, st>>>(a.scales, a.rows, a.lines, (a.cols + 127) / 128);
-  return launch_status();
+  if (!a.codes) return launch_forward<XT, WT, LAYER, -1>(a, st);
+  return fmt == MXQ_E4M3 ? launch_forward<XT, WT, LAYER, MXQ_E4M3>(a, st)
+                         : launch_forward<XT, WT, LAYER, MXQ_E5M2>(a, st);
 }
 
 template <typename XT, typename WT, bool LAYER>
 mxq_status run_backward(const NGrad& a, cudaStream_t st) {
-  norm_grad_rows<XT, WT, LAYER><<<static_cast<unsigned>(a.rows), 256, 0, st>>>(a);
-  const unsigned groups = static_cast<unsigned>((a.cols + 255) / 256);
-  norm_grad_cols<XT, LAYER><<<dim3(groups, static_cast<unsigned>(a.splits)), 256, 0, st>>>(a);
-  norm_grad_join<<<groups, 256, 0, st>>>(a.part, a.cols, a.splits, a.dweight, a.dbias);
-  return launch_status();
+  const RowPlan p = backward_plan(a.cols, std::is_same<XT, float>::value ? MXQ_OUT_F32
+                                                                         : MXQ_OUT_BF16);
+  const unsigned grid = static_cast<unsigned>(a.splits);
+  bool ok = true;
+  if (p.warp) {
+    const size_t smem = size_t(8) * 8 * p.i * 32 * sizeof(float);
+    ok = p.i == 1 ? launch_early(norm_grad_regs<XT, WT, LAYER, true, 1>, grid, 256, smem, st, a)
+                  : launch_early(norm_grad_regs<XT, WT, LAYER, true, 2>, grid, 256, smem, st, a);
+  } else if (p.i) {
+    if (p.i == 1) ok = launch_early(norm_grad_regs<XT, WT, LAYER, false, 1>, grid, p.nt, 0, st, a);
+    else if (p.i == 2)
+      ok = launch_early(norm_grad_regs<XT, WT, LAYER, false, 2>, grid, p.nt, 0, st, a);
+    else if constexpr (std::is_same<XT, __nv_bfloat16>::value)
+      ok = launch_early(norm_grad_regs<XT, WT, LAYER, false, 4>, grid, p.nt, 0, st, a);
+  } else {
+    norm_grad_rows<XT, WT, LAYER><<<static_cast<unsigned>(a.rows), 256, 0, st>>>(a);
+    const unsigned groups = static_cast<unsigned>((a.cols + 255) / 256);
+    norm_grad_cols<XT, LAYER><<<dim3(groups, grid), 256, 0, st>>>(a);
+  }
+  if (!ok) return MXQ_ERR_CUDA;
+  const JoinArgs j{a.part, a.cols, a.splits, a.dweight, a.dbias};
+  ok = launch_early(norm_grad_join, static_cast<unsigned>((a.cols + 31) / 32), 256, 0, st, j);
+  return ok ? launch_status() : MXQ_ERR_CUDA;
 }
 
 // Calls f<XT, WT, LAYER>() for the run-time types.
@@ -395,7 +748,9 @@ extern "C" mxq_status mxq_norm_forward(const mxq_norm_args* p, void* stream) {
 extern "C" size_t mxq_norm_backward_workspace_size(int64_t rows, int64_t cols) {
   if (check_common(rows, cols, MXQ_NORM_LAYER, MXQ_OUT_F32, MXQ_OUT_F32) != MXQ_OK) return 0;
   if (rows == 0 || cols == 0) return 0;
-  return static_cast<size_t>(grad_splits(rows, cols)) * 2 * cols * sizeof(float);
+  const int splits = std::max(grad_splits(rows, cols, MXQ_OUT_BF16),
+                              grad_splits(rows, cols, MXQ_OUT_F32));
+  return static_cast<size_t>(splits) * 2 * cols * sizeof(float);
 }
 
 extern "C" mxq_status mxq_norm_backward(const mxq_norm_grad_args* p, void* stream) {
@@ -412,6 +767,7 @@ extern "C" mxq_status mxq_norm_backward(const mxq_norm_grad_args* p, void* strea
     return MXQ_OK;
   }
   if (!p->dy || !p->x || !p->weight || !p->rstd || !p->dx || !p->workspace) return MXQ_ERR_ARG;
+  if (p->dbias && p->kind != MXQ_NORM_LAYER) return MXQ_ERR_ARG;
   if (p->kind == MXQ_NORM_LAYER && !p->mean) return MXQ_ERR_ARG;
   if (!aligned16(p->dy) || !aligned16(p->x) || !aligned16(p->weight) || !aligned16(p->dx))
     return MXQ_ERR_ALIGN;
@@ -430,7 +786,7 @@ extern "C" mxq_status mxq_norm_backward(const mxq_norm_grad_args* p, void* strea
   a.part = static_cast<float*>(p->workspace);
   a.rows = p->rows;
   a.cols = p->cols;
-  a.splits = grad_splits(p->rows, p->cols);
+  a.splits = grad_splits(p->rows, p->cols, p->x_dtype);
   a.vec = p->cols % 8 == 0;
   return dispatch(p->x_dtype, p->w_dtype, p->kind, Backward{a, s});
 }

@@ -19,6 +19,7 @@ from __future__ import annotations
 import ctypes
 import functools
 import os
+import struct
 import threading
 
 import torch
@@ -107,6 +108,11 @@ class NormGradArgs(ctypes.Structure):
                 ("rows", ctypes.c_int64), ("cols", ctypes.c_int64), ("kind", ctypes.c_int),
                 ("x_dtype", ctypes.c_int), ("w_dtype", ctypes.c_int)]
 
+
+# The same two structures as native-layout formats: packing one takes a third
+# of the time of filling the ctypes mirror, which small calls notice.
+_NORM_ARGS = struct.Struct("@8P2qf4i0q")
+_NORM_GRAD_ARGS = struct.Struct("@9PN2q3i0q")
 
 _lib = None
 _lock = threading.Lock()
@@ -261,12 +267,12 @@ def mxq_fp8_gemm(A, sA, fmt_a, B, sB, fmt_b, b_scales, M, N, K, C, out_dtype, st
 
 
 def mxq_norm_forward(args, stream):
-    """args: address of a NormArgs structure in host memory."""
+    """args: address of a NormArgs structure in host memory, or its bytes."""
     return lib().mxq_norm_forward(args, stream)
 
 
 def mxq_norm_backward(args, stream):
-    """args: address of a NormGradArgs structure in host memory."""
+    """args: address of a NormGradArgs structure in host memory, or its bytes."""
     return lib().mxq_norm_backward(args, stream)
 
 
@@ -574,6 +580,7 @@ def mx_gemm_quantize(A, sA, B, sB, fmt, M, N, K, out_fmt="e4m3", out=None, works
 
 # ---- FP8 with one fp32 scale per block of 128 ---------------------------------------
 
+@functools.lru_cache(maxsize=4096)
 def fp8_shapes(lines: int, blocked: int, scales="line"):
     """(codes shape, scales shape) of `lines` code lines of `blocked` elements:
     a line's pitch is `blocked` rounded up to 16; line scales are [ceil(blocked
@@ -605,9 +612,12 @@ def fp8_quantize(x: torch.Tensor, axis="row", fmt="e4m3", out=None):
     R, C = x.shape
     ax, f = AXES[axis], FP8_FMTS[fmt]
     lines, blocked = (R, C) if ax == ROWWISE else (C, R)
-    codes, scales = out if out is not None else _fp8_buffers(lines, blocked, "line", x.device)
     dev = x.get_device()
-    _need_fp8(codes, scales, lines, blocked, "line", dev)
+    if out is None:
+        codes, scales = _fp8_buffers(lines, blocked, "line", x.device)
+    else:
+        codes, scales = out
+        _need_fp8(codes, scales, lines, blocked, "line", dev)
     _ok(mxq_fp8_quantize(x.data_ptr(), R, C, ax, f, codes.data_ptr(), scales.data_ptr(),
                          _stream(dev)), "mxq_fp8_quantize")
     return codes, scales
@@ -619,12 +629,14 @@ def fp8_quantize_dual(x: torch.Tensor, fmt_r="e4m3", fmt_c="e4m3", out=None):
     _need_input(x)
     R, C = x.shape
     fr, fc = FP8_FMTS[fmt_r], FP8_FMTS[fmt_c]
-    if out is None:
-        out = _fp8_buffers(R, C, "line", x.device) + _fp8_buffers(C, R, "line", x.device)
-    cr, sr, cc, sc = out
     dev = x.get_device()
-    _need_fp8(cr, sr, R, C, "line", dev, "_r")
-    _need_fp8(cc, sc, C, R, "line", dev, "_c")
+    if out is None:
+        cr, sr = _fp8_buffers(R, C, "line", x.device)
+        cc, sc = _fp8_buffers(C, R, "line", x.device)
+    else:
+        cr, sr, cc, sc = out
+        _need_fp8(cr, sr, R, C, "line", dev, "_r")
+        _need_fp8(cc, sc, C, R, "line", dev, "_c")
     _ok(mxq_fp8_quantize_dual(x.data_ptr(), R, C, fr, cr.data_ptr(), sr.data_ptr(), fc,
                               cc.data_ptr(), sc.data_ptr(), _stream(dev)), "mxq_fp8_quantize_dual")
     return cr, sr, cc, sc
@@ -637,13 +649,15 @@ def fp8_quantize_tiles(w: torch.Tensor, fmt="e4m3", out=None):
     _need_input(w)
     R, C = w.shape
     f = FP8_FMTS[fmt]
-    if out is None:
-        out = _fp8_buffers(R, C, "tile", w.device) + _fp8_buffers(C, R, "tile", w.device)
-    codes, scales, codes_t, scales_t = out
     dev = w.get_device()
-    _need_fp8(codes, scales, R, C, "tile", dev)
-    if codes_t is not None or scales_t is not None:
-        _need_fp8(codes_t, scales_t, C, R, "tile", dev, "_t")
+    if out is None:
+        codes, scales = _fp8_buffers(R, C, "tile", w.device)
+        codes_t, scales_t = _fp8_buffers(C, R, "tile", w.device)
+    else:
+        codes, scales, codes_t, scales_t = out
+        _need_fp8(codes, scales, R, C, "tile", dev)
+        if codes_t is not None or scales_t is not None:
+            _need_fp8(codes_t, scales_t, C, R, "tile", dev, "_t")
     _ok(mxq_fp8_quantize_tiles(w.data_ptr(), R, C, f, codes.data_ptr(), scales.data_ptr(),
                                _ptr(codes_t), _ptr(scales_t), _stream(dev)),
         "mxq_fp8_quantize_tiles")
@@ -659,13 +673,17 @@ def fp8_gemm(A, sA, B, sB, M, N, K, fmt_a="e4m3", fmt_b="e4m3", b_scales="tile",
     od = _out_code(out_dtype)
     fa, fb, bs = FP8_FMTS[fmt_a], FP8_FMTS[fmt_b], B_SCALES[b_scales]
     M, N, K = int(M), int(N), int(K)
-    _need(A, "A", torch.uint8, 0)
+    (m, pa), (ka, la) = fp8_shapes(M, K)
+    (n, pb), (kb, lb) = fp8_shapes(N, K, bs)
+    _need(A, "codes_A", torch.uint8, m * pa)
     dev = A.get_device()
-    _need_fp8(A, sA, M, K, "line", dev, "_A")
-    _need_fp8(B, sB, N, K, bs, dev, "_B")
+    _need(sA, "scales_A", torch.float32, ka * la, dev)
+    _need(B, "codes_B", torch.uint8, n * pb, dev)
+    _need(sB, "scales_B", torch.float32, kb * lb, dev)
     if out is None:
         out = torch.empty((M, N), dtype=out_dtype, device=A.device)
-    _need(out, "out", out_dtype, M * N, dev)
+    else:
+        _need(out, "out", out_dtype, M * N, dev)
     _ok(mxq_fp8_gemm(A.data_ptr(), sA.data_ptr(), fa, B.data_ptr(), sB.data_ptr(), fb, bs, M, N, K,
                      out.data_ptr(), od, _stream(dev)), "mxq_fp8_gemm")
     return out
@@ -673,27 +691,24 @@ def fp8_gemm(A, sA, B, sB, M, N, K, fmt_a="e4m3", fmt_b="e4m3", b_scales="tile",
 
 # ---- layer norm and RMS norm ---------------------------------------------------------
 
+_FLOAT_CODES = {torch.bfloat16: OUT_BF16, torch.float32: OUT_F32}
+
+
 def _need_norm(x, weight, bias):
     """x [rows, cols] and the vectors of its norm; returns (device index, code of
     x's dtype, code of weight's dtype)."""
     if not isinstance(x, torch.Tensor) or x.dim() != 2:
         raise ValueError("x must be a 2-D torch.Tensor [rows, cols]")
-    xd = _out_code_of(x, "x")
     _need(x, "x", None, 0)
     dev = x.get_device()
     _need(weight, "weight", None, x.shape[1], dev)
-    wd = _out_code_of(weight, "weight")
     if bias is not None:
         _need(bias, "bias", weight.dtype, x.shape[1], dev)
+    xd, wd = _FLOAT_CODES.get(x.dtype), _FLOAT_CODES.get(weight.dtype)
+    if xd is None or wd is None:
+        raise ValueError(f"x and weight must be torch.float32 or torch.bfloat16, got {x.dtype} "
+                         f"and {weight.dtype}")
     return dev, xd, wd
-
-
-def _out_code_of(t, name):
-    if t.dtype is torch.bfloat16:
-        return OUT_BF16
-    if t.dtype is torch.float32:
-        return OUT_F32
-    raise ValueError(f"{name} must be torch.float32 or torch.bfloat16, got {t.dtype}")
 
 
 def _norm_forward(x, weight, bias, eps, kind, fmt, with_y, out):
@@ -701,19 +716,27 @@ def _norm_forward(x, weight, bias, eps, kind, fmt, with_y, out):
     dev, xd, wd = _need_norm(x, weight, bias)
     R, C = x.shape
     y = codes = scales = None
+    f = 0
     if with_y:
-        y = torch.empty_like(x) if out is None else out
-        _need(y, "out", x.dtype, R * C, dev)
-    if fmt is not None:
-        codes, scales = _fp8_buffers(R, C, "line", x.device) if out is None else out
-        _need_fp8(codes, scales, R, C, "line", dev)
-        fmt = FP8_FMTS[fmt]
-    stats = torch.empty((2 if kind == NORM_LAYER else 1, R), dtype=torch.float32, device=x.device)
-    rstd = stats[0]
-    mean = stats[1] if kind == NORM_LAYER else None
-    a = NormArgs(x.data_ptr(), weight.data_ptr(), _ptr(bias), _ptr(y), _ptr(mean), rstd.data_ptr(),
-                 _ptr(codes), _ptr(scales), R, C, eps, kind, xd, wd, fmt or 0)
-    _ok(mxq_norm_forward(ctypes.addressof(a), _stream(dev)), "mxq_norm_forward")
+        if out is None:
+            y = torch.empty_like(x)
+        else:
+            y = out
+            _need(y, "out", x.dtype, R * C, dev)
+    else:
+        f = FP8_FMTS[fmt]
+        if out is None:
+            codes, scales = _fp8_buffers(R, C, "line", x.device)
+        else:
+            codes, scales = out
+            _need_fp8(codes, scales, R, C, "line", dev)
+    rstd = torch.empty(R, dtype=torch.float32, device=x.device)
+    mean = torch.empty_like(rstd) if kind == NORM_LAYER else None
+    a = _NORM_ARGS.pack(x.data_ptr(), weight.data_ptr(), 0 if bias is None else bias.data_ptr(),
+                        y.data_ptr() if with_y else 0, 0 if mean is None else mean.data_ptr(),
+                        rstd.data_ptr(), 0 if with_y else codes.data_ptr(),
+                        0 if with_y else scales.data_ptr(), R, C, eps, kind, xd, wd, f)
+    _ok(mxq_norm_forward(a, _stream(dev)), "mxq_norm_forward")
     return y, codes, scales, mean, rstd
 
 
@@ -745,6 +768,16 @@ def rms_norm_quantize(x: torch.Tensor, weight, eps=1e-5, fmt="e4m3", out=None):
     return codes, scales, rstd
 
 
+@functools.lru_cache(maxsize=4096)
+def _norm_backward_workspace(rows, cols):
+    return int(mxq_norm_backward_workspace_size(rows, cols))
+
+
+def norm_backward_workspace(rows, cols, device):
+    return torch.empty(max(_norm_backward_workspace(rows, cols), 256), dtype=torch.uint8,
+                       device=device)
+
+
 def _norm_backward(dy, x, weight, mean, rstd, kind, out, workspace):
     dev, xd, wd = _need_norm(x, weight, None)
     R, C = x.shape
@@ -752,25 +785,29 @@ def _norm_backward(dy, x, weight, mean, rstd, kind, out, workspace):
     _need(rstd, "rstd", torch.float32, R, dev)
     if kind == NORM_LAYER:
         _need(mean, "mean", torch.float32, R, dev)
-    dx = torch.empty_like(x) if out is None else out
-    _need(dx, "out", x.dtype, R * C, dev)
+    if out is None:
+        dx = torch.empty_like(x)
+    else:
+        dx = out
+        _need(dx, "out", x.dtype, R * C, dev)
     if workspace is None:
-        n = mxq_norm_backward_workspace_size(R, C)
-        workspace = torch.empty(max(int(n), 256), dtype=torch.uint8, device=x.device)
-    _need(workspace, "workspace", torch.uint8, 0, dev)   # its size is checked by the library
-    grads = torch.empty((2 if kind == NORM_LAYER else 1, C), dtype=torch.float32, device=x.device)
-    dw = grads[0]
-    db = grads[1] if kind == NORM_LAYER else None
-    a = NormGradArgs(dy.data_ptr(), x.data_ptr(), weight.data_ptr(), _ptr(mean), rstd.data_ptr(),
-                     dx.data_ptr(), dw.data_ptr(), _ptr(db), workspace.data_ptr(),
-                     workspace.numel(), R, C, kind, xd, wd)
-    _ok(mxq_norm_backward(ctypes.addressof(a), _stream(dev)), "mxq_norm_backward")
+        workspace = norm_backward_workspace(R, C, x.device)
+    else:
+        _need(workspace, "workspace", torch.uint8, 0, dev)   # its size is checked by the library
+    dw = torch.empty(C, dtype=torch.float32, device=x.device)
+    db = torch.empty_like(dw) if kind == NORM_LAYER else None
+    a = _NORM_GRAD_ARGS.pack(dy.data_ptr(), x.data_ptr(), weight.data_ptr(),
+                             0 if mean is None else mean.data_ptr(), rstd.data_ptr(),
+                             dx.data_ptr(), dw.data_ptr(), 0 if db is None else db.data_ptr(),
+                             workspace.data_ptr(), workspace.numel(), R, C, kind, xd, wd)
+    _ok(mxq_norm_backward(a, _stream(dev)), "mxq_norm_backward")
     return dx, dw, db
 
 
 def layer_norm_backward(dy, x, weight, mean, rstd, out=None, workspace=None):
     """Gradients of layer_norm from its statistics; returns (dx, dweight, dbias),
-    dx in x's dtype and the others in fp32."""
+    dx in x's dtype and the others in fp32.  workspace: as
+    norm_backward_workspace returns it, for callers that keep one."""
     return _norm_backward(dy, x, weight, mean, rstd, NORM_LAYER, out, workspace)
 
 

@@ -109,7 +109,7 @@ def test_norm_backward_refusals():
     odd = ODD.value
     assert mxq.mxq_norm_backward(None, None) == 1
     assert _grad_args(cols=0) == 0
-    for kw in (dict(rows=-1), dict(kind=5), dict(x_dtype=3), dict(dy=None), dict(x=None),
+    for kw in (dict(rows=-1), dict(kind=5), dict(kind=mxq.NORM_RMS), dict(x_dtype=3), dict(dy=None), dict(x=None),
                dict(weight=None), dict(mean=None), dict(rstd=None), dict(dx=None),
                dict(dweight=None), dict(workspace=None)):
         assert _grad_args(**kw) == 1, kw
@@ -138,6 +138,10 @@ def test_argument_structures_match_the_header(tmp_path, struct, name):
     got = subprocess.run([str(tmp_path / "layout")], capture_output=True, text=True, check=True)
     want = [ctypes.sizeof(struct)] + [getattr(struct, f).offset for f in fields]
     assert [int(v) for v in got.stdout.split()] == want
+    # the packed form the binding passes: the same bytes as the mirror's
+    packed = {"mxq_norm_args": mxq._NORM_ARGS, "mxq_norm_grad_args": mxq._NORM_GRAD_ARGS}[name]
+    values = list(range(1, len(fields) + 1))
+    assert packed.pack(*values) == bytes(struct(*values))
 
 
 # ---- the binding's buffer checks, against recorders in place of the library --------
