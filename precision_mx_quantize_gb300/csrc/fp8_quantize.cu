@@ -43,7 +43,7 @@ struct QArgs {
 MXQ_DEV uint32_t mag2(uint32_t w) { return w & 0x7FFF7FFFu; }
 
 template <int MODE, int FR, int FC>
-__global__ void __launch_bounds__(256) fp8_quant_kernel(const QArgs a) {
+__global__ void __launch_bounds__(256, MODE == Q_TILES ? 3 : 4) fp8_quant_kernel(const QArgs a) {
   constexpr bool ROW = MODE == Q_ROW || MODE == Q_DUAL;
   constexpr bool COL = MODE == Q_COL || MODE == Q_DUAL;
   constexpr bool TILES = MODE == Q_TILES;

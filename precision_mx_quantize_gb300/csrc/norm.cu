@@ -27,7 +27,8 @@ constexpr int N_MAX_WARPS = 32;
 
 // Eight consecutive elements of a row from `col` on, zero past its end.  vec:
 // the row's start is 16-byte aligned and cols % 8 == 0.
-MXQ_DEV void load8(const __nv_bfloat16* row, int64_t col, int64_t cols, bool vec, float (&f)[8]) {
+template <typename Ix>
+MXQ_DEV void load8(const __nv_bfloat16* row, Ix col, Ix cols, bool vec, float (&f)[8]) {
   if (vec) {
     const uint4 w = *reinterpret_cast<const uint4*>(row + col);
     f[0] = bf16lo(w.x); f[1] = bf16hi(w.x); f[2] = bf16lo(w.y); f[3] = bf16hi(w.y);
@@ -38,7 +39,8 @@ MXQ_DEV void load8(const __nv_bfloat16* row, int64_t col, int64_t cols, bool vec
   }
 }
 
-MXQ_DEV void load8(const float* row, int64_t col, int64_t cols, bool vec, float (&f)[8]) {
+template <typename Ix>
+MXQ_DEV void load8(const float* row, Ix col, Ix cols, bool vec, float (&f)[8]) {
   if (vec) {
     const float4 a = *reinterpret_cast<const float4*>(row + col);
     const float4 b = *reinterpret_cast<const float4*>(row + col + 4);
@@ -55,7 +57,8 @@ MXQ_DEV uint32_t pack_bf16(float a, float b) {
   return *reinterpret_cast<const uint32_t*>(&t);
 }
 
-MXQ_DEV void store8(__nv_bfloat16* row, int64_t col, int64_t cols, bool vec, const float (&f)[8]) {
+template <typename Ix>
+MXQ_DEV void store8(__nv_bfloat16* row, Ix col, Ix cols, bool vec, const float (&f)[8]) {
   if (vec) {
     *reinterpret_cast<uint4*>(row + col) =
         make_uint4(pack_bf16(f[0], f[1]), pack_bf16(f[2], f[3]), pack_bf16(f[4], f[5]),
@@ -67,7 +70,8 @@ MXQ_DEV void store8(__nv_bfloat16* row, int64_t col, int64_t cols, bool vec, con
   }
 }
 
-MXQ_DEV void store8(float* row, int64_t col, int64_t cols, bool vec, const float (&f)[8]) {
+template <typename Ix>
+MXQ_DEV void store8(float* row, Ix col, Ix cols, bool vec, const float (&f)[8]) {
   if (vec) {
     *reinterpret_cast<float4*>(row + col) = make_float4(f[0], f[1], f[2], f[3]);
     *reinterpret_cast<float4*>(row + col + 4) = make_float4(f[4], f[5], f[6], f[7]);
@@ -85,7 +89,7 @@ struct Raw8;
 template <>
 struct Raw8<__nv_bfloat16> {
   uint32_t w[4];
-  MXQ_DEV void load(const __nv_bfloat16* row, int64_t col, int64_t cols, bool vec) {
+  MXQ_DEV void load(const __nv_bfloat16* row, int col, int cols, bool vec) {
     w[0] = w[1] = w[2] = w[3] = 0u;
     if (col >= cols) return;
     if (vec) {
@@ -104,7 +108,7 @@ struct Raw8<__nv_bfloat16> {
 template <>
 struct Raw8<float> {
   float f[8];
-  MXQ_DEV void load(const float* row, int64_t col, int64_t cols, bool vec) {
+  MXQ_DEV void load(const float* row, int col, int cols, bool vec) {
     if (col < cols) {
       load8(row, col, cols, vec, f);
     } else {
@@ -243,7 +247,7 @@ __global__ void __launch_bounds__(256) norm_rows(const NArgs a) {
 template <typename XT, typename WT, bool LAYER, int FMT, bool WARP, int I>
 __global__ void __launch_bounds__(WARP ? 256 : 512) norm_regs(const NArgs a) {
   __shared__ float buf[WARP ? 1 : 2 * N_MAX_WARPS];
-  const int64_t cols = a.cols;
+  const int cols = static_cast<int>(a.cols);
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int64_t r = WARP ? int64_t(blockIdx.x) * 8 + warp : blockIdx.x;
   const int t = WARP ? lane : threadIdx.x, nt = WARP ? 32 : blockDim.x;
@@ -251,7 +255,7 @@ __global__ void __launch_bounds__(WARP ? 256 : 512) norm_regs(const NArgs a) {
   griddep_wait();
   griddep_launch_dependents();
   if (r >= a.rows) return;   // whole warps, and only where a warp has its own row
-  const XT* x = static_cast<const XT*>(a.x) + r * cols;
+  const XT* x = static_cast<const XT*>(a.x) + r * a.cols;
   Raw8<XT> raw[I];
   Raw8<WT> w[I], b[I];
 #pragma unroll
@@ -283,10 +287,15 @@ __global__ void __launch_bounds__(WARP ? 256 : 512) norm_regs(const NArgs a) {
   }
 #pragma unroll
   for (int i = 0; i < I; ++i) {
-    const int64_t c = 8 * (t + i * nt);
+    const int n = cols - 8 * (t + i * nt);   // elements of this chunk inside the row
+    if (n >= 8) {
 #pragma unroll
-    for (int j = 0; j < 8; ++j)
-      if (vec ? c < cols : c + j < cols) s += (raw[i][j] - mean) * (raw[i][j] - mean);
+      for (int j = 0; j < 8; ++j) s += (raw[i][j] - mean) * (raw[i][j] - mean);
+    } else {
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        if (j < n) s += (raw[i][j] - mean) * (raw[i][j] - mean);
+    }
   }
   const float rstd = 1.0f / sqrtf(row_sum(s, 1) * inv_n + a.eps);
   if (t == 0) {
@@ -295,23 +304,23 @@ __global__ void __launch_bounds__(WARP ? 256 : 512) norm_regs(const NArgs a) {
   }
 #pragma unroll
   for (int i = 0; i < I; ++i) {
-    const int64_t c = 8 * (t + i * nt);
-    if (8 * ((c >> 3) & ~int64_t(15)) >= cols) break;   // uniform over the 16 lanes of a block
+    const int c = 8 * (t + i * nt);
+    if ((c & ~127) >= cols) break;   // uniform over the 16 lanes of a block
     float f[8];
+    // weight and bias are zero past the row's end, and so is f
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
       f[j] = (raw[i][j] - mean) * rstd * w[i][j];
       if (LAYER && a.bias) f[j] += b[i][j];
-      if (vec ? c >= cols : c + j >= cols) f[j] = 0.0f;
     }
     if (a.y && c < cols && MXQ_IN_BOUNDS(r < a.rows, &g_err_norm, SITE_B_NORM))
-      store8(static_cast<XT*>(a.y) + r * cols, c, cols, vec, f);
+      store8(static_cast<XT*>(a.y) + r * a.cols, c, cols, vec, f);
     if constexpr (FMT >= 0) {
       float scale;
       const uint2 q = encode_block<FMT>(f, scale);
       if (c < a.pitch && MXQ_IN_BOUNDS(c + 8 <= a.pitch, &g_err_norm, SITE_B_NORM))
         *reinterpret_cast<uint2*>(a.codes + r * a.pitch + c) = q;
-      if (((c >> 3) & 15) == 0) store_scale(a, c >> 7, r, scale);
+      if ((c & 127) == 0) store_scale(a, c >> 7, r, scale);
     }
   }
 }
@@ -376,7 +385,7 @@ template <typename XT, typename WT, bool LAYER, bool WARP, int I>
 __global__ void __launch_bounds__(WARP ? 256 : 512) norm_grad_regs(const NGrad a) {
   extern __shared__ float sums[];          // WARP: [8][8 I 32] for the final join
   __shared__ float2 buf[WARP ? 1 : 2 * N_MAX_WARPS];
-  const int64_t cols = a.cols;
+  const int cols = static_cast<int>(a.cols);
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int t = WARP ? lane : threadIdx.x, nt = WARP ? 32 : blockDim.x;
   const int64_t first = WARP ? int64_t(blockIdx.x) * 8 + warp : blockIdx.x;
@@ -399,8 +408,8 @@ __global__ void __launch_bounds__(WARP ? 256 : 512) norm_grad_regs(const NGrad a
     if (r >= a.rows) return;
 #pragma unroll
     for (int i = 0; i < I; ++i) {
-      x[i].load(static_cast<const XT*>(a.x) + r * cols, 8 * (t + i * nt), cols, vec);
-      dy[i].load(static_cast<const XT*>(a.dy) + r * cols, 8 * (t + i * nt), cols, vec);
+      x[i].load(static_cast<const XT*>(a.x) + r * a.cols, 8 * (t + i * nt), cols, vec);
+      dy[i].load(static_cast<const XT*>(a.dy) + r * a.cols, 8 * (t + i * nt), cols, vec);
     }
     mean = LAYER ? a.mean[r] : 0.0f;
     rstd = a.rstd[r];
@@ -440,16 +449,16 @@ __global__ void __launch_bounds__(WARP ? 256 : 512) norm_grad_regs(const NGrad a
     const float c1 = LAYER ? s1 * inv_n : 0.0f, c2 = s2 * inv_n;
 #pragma unroll
     for (int i = 0; i < I; ++i) {
-      const int64_t c = 8 * (t + i * nt);
+      const int c = 8 * (t + i * nt);
       if (c >= cols) break;
       float f[8];
 #pragma unroll
       for (int j = 0; j < 8; ++j) f[j] = rs * (g[i][j] - c1 - h[i][j] * c2);
       if (MXQ_IN_BOUNDS(r < a.rows, &g_err_norm, SITE_B_NORM_GRAD))
-        store8(static_cast<XT*>(a.dx) + r * cols, c, cols, vec, f);
+        store8(static_cast<XT*>(a.dx) + r * a.cols, c, cols, vec, f);
     }
   }
-  float* part = a.part + int64_t(blockIdx.x) * 2 * cols;
+  float* part = a.part + int64_t(blockIdx.x) * 2 * a.cols;
   if constexpr (WARP) {
     // the eight warps' sums, in order
 #pragma unroll
@@ -467,14 +476,14 @@ __global__ void __launch_bounds__(WARP ? 256 : 512) norm_grad_regs(const NGrad a
 #pragma unroll
         for (int q = 0; q < 8; ++q) v += sums[q * 8 * I * 32 + e];
         // element e: lane e % 32, chunk and place e / 32
-        const int64_t c = 8 * ((e & 31) + (e >> 8) * 32) + ((e >> 5) & 7);
+        const int c = 8 * ((e & 31) + (e >> 8) * 32) + ((e >> 5) & 7);
         if (c < cols) part[k * cols + c] = v;
       }
     }
   } else {
 #pragma unroll
     for (int i = 0; i < I; ++i) {
-      const int64_t c = 8 * (t + i * nt);
+      const int c = 8 * (t + i * nt);
       if (c >= cols) break;
       store8(part, c, cols, cols % 4 == 0 && vec, dw[i]);
       if (LAYER) store8(part + cols, c, cols, cols % 4 == 0 && vec, db[i]);
