@@ -179,15 +179,16 @@ MXQ_DEV void arrive_remote_if(bool p, uint32_t cluster_bar) {
 constexpr int L_THREADS = 192;
 constexpr int L_WBYTES = 128 * 128;   // a stage's lines of B
 constexpr int L_MAX_SPLIT = 8;        // CTAs of a cluster that share a tile's K blocks
-constexpr int L_GROUP = 8;            // K blocks whose scales are loaded together
 
 template <int T>
 struct Lanes {
   static constexpr int NB = T == 128 ? 2 : 4;             // accumulators in tensor memory
   static constexpr uint32_t TMEM = NB * T;                // a power of two, at least 32
+  // K blocks whose scales are loaded together
+  static constexpr int GROUP = T == 128 ? 4 : 8;
   static constexpr int STAGE = L_WBYTES + T * 128;
   static constexpr int STAGES = T == 128 ? 3 : T == 64 ? 4 : 5;   // two CTAs fit in an SM
-  static constexpr int SMEM = STAGES * STAGE + 2 * L_GROUP * T * 4 + 256 + 1024;
+  static constexpr int SMEM = STAGES * STAGE + 2 * GROUP * T * 4 + 256 + 1024;
   static_assert(TMEM >= 32 && TMEM <= 256, "two CTAs share an SM's tensor memory");
   static_assert(STAGE % 1024 == 0 && 2 * (SMEM + 1024) <= 228 * 1024, "swizzle atoms, two CTAs");
   static_assert(T * 128 * 4 <= STAGES * STAGE, "partial sums fit in the ring");
@@ -204,12 +205,12 @@ __global__ void __launch_bounds__(L_THREADS, 2)
     fp8_gemm_lanes(const __grid_constant__ CUtensorMap ta, const __grid_constant__ CUtensorMap tb,
                    const FArgs a) {
   using L = Lanes<T>;
-  constexpr int S = L::STAGES, NB = L::NB;
+  constexpr int S = L::STAGES, NB = L::NB, G = L::GROUP;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~static_cast<uintptr_t>(1023));
-  float* sa = reinterpret_cast<float*>(smem + S * L::STAGE);   // [2][L_GROUP][T] scales of A
-  uint64_t* full = reinterpret_cast<uint64_t*>(sa + 2 * L_GROUP * T);
+  float* sa = reinterpret_cast<float*>(smem + S * L::STAGE);   // [2][G][T] scales of A
+  uint64_t* full = reinterpret_cast<uint64_t*>(sa + 2 * G * T);
   uint64_t* empty = full + S;
   uint64_t* acc_full = empty + S;
   uint64_t* acc_empty = acc_full + NB;
@@ -307,20 +308,20 @@ __global__ void __launch_bounds__(L_THREADS, 2)
     const int quad = warp & 3;                // tensor-memory lane quadrant
     const int et = threadIdx.x - 64;          // epilogue thread
     const int64_t n = n0 + quad * 32 + lane;  // this thread's line of B
-    // Scales come in groups of eight K blocks, loaded one group ahead (a load
+    // Scales come in groups of G K blocks, loaded one group ahead (a load
     // takes longer than the copy of a block): those of A through shared
     // memory, those of this thread's line of B in registers.
-    constexpr int NA = (L_GROUP * T + 127) / 128;
-    float next_a[NA], next_b[L_GROUP], sb[L_GROUP];
+    constexpr int NA = (G * T + 127) / 128;
+    float next_a[NA], next_b[G], sb[G];
     auto load = [&](int kb) {
 #pragma unroll
       for (int i = 0; i < NA; ++i) {
         const int e = et + 128 * i, k = kb + e / T;
         const int64_t m = m0 + e % T;
-        next_a[i] = e < L_GROUP * T && k < nk && m < a.M ? a.sA[(kb0 + k) * a.lines_a + m] : 0.0f;
+        next_a[i] = e < G * T && k < nk && m < a.M ? a.sA[(kb0 + k) * a.lines_a + m] : 0.0f;
       }
 #pragma unroll
-      for (int i = 0; i < L_GROUP; ++i) {
+      for (int i = 0; i < G; ++i) {
         const int64_t k = kb0 + kb + i;
         next_b[i] = 0.0f;
         if (kb + i < nk && n < a.N)
@@ -330,20 +331,20 @@ __global__ void __launch_bounds__(L_THREADS, 2)
 #pragma unroll
     for (int j = 0; j < T; ++j) acc[j] = 0.0f;
     load(0);
-    for (int g = 0; g < nk; g += L_GROUP) {
+    for (int g = 0; g < nk; g += G) {
       // two buffers and one barrier a group: a warp that stages group k + 2
       // has passed barrier k + 1, which every warp reached after its last read
       // of group k
-      float* buf = sa + ((g / L_GROUP) & 1) * L_GROUP * T;
+      float* buf = sa + ((g / G) & 1) * G * T;
 #pragma unroll
       for (int i = 0; i < NA; ++i)
-        if (et + 128 * i < L_GROUP * T) buf[et + 128 * i] = next_a[i];
+        if (et + 128 * i < G * T) buf[et + 128 * i] = next_a[i];
 #pragma unroll
-      for (int i = 0; i < L_GROUP; ++i) sb[i] = next_b[i];
-      load(g + L_GROUP);
+      for (int i = 0; i < G; ++i) sb[i] = next_b[i];
+      load(g + G);
       asm volatile("bar.sync 1, 128;" ::: "memory");
 #pragma unroll
-      for (int i = 0; i < L_GROUP; ++i) {
+      for (int i = 0; i < G; ++i) {
         const int kb = g + i, b = kb % NB;
         if (kb >= nk) break;
         fwait_or_abort(smem_u32(&acc_full[b]), (kb / NB) & 1, tmo, abort_flag, SITE_FP8_TMEM_FULL);

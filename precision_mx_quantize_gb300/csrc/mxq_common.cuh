@@ -36,6 +36,7 @@ enum : uint32_t {
   SITE_FP8_TMEM_EMPTY = 12,
   SITE_FP8_DRAIN = 13,
   SITE_FP8_SCALES = 14,
+  SITE_NORM_FULL = 15,
   // bounds checks of the bounds-checked build (MXQ_DEBUG_BOUNDS)
   SITE_B_QUANT_TILE = 16,    // quantizer tile coordinates
   SITE_B_QUANT_TMA = 17,     // quantizer TMA coordinate alignment

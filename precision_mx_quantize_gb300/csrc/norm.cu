@@ -24,6 +24,7 @@ __device__ uint32_t g_err_norm;
 namespace {
 
 constexpr int N_MAX_WARPS = 32;
+constexpr int N_MAX_SLOTS = 8;
 
 // Eight consecutive elements of a row from `col` on, zero past its end.  vec:
 // the row's start is 16-byte aligned and cols % 8 == 0.
@@ -338,6 +339,8 @@ struct NGrad {
   int64_t rows, cols;
   int32_t splits;
   int32_t vec;
+  int32_t slots;      // norm_grad_ring: rows in flight
+  uint64_t timeout_ns;
 };
 
 // dx of one row per CTA (rows of any length).
@@ -491,6 +494,136 @@ __global__ void __launch_bounds__(WARP ? 256 : 512) norm_grad_regs(const NGrad a
   }
 }
 
+// The same for rows that a CTA shares and whose starts are 16-byte aligned: the
+// rows come through a ring of a.slots pairs (x, dy) in shared memory, filled by
+// bulk copies a.slots rows ahead.  One row ahead in registers left each row
+// waiting for its loads (8192x4096 bf16, both kernels: 48 us against 39).
+template <typename XT, typename WT, bool LAYER, int I>
+__global__ void __launch_bounds__(512) norm_grad_ring(const NGrad a) {
+  extern __shared__ __align__(128) uint8_t ring[];
+  __shared__ __align__(8) uint64_t full[N_MAX_SLOTS];
+  __shared__ float buf[2][2][16];
+  const int cols = static_cast<int>(a.cols), nt = blockDim.x, t = threadIdx.x;
+  const int lane = t & 31, warp = t >> 5;
+  const float inv_n = 1.0f / static_cast<float>(cols);
+  const uint32_t row_bytes = cols * sizeof(XT), slot_bytes = 2 * row_bytes;
+  const int slots = a.slots;
+  if (t == 0) {
+    for (int i = 0; i < slots; ++i) mbar_init(smem_u32(&full[i]), 1);
+    fence_mbar_init();
+  }
+  __syncthreads();
+  griddep_wait();
+  griddep_launch_dependents();
+  auto fetch = [&](int64_t r, int slot) {   // one thread
+    if (r >= a.rows || !MXQ_IN_BOUNDS(slot < slots, &g_err_norm, SITE_B_NORM_GRAD)) return;
+    const uint32_t bar = smem_u32(&full[slot]), dst = smem_u32(ring) + slot * slot_bytes;
+    mbar_arrive_expect_tx(bar, slot_bytes);
+    bulk_load(dst, static_cast<const XT*>(a.x) + r * a.cols, row_bytes, bar);
+    bulk_load(dst + row_bytes, static_cast<const XT*>(a.dy) + r * a.cols, row_bytes, bar);
+  };
+  if (t == 0)
+    for (int i = 0; i < slots; ++i) fetch(blockIdx.x + int64_t(i) * gridDim.x, i);
+  float dw[I][8], db[I][8];
+#pragma unroll
+  for (int i = 0; i < I; ++i)
+#pragma unroll
+    for (int j = 0; j < 8; ++j) dw[i][j] = db[i][j] = 0.0f;
+  // The weight stays in registers where there is room, else comes from L1.
+  constexpr bool KEEP = I <= 2;
+  Raw8<WT> kept[KEEP ? I : 1];
+  auto weight = [&](int i) {
+    Raw8<WT> w;
+    w.load(static_cast<const WT*>(a.weight), 8 * (t + i * nt), cols, true);
+    return w;
+  };
+  if constexpr (KEEP) {
+#pragma unroll
+    for (int i = 0; i < I; ++i) kept[i] = weight(i);
+  }
+  int slot = 0, phase = 0, parity = 0;
+  bool ok = true;
+  float next_m = LAYER ? a.mean[blockIdx.x] : 0.0f, next_rs = a.rstd[blockIdx.x];
+  for (int64_t r = blockIdx.x; r < a.rows; r += gridDim.x, parity ^= 1) {
+    const float m = next_m, rs = next_rs;
+    if (r + gridDim.x < a.rows) {   // a row ahead: the load takes as long as a row
+      if (LAYER) next_m = a.mean[r + gridDim.x];
+      next_rs = a.rstd[r + gridDim.x];
+    }
+    if (ok && !mbar_wait(smem_u32(&full[slot]), phase, a.timeout_ns)) {
+      record_error(&g_err_norm, MXQ_ERR_TIMEOUT, SITE_NORM_FULL);
+      ok = false;   // the results are void; no further wait
+    }
+    const XT* x = reinterpret_cast<const XT*>(ring + slot * slot_bytes);
+    const XT* dy = x + cols;
+    float s1 = 0.0f, s2 = 0.0f;
+    // x and dy are kept as they lie in memory: two operations more per element
+    // below, but bf16 rows then take half the registers
+    Raw8<XT> xr[I], dr[I];
+#pragma unroll
+    for (int i = 0; i < I; ++i) {
+      xr[i].load(x, 8 * (t + i * nt), cols, true);
+      dr[i].load(dy, 8 * (t + i * nt), cols, true);
+      const Raw8<WT> w = KEEP ? kept[KEEP ? i : 0] : weight(i);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const float d = dr[i][j], h = (xr[i][j] - m) * rs, g = d * w[j];   // zero past the end
+        dw[i][j] += d * h;
+        db[i][j] += d;
+        s1 += g;
+        s2 += g * h;
+      }
+    }
+    // Both sums at once: lanes 0-15 of a warp take s1, lanes 16-31 s2.  Two
+    // buffers, one barrier a row: a warp writes row k + 2's sums after barrier
+    // k + 1, which every warp reached after reading row k's.
+    const bool hi = lane >= 16;
+    float v = hi ? s2 : s1;
+    v += __shfl_xor_sync(~0u, hi ? s1 : s2, 16);
+#pragma unroll
+    for (int d = 8; d; d >>= 1) v += __shfl_xor_sync(~0u, v, d);
+    if ((lane & 15) == 0) buf[parity][hi][warp] = v;
+    __syncthreads();   // and every thread has read the slot
+    if (t == 0) fetch(r + int64_t(slots) * gridDim.x, slot);
+    if (++slot == slots) { slot = 0; phase ^= 1; }
+    v = (lane & 15) < (nt >> 5) ? buf[parity][hi][lane & 15] : 0.0f;
+#pragma unroll
+    for (int d = 8; d; d >>= 1) v += __shfl_xor_sync(~0u, v, d);
+    const float c1 = LAYER ? __shfl_sync(~0u, v, 0) * inv_n : 0.0f;
+    const float c2 = __shfl_sync(~0u, v, 16) * inv_n;
+#pragma unroll
+    for (int i = 0; i < I; ++i) {
+      const int c = 8 * (t + i * nt);
+      if (c >= cols) break;
+      float f[8];
+      const Raw8<WT> w = KEEP ? kept[KEEP ? i : 0] : weight(i);
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        f[j] = rs * (dr[i][j] * w[j] - c1 - (xr[i][j] - m) * rs * c2);
+      if (MXQ_IN_BOUNDS(r < a.rows, &g_err_norm, SITE_B_NORM_GRAD))
+        store8(static_cast<XT*>(a.dx) + r * a.cols, c, cols, true, f);
+    }
+  }
+  if (!ok && t == 0) {   // the copies in flight land before shared memory is released
+    const uint64_t t0 = global_ns();
+    for (int i = 0; i < slots; ++i) {
+      const int64_t rounds = (a.rows - blockIdx.x + gridDim.x - 1) / gridDim.x;   // rows fetched
+      if (i >= rounds) break;
+      const int64_t last = (rounds - 1 - i) / slots;   // the slot's last phase
+      while (!mbar_try_wait(smem_u32(&full[i]), last & 1) && global_ns() - t0 < a.timeout_ns) {
+      }
+    }
+  }
+  float* part = a.part + int64_t(blockIdx.x) * 2 * a.cols;
+#pragma unroll
+  for (int i = 0; i < I; ++i) {
+    const int c = 8 * (t + i * nt);
+    if (c >= cols) break;
+    store8(part, c, cols, true, dw[i]);
+    if (LAYER) store8(part + cols, c, cols, true, db[i]);
+  }
+}
+
 // Partial sums of dw and db: a CTA takes 256 columns and every splits-th
 // group of rows, one column per thread.
 template <typename XT, bool LAYER>
@@ -511,8 +644,8 @@ __global__ void __launch_bounds__(256) norm_grad_cols(const NGrad a) {
   p[a.cols + c] = db;
 }
 
-// The partial sums of each column, in a fixed order: 32 columns a CTA, its
-// eight warps take every eighth split each and are added up in order.
+// The partial sums of each column, in a fixed order: 32 columns a CTA, its 32
+// warps take every 32nd split each and are added up in order.
 struct JoinArgs {
   const float* part;   // [splits][2][cols]
   int64_t cols;
@@ -521,8 +654,8 @@ struct JoinArgs {
   float* dbias;        // or null
 };
 
-__global__ void __launch_bounds__(256) norm_grad_join(const JoinArgs a) {
-  __shared__ float sums[2][8][32];
+__global__ void __launch_bounds__(1024) norm_grad_join(const JoinArgs a) {
+  __shared__ float sums[2][32][32];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int64_t cols = a.cols, c = int64_t(blockIdx.x) * 32 + lane;
   griddep_wait();
@@ -530,7 +663,7 @@ __global__ void __launch_bounds__(256) norm_grad_join(const JoinArgs a) {
   float dw = 0.0f, db = 0.0f;
   if (c < cols) {
 #pragma unroll 4
-    for (int s = warp; s < a.splits; s += 8) {
+    for (int s = warp; s < a.splits; s += 32) {
       const float* p = a.part + int64_t(s) * 2 * cols + c;
       dw += p[0];
       if (a.dbias) db += p[cols];
@@ -543,7 +676,7 @@ __global__ void __launch_bounds__(256) norm_grad_join(const JoinArgs a) {
     float* out = warp ? a.dbias : a.dweight;
     float v = 0.0f;
 #pragma unroll
-    for (int q = 0; q < 8; ++q) v += sums[warp][q][lane];
+    for (int q = 0; q < 32; ++q) v += sums[warp][q][lane];
     if (out && MXQ_IN_BOUNDS(c < cols, &g_err_norm, SITE_B_NORM_GRAD)) out[c] = v;
   }
 }
@@ -579,6 +712,17 @@ RowPlan backward_plan(int64_t cols, int x_dtype) {
   return {false, 256, 0};
 }
 
+int grad_ctas_per_sm(const RowPlan& p) { return std::max(1, (p.i == 1 ? 768 : 512) / p.nt); }
+
+// Rows in flight of a CTA of norm_grad_ring, 0 where it does not apply: the
+// shared memory of an SM (208 KB of it) split among its CTAs.
+int grad_slots(const RowPlan& p, int64_t cols, int x_dtype) {
+  const int64_t row = cols * (x_dtype == MXQ_OUT_BF16 ? 2 : 4);
+  if (p.warp || !p.i || cols % 8 != 0) return 0;
+  const int64_t fit = (208 * 1024 / grad_ctas_per_sm(p)) / (2 * row);
+  return fit < 2 ? 0 : static_cast<int>(std::min<int64_t>(fit, N_MAX_SLOTS));
+}
+
 // Sets of partial sums.  Register kernels: one per CTA, as many CTAs as the
 // registers let an SM hold at once (about 768, 512 and 512 threads with one,
 // two and four chunks each).  Longer rows: enough that the column sums fill the
@@ -586,8 +730,7 @@ RowPlan backward_plan(int64_t cols, int x_dtype) {
 int grad_splits(int64_t rows, int64_t cols, int x_dtype) {
   const RowPlan p = backward_plan(cols, x_dtype);
   if (p.i) {
-    const int per_sm = std::max(1, (p.i == 1 ? 768 : 512) / p.nt);
-    const int64_t want = int64_t(per_sm) * sm_count();
+    const int64_t want = int64_t(grad_ctas_per_sm(p)) * sm_count();
     return static_cast<int>(std::min<int64_t>(p.warp ? (rows + 7) / 8 : rows, want));
   }
   const int64_t want = std::max<int64_t>(1, 8 * sm_count() / ((cols + 255) / 256));
@@ -638,6 +781,14 @@ mxq_status run_forward(const NArgs& a, int fmt, cudaStream_t st) {
                          : launch_forward<XT, WT, LAYER, MXQ_E5M2>(a, st);
 }
 
+template <typename XT, typename WT, bool LAYER, int I>
+bool launch_ring(const NGrad& a, int nt, size_t smem, cudaStream_t st) {
+  return ensure_dynamic_smem(reinterpret_cast<const void*>(norm_grad_ring<XT, WT, LAYER, I>),
+                             static_cast<int>(smem)) &&
+         launch_early(norm_grad_ring<XT, WT, LAYER, I>, static_cast<unsigned>(a.splits), nt, smem,
+                      st, a);
+}
+
 template <typename XT, typename WT, bool LAYER>
 mxq_status run_backward(const NGrad& a, cudaStream_t st) {
   const RowPlan p = backward_plan(a.cols, std::is_same<XT, float>::value ? MXQ_OUT_F32
@@ -648,6 +799,12 @@ mxq_status run_backward(const NGrad& a, cudaStream_t st) {
     const size_t smem = size_t(8) * 8 * p.i * 32 * sizeof(float);
     ok = p.i == 1 ? launch_early(norm_grad_regs<XT, WT, LAYER, true, 1>, grid, 256, smem, st, a)
                   : launch_early(norm_grad_regs<XT, WT, LAYER, true, 2>, grid, 256, smem, st, a);
+  } else if (p.i && a.slots) {
+    const size_t smem = size_t(a.slots) * 2 * a.cols * sizeof(XT);
+    if (p.i == 1) ok = launch_ring<XT, WT, LAYER, 1>(a, p.nt, smem, st);
+    else if (p.i == 2) ok = launch_ring<XT, WT, LAYER, 2>(a, p.nt, smem, st);
+    else if constexpr (std::is_same<XT, __nv_bfloat16>::value)
+      ok = launch_ring<XT, WT, LAYER, 4>(a, p.nt, smem, st);
   } else if (p.i) {
     if (p.i == 1) ok = launch_early(norm_grad_regs<XT, WT, LAYER, false, 1>, grid, p.nt, 0, st, a);
     else if (p.i == 2)
@@ -661,7 +818,7 @@ mxq_status run_backward(const NGrad& a, cudaStream_t st) {
   }
   if (!ok) return MXQ_ERR_CUDA;
   const JoinArgs j{a.part, a.cols, a.splits, a.dweight, a.dbias};
-  ok = launch_early(norm_grad_join, static_cast<unsigned>((a.cols + 31) / 32), 256, 0, st, j);
+  ok = launch_early(norm_grad_join, static_cast<unsigned>((a.cols + 31) / 32), 1024, 0, st, j);
   return ok ? launch_status() : MXQ_ERR_CUDA;
 }
 
@@ -797,5 +954,7 @@ extern "C" mxq_status mxq_norm_backward(const mxq_norm_grad_args* p, void* strea
   a.cols = p->cols;
   a.splits = grad_splits(p->rows, p->cols, p->x_dtype);
   a.vec = p->cols % 8 == 0;
+  a.slots = grad_slots(backward_plan(p->cols, p->x_dtype), p->cols, p->x_dtype);
+  a.timeout_ns = wait_timeout_ns();
   return dispatch(p->x_dtype, p->w_dtype, p->kind, Backward{a, s});
 }
