@@ -182,12 +182,12 @@ constexpr int L_MAX_SPLIT = 8;        // CTAs of a cluster that share a tile's K
 
 template <int T>
 struct Lanes {
-  static constexpr int NB = T == 128 ? 2 : 4;             // accumulators in tensor memory
+  static constexpr int NB = 4;                            // accumulators in tensor memory
   static constexpr uint32_t TMEM = NB * T;                // a power of two, at least 32
   // K blocks whose scales are loaded together
-  static constexpr int GROUP = T == 128 ? 4 : 8;
+  static constexpr int GROUP = 8;
   static constexpr int STAGE = L_WBYTES + T * 128;
-  static constexpr int STAGES = T == 128 ? 3 : T == 64 ? 4 : 5;   // two CTAs fit in an SM
+  static constexpr int STAGES = T == 64 ? 4 : 5;          // two CTAs fit in an SM
   static constexpr int SMEM = STAGES * STAGE + 2 * GROUP * T * 4 + 256 + 1024;
   static_assert(TMEM >= 32 && TMEM <= 256, "two CTAs share an SM's tensor memory");
   static_assert(STAGE % 1024 == 0 && 2 * (SMEM + 1024) <= 228 * 1024, "swizzle atoms, two CTAs");
@@ -569,17 +569,33 @@ MXQ_DEV void stage_out(const float (&acc)[128], uint32_t out, int quad, int lane
   }
 }
 
-// A half tile straight from the registers, element by element (rows of C that
-// no tensor map can describe).
-template <bool LINES>
-MXQ_DEV void store_out(const FArgs& a, const float (&acc)[128], int64_t row0, int64_t col0,
-                       int lane) {
+// Copies a staged pass out to rows of C that no tensor map can describe (not
+// 16-byte multiples): each warp its 32 rows, neighbouring lanes neighbouring
+// columns.  bf16 goes in pairs where N is even.
+MXQ_DEV void copy_out(const FArgs& a, uint32_t out, int quad, int lane, int64_t row0, int64_t col0,
+                      bool bf16) {
+  const bool pairs = bf16 && a.N % 2 == 0;
+  const int per = pairs ? 2 : 1, steps = bf16 && !pairs ? 4 : 2, shift = bf16 ? 1 : 2;
+#pragma unroll 4
+  for (int i = 0; i < 32; ++i) {
+    const int r = quad * 32 + i;
+    const int64_t to = (row0 + r) * a.N + col0;
 #pragma unroll
-  for (int j = 0; j < 128; ++j) {
-    const int64_t row = row0 + acc_row<LINES>(j, lane), col = col0 + acc_col<LINES>(j, lane);
-    if (row >= a.M || col >= a.N) continue;
-    if (a.out_bf16) static_cast<__nv_bfloat16*>(a.C)[row * a.N + col] = __float2bfloat16_rn(acc[j]);
-    else static_cast<float*>(a.C)[row * a.N + col] = acc[j];
+    for (int k = 0; k < 4; ++k) {
+      const int c = (k * 32 + lane) * per, byte = c << shift;
+      if (k >= steps || row0 + r >= a.M || col0 + c >= a.N) continue;
+      const uint32_t at = out + (byte >> 7) * 16384 + r * 128 + ((byte & 127) ^ ((r & 7) << 4));
+      if (bf16 && !pairs) {
+        uint16_t v;
+        asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v) : "r"(at));
+        static_cast<uint16_t*>(a.C)[to + c] = v;
+      } else {
+        uint32_t v;
+        asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(at));
+        if (bf16) *reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(a.C) + to + c) = v;
+        else static_cast<uint32_t*>(a.C)[to + c] = v;
+      }
+    }
   }
 }
 
@@ -872,30 +888,28 @@ __global__ void __launch_bounds__(P_THREADS, 1)
       tile_coords(t, p, mp, nt);
       const int row0 = (mp * 2 + static_cast<int>(rank)) * 128, col0 = nt * 256 + h * 128;
       if (!MXQ_IN_BOUNDS(mp < p.n_mp && nt < p.n_nt, &g_err_fp8_gemm, SITE_B_FP8_GEMM)) continue;
-      if (p.tma_out) {
-        // The half tile goes through shared memory and leaves by TMA, under
-        // the next tile's K loop: stored from the registers it took as long as
-        // three K blocks, and the MMAs only run two ahead.
-        const bool bf16 = a.out_bf16 != 0;
-        const uint32_t mine = smem_u32(out) + h * 32768;
-        const bool first = threadIdx.x % 128 == 0;   // issues and tracks the copies
+      // The half tile goes through shared memory and leaves by TMA, under the
+      // next tile's K loop: stored from the registers it took as long as three
+      // K blocks, and the MMAs only run two ahead.
+      const bool bf16 = a.out_bf16 != 0;
+      const uint32_t mine = smem_u32(out) + h * 32768;
+      const bool first = threadIdx.x % 128 == 0;   // issues and tracks the copies
 #pragma unroll
-        for (int pass = 0; pass < 2; ++pass) {
-          if (pass && bf16) break;
-          if (first) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
-          asm volatile("bar.sync %0, 128;" ::"r"(1 + h) : "memory");
-          stage_out<LINES>(acc, mine, quad, lane, bf16, pass);
-          asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-          asm volatile("bar.sync %0, 128;" ::"r"(1 + h) : "memory");
-          if (first && row0 < a.M) {
-            const int wide = bf16 ? 64 : 32, x = col0 + (bf16 ? 0 : 64 * pass);
-            if (x < a.N) tma_store_2d(&tc, mine, x, row0);
-            if (x + wide < a.N) tma_store_2d(&tc, mine + 16384, x + wide, row0);
-            asm volatile("cp.async.bulk.commit_group;" ::: "memory");
-          }
+      for (int pass = 0; pass < 2; ++pass) {
+        if (pass && bf16) break;
+        if (first) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+        asm volatile("bar.sync %0, 128;" ::"r"(1 + h) : "memory");
+        stage_out<LINES>(acc, mine, quad, lane, bf16, pass);
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        asm volatile("bar.sync %0, 128;" ::"r"(1 + h) : "memory");
+        const int wide = bf16 ? 64 : 32, x = col0 + 64 * pass;
+        if (!p.tma_out) {
+          copy_out(a, mine, quad, lane, row0, x, bf16);
+        } else if (first && row0 < a.M) {
+          if (x < a.N) tma_store_2d(&tc, mine, x, row0);
+          if (x + wide < a.N) tma_store_2d(&tc, mine + 16384, x + wide, row0);
+          asm volatile("cp.async.bulk.commit_group;" ::: "memory");
         }
-      } else {
-        store_out<LINES>(a, acc, row0 + quad * 32, col0, lane);
       }
     }
     if (threadIdx.x % 128 == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
@@ -943,16 +957,39 @@ bool code_map(CUtensorMap* map, const void* codes, int64_t lines, int64_t K, int
                        CU_TENSOR_MAP_L2_PROMOTION_L2_256B) == CUDA_SUCCESS;
 }
 
-// CTAs that share the K blocks of a tile.  A CTA streams its lines of B no
-// faster than its few copies in flight allow, and a product of few tokens has
-// few tiles: splitting K until two CTAs sit on every SM, as long as each keeps
-// four blocks, fills the machine (1x4096x14336: FIXME).
+// CTAs that share the K blocks of a tile: as many as leave the grid one wave
+// (two CTAs an SM) and each of them six blocks.  A tile alone streams its
+// lines of B no faster than one CTA's copies; past one wave or with fewer
+// blocks the joins cost more.  Measured at 1, 2, 4 and 8 CTAs: 1x4096x4096 8.6,
+// 5.7, 4.1, 4.6 us, 1x4096x14336 26, 15.7, 12.0, 11.6 us, 16x6144x4096 9.1, 7.6,
+// 6.3, 8.5 us.
 uint32_t lanes_split(int64_t tiles, int nk) {
   uint32_t split = 1;
-  while (split < L_MAX_SPLIT && tiles * split < 2 * sm_count() &&
-         nk >= static_cast<int>(8 * split))
+  while (split < L_MAX_SPLIT && tiles * 2 * split <= 2 * sm_count() &&
+         nk >= static_cast<int>(12 * split))
     split *= 2;
   return split;
+}
+
+int lanes_tokens(int64_t M) { return M <= 16 ? 16 : M <= 32 ? 32 : 64; }
+
+// Which kernel: modeled times in microseconds, fitted to measurements -- a K
+// block takes 0.45 us on a CTA pair, 0.85 or (up to 32 tokens) 0.55 us with two
+// few-token CTAs an SM, a join 3 us, a tile whose rows of C no TMA store takes
+// 5 us.  Lanes against pairs, measured: 64x28672x4096 24 and 33 us, 128x4096x4096
+// 12 and 16, 256x4096x4096 19 and 16, 512x4096x4096 21 and 17, 1024x1024x1024 7.6
+// and 7.6, 2048x2048x2048 25 and 12.
+bool pairs_win(int64_t M, int64_t N, int nk, bool tma_out) {
+  const int64_t sms = sm_count(), t = lanes_tokens(M);
+  const int64_t pair_tiles = ((M + 255) / 256) * ((N + 255) / 256);
+  const int64_t lane_tiles = ((M + t - 1) / t) * ((N + 127) / 128);
+  const uint32_t split = lanes_split(lane_tiles, nk);
+  const double pair_waves = std::ceil(pair_tiles / double(sms / 2));
+  const double lane_waves = std::ceil(lane_tiles * split / double(2 * sms));
+  const double pair_us = 1.0 + pair_waves * ((tma_out ? 1.0 : 6.0) + 0.45 * nk);
+  const double lane_us = (split > 1 ? 3.0 : 0.0) +
+                         lane_waves * (0.5 + (t == 64 ? 0.85 : 0.55) * nk / split);
+  return pair_us < lane_us;
 }
 
 template <int T>
@@ -1088,16 +1125,16 @@ extern "C" mxq_status mxq_fp8_gemm(const void* A, const float* sA, int fmt_a, co
   a.out_bf16 = out_dtype == MXQ_OUT_BF16;
   a.timeout_ns = wait_timeout_ns();
   const uint32_t e5a = fmt_a == MXQ_E5M2, e5b = fmt_b == MXQ_E5M2;
-  const int64_t tiles = ((M + 255) / 256) * ((N + 255) / 256);
-  if (M > 128 && tiles >= 24) {
+  if (pairs_win(M, N, a.nk, N * (a.out_bf16 ? 2 : 4) % 16 == 0)) {
     const uint32_t types = e5a << 7 | e5b << 10;
     return a.tiles ? launch_pair<false>(A, B, K, a, types, stream)
                    : launch_pair<true>(A, B, K, a, types, stream);
   }
   // the lines of B are the MMA's rows (its A operand)
   a.idesc_fmt = e5b << 7 | e5a << 10;
-  if (M <= 16) return launch_lanes<16>(A, B, K, a, stream);
-  if (M <= 32) return launch_lanes<32>(A, B, K, a, stream);
-  if (M <= 64) return launch_lanes<64>(A, B, K, a, stream);
-  return launch_lanes<128>(A, B, K, a, stream);
+  switch (lanes_tokens(M)) {
+    case 16: return launch_lanes<16>(A, B, K, a, stream);
+    case 32: return launch_lanes<32>(A, B, K, a, stream);
+    default: return launch_lanes<64>(A, B, K, a, stream);
+  }
 }
