@@ -62,6 +62,26 @@ inline int64_t fp8_lines(int64_t lines) { return (lines + 3) / 4 * 4; }
 
 inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
+// A launch that may start while the previous kernel on the stream drains; the
+// kernels wait for it before their first global access.
+template <typename K, typename... A>
+bool launch_early(K kernel, unsigned grid, int threads, size_t smem, cudaStream_t st,
+                  const A&... args) {
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.gridDim = dim3(grid, 1, 1);
+  cfg.blockDim = dim3(static_cast<unsigned>(threads), 1, 1);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  if (cudaLaunchKernelEx(&cfg, kernel, args...) == cudaSuccess) return true;
+  cudaGetLastError();
+  return false;
+}
+
 inline bool is_fp8(int fmt) { return fmt == MXQ_E4M3 || fmt == MXQ_E5M2; }
 
 inline mxq_status launch_status() {

@@ -138,22 +138,16 @@ MXQ_DEV float cta_sum(float v, float* buf) {
   return s;
 }
 
-// Codes of the eight values a lane holds of a 128-element block that 16
-// neighbouring lanes share, and the block's scale.
-template <int FMT>
-MXQ_DEV uint2 encode_block(const float (&f)[8], float& scale) {
-  float m = fabsf(f[0]);
-#pragma unroll
-  for (int j = 1; j < 7; j += 2) m = max3_abs_nan(m, f[j], f[j + 1]);
-  m = max3_abs_nan(m, f[7], f[7]);
-#pragma unroll
-  for (int d = 8; d; d >>= 1) {
-    const float o = __shfl_xor_sync(~0u, m, d);
-    m = max3_abs_nan(m, o, o);
+// After a wait ran out: waits (bounded) until the copies of a ring that serves
+// every grid-th row have landed, so that shared memory can be released.
+MXQ_DEV void drain_ring(uint64_t* full, int slots, int64_t rows, uint64_t limit_ns) {
+  const int64_t fetched = (rows - blockIdx.x + gridDim.x - 1) / gridDim.x;
+  const uint64_t t0 = global_ns();
+  for (int i = 0; i < slots && i < fetched; ++i) {
+    const int64_t last = (fetched - 1 - i) / slots;   // the slot's last phase
+    while (!mbar_try_wait(smem_u32(&full[i]), last & 1) && global_ns() - t0 < limit_ns) {
+    }
   }
-  float mul;
-  fp8_scale<FMT>(m, scale, mul);
-  return fp8_encode8<FMT>(f, mul);
 }
 
 struct NArgs {
@@ -168,6 +162,8 @@ struct NArgs {
   int64_t rows, cols, pitch, lines;
   float eps;
   int32_t vec;
+  int32_t slots;      // norm_ring: rows in flight
+  uint64_t timeout_ns;
 };
 
 // The scale of block kb of row r; the last row also writes those of the
@@ -179,12 +175,48 @@ MXQ_DEV void store_scale(const NArgs& a, int64_t kb, int64_t r, float scale) {
     for (int64_t l = a.rows; l < a.lines; ++l) s[l] = F_TINY;
 }
 
+// Codes and scales of the I chunks of eight values that a lane holds of row r,
+// chunk i at column c0 + i * step (a multiple of 128): 16 neighbouring lanes
+// share a block.  The two divisions of a block's scale cost as much as the rest
+// of its codes, so of the I blocks each lane works out one.
+template <int FMT, int I>
+MXQ_DEV void encode_chunks(const NArgs& a, int64_t r, int64_t c0, int64_t step,
+                           const float (&f)[I][8]) {
+  const int lane = threadIdx.x & 31, which = lane & (I - 1);
+  float own = 0.0f;
+#pragma unroll
+  for (int i = 0; i < I; ++i) {
+    float m = fabsf(f[i][0]);
+#pragma unroll
+    for (int j = 1; j < 7; j += 2) m = max3_abs_nan(m, f[i][j], f[i][j + 1]);
+    m = max3_abs_nan(m, f[i][7], f[i][7]);
+#pragma unroll
+    for (int d = 8; d; d >>= 1) {
+      const float o = __shfl_xor_sync(~0u, m, d);
+      m = max3_abs_nan(m, o, o);
+    }
+    if (i == which) own = m;
+  }
+  float scale, mul;
+  fp8_scale<FMT>(own, scale, mul);
+  const int64_t block = (c0 + which * step) >> 7;
+  if ((lane & 15) < I && block * 128 < a.cols) store_scale(a, block, r, scale);
+#pragma unroll
+  for (int i = 0; i < I; ++i) {
+    const float k = __shfl_sync(~0u, mul, (lane & 16) + i);
+    const int64_t c = c0 + i * step;
+    const uint2 q = fp8_encode8<FMT>(f[i], k);
+    if (c < a.pitch && MXQ_IN_BOUNDS(c + 8 <= a.pitch, &g_err_norm, SITE_B_NORM))
+      *reinterpret_cast<uint2*>(a.codes + r * a.pitch + c) = q;
+  }
+}
+
 // One CTA per row, reading the row again for each pass (rows of any length).
 template <typename XT, typename WT, bool LAYER, int FMT>
 __global__ void __launch_bounds__(256) norm_rows(const NArgs a) {
   __shared__ float buf[N_MAX_WARPS];
   const int64_t r = blockIdx.x, cols = a.cols;
-  const int64_t n_chunks = (cols + 7) / 8, n_pad = (n_chunks + 15) / 16 * 16;
+  const int64_t n_chunks = (cols + 7) / 8;
   griddep_wait();
   griddep_launch_dependents();
   const XT* x = static_cast<const XT*>(a.x) + r * cols;
@@ -214,7 +246,8 @@ __global__ void __launch_bounds__(256) norm_rows(const NArgs a) {
     if (LAYER && a.mean) a.mean[r] = mean;
     if (a.rstd) a.rstd[r] = rstd;
   }
-  for (int64_t c = threadIdx.x; c < n_pad; c += blockDim.x) {
+  const int64_t n_all = (n_chunks + 31) / 32 * 32;   // whole warps
+  for (int64_t c = threadIdx.x; c < n_all; c += blockDim.x) {
     float wf[8], bf[8];
 #pragma unroll
     for (int j = 0; j < 8; ++j) f[j] = wf[j] = bf[j] = 0.0f;
@@ -230,11 +263,10 @@ __global__ void __launch_bounds__(256) norm_rows(const NArgs a) {
       if (a.y) store8(static_cast<XT*>(a.y) + r * cols, 8 * c, cols, vec, f);
     }
     if constexpr (FMT >= 0) {
-      float scale;
-      const uint2 q = encode_block<FMT>(f, scale);
-      if (8 * c < a.pitch)
-        *reinterpret_cast<uint2*>(a.codes + r * a.pitch + 8 * c) = q;
-      if ((c & 15) == 0) store_scale(a, c >> 4, r, scale);
+      float chunk[1][8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) chunk[0][j] = f[j];
+      encode_chunks<FMT, 1>(a, r, 8 * c, 0, chunk);
     }
   }
 }
@@ -303,27 +335,121 @@ __global__ void __launch_bounds__(WARP ? 256 : 512) norm_regs(const NArgs a) {
     if (LAYER && a.mean) a.mean[r] = mean;
     if (a.rstd) a.rstd[r] = rstd;
   }
+  float f[I][8];
 #pragma unroll
   for (int i = 0; i < I; ++i) {
     const int c = 8 * (t + i * nt);
-    if ((c & ~127) >= cols) break;   // uniform over the 16 lanes of a block
-    float f[8];
     // weight and bias are zero past the row's end, and so is f
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
-      f[j] = (raw[i][j] - mean) * rstd * w[i][j];
-      if (LAYER && a.bias) f[j] += b[i][j];
+      f[i][j] = (raw[i][j] - mean) * rstd * w[i][j];
+      if (LAYER && a.bias) f[i][j] += b[i][j];
     }
     if (a.y && c < cols && MXQ_IN_BOUNDS(r < a.rows, &g_err_norm, SITE_B_NORM))
-      store8(static_cast<XT*>(a.y) + r * a.cols, c, cols, vec, f);
-    if constexpr (FMT >= 0) {
-      float scale;
-      const uint2 q = encode_block<FMT>(f, scale);
-      if (c < a.pitch && MXQ_IN_BOUNDS(c + 8 <= a.pitch, &g_err_norm, SITE_B_NORM))
-        *reinterpret_cast<uint2*>(a.codes + r * a.pitch + c) = q;
-      if ((c & 127) == 0) store_scale(a, c >> 7, r, scale);
-    }
+      store8(static_cast<XT*>(a.y) + r * a.cols, c, cols, vec, f[i]);
   }
+  if constexpr (FMT >= 0) encode_chunks<FMT, I>(a, r, 8 * t, 8 * nt, f);
+}
+
+// The same for many rows whose starts are 16-byte aligned: persistent CTAs keep
+// their columns' weight and bias in registers, and the rows come through a
+// ring in shared memory, filled by bulk copies a.slots rows ahead.  With a CTA
+// for every row, loads fill a third of its life and the memory waits for the
+// rest (8192x4096 bf16, layer norm: 34.6 us against 24.7).
+template <typename XT, typename WT, bool LAYER, int FMT, int I>
+__global__ void __launch_bounds__(512) norm_ring(const NArgs a) {
+  extern __shared__ __align__(128) uint8_t ring[];
+  __shared__ __align__(8) uint64_t full[N_MAX_SLOTS];
+  __shared__ float buf[2][2][16];
+  const int cols = static_cast<int>(a.cols), nt = blockDim.x, t = threadIdx.x;
+  const int lane = t & 31, warp = t >> 5;
+  const float inv_n = 1.0f / static_cast<float>(cols);
+  const uint32_t row_bytes = cols * sizeof(XT);
+  const int slots = a.slots;
+  if (t == 0) {
+    for (int i = 0; i < slots; ++i) mbar_init(smem_u32(&full[i]), 1);
+    fence_mbar_init();
+  }
+  __syncthreads();
+  griddep_wait();
+  griddep_launch_dependents();
+  auto fetch = [&](int64_t r, int slot) {   // one thread
+    if (r >= a.rows || !MXQ_IN_BOUNDS(slot < slots, &g_err_norm, SITE_B_NORM)) return;
+    const uint32_t bar = smem_u32(&full[slot]);
+    mbar_arrive_expect_tx(bar, row_bytes);
+    bulk_load(smem_u32(ring) + slot * row_bytes, static_cast<const XT*>(a.x) + r * a.cols,
+              row_bytes, bar);
+  };
+  if (t == 0)
+    for (int i = 0; i < slots; ++i) fetch(blockIdx.x + int64_t(i) * gridDim.x, i);
+  Raw8<WT> w[I], b[I];
+#pragma unroll
+  for (int i = 0; i < I; ++i) {
+    w[i].load(static_cast<const WT*>(a.weight), 8 * (t + i * nt), cols, true);
+    if (LAYER && a.bias) b[i].load(static_cast<const WT*>(a.bias), 8 * (t + i * nt), cols, true);
+  }
+  int slot = 0, phase = 0, parity = 0;
+  bool ok = true;
+  for (int64_t r = blockIdx.x; r < a.rows; r += gridDim.x, parity ^= 1) {
+    if (ok && !mbar_wait(smem_u32(&full[slot]), phase, a.timeout_ns)) {
+      record_error(&g_err_norm, MXQ_ERR_TIMEOUT, SITE_NORM_FULL);
+      ok = false;   // the results are void; no further wait
+    }
+    const XT* x = reinterpret_cast<const XT*>(ring + slot * row_bytes);
+    Raw8<XT> raw[I];
+#pragma unroll
+    for (int i = 0; i < I; ++i) raw[i].load(x, 8 * (t + i * nt), cols, true);
+    // Sum over the row.  Each of a row's sums has its own buffer, and rows take
+    // them in turn: a warp writes row k + 2's after a barrier of row k + 1,
+    // which every warp reached after reading row k's.
+    auto row_sum = [&](float v, int part) {
+      v = warp_sum(v);
+      if (lane == 0) buf[parity][part][warp] = v;
+      __syncthreads();
+      v = (lane & 15) < (nt >> 5) ? buf[parity][part][lane & 15] : 0.0f;
+#pragma unroll
+      for (int d = 8; d; d >>= 1) v += __shfl_xor_sync(~0u, v, d);
+      return v;
+    };
+    float mean = 0.0f, s = 0.0f;
+    if constexpr (LAYER) {
+#pragma unroll
+      for (int i = 0; i < I; ++i)
+#pragma unroll
+        for (int j = 0; j < 8; ++j) s += raw[i][j];   // zero past the row's end
+      mean = row_sum(s, 0) * inv_n;
+      s = 0.0f;
+    }
+#pragma unroll
+    for (int i = 0; i < I; ++i) {
+      if (8 * (t + i * nt) >= cols) break;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) s += (raw[i][j] - mean) * (raw[i][j] - mean);
+    }
+    const float rstd = 1.0f / sqrtf(row_sum(s, 1) * inv_n + a.eps);
+    // past a barrier: every thread has read the slot
+    if (t == 0) {
+      fetch(r + int64_t(slots) * gridDim.x, slot);
+      if (LAYER && a.mean) a.mean[r] = mean;
+      if (a.rstd) a.rstd[r] = rstd;
+    }
+    if (++slot == slots) { slot = 0; phase ^= 1; }
+    float f[I][8];
+#pragma unroll
+    for (int i = 0; i < I; ++i) {
+      const int c = 8 * (t + i * nt);
+      // weight and bias are zero past the row's end, and so is f
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        f[i][j] = (raw[i][j] - mean) * rstd * w[i][j];
+        if (LAYER && a.bias) f[i][j] += b[i][j];
+      }
+      if (a.y && c < cols && MXQ_IN_BOUNDS(r < a.rows, &g_err_norm, SITE_B_NORM))
+        store8(static_cast<XT*>(a.y) + r * a.cols, c, cols, true, f[i]);
+    }
+    if constexpr (FMT >= 0) encode_chunks<FMT, I>(a, r, 8 * t, 8 * nt, f);
+  }
+  if (!ok && t == 0) drain_ring(full, slots, a.rows, a.timeout_ns);
 }
 
 struct NGrad {
@@ -524,11 +650,23 @@ __global__ void __launch_bounds__(512) norm_grad_ring(const NGrad a) {
   };
   if (t == 0)
     for (int i = 0; i < slots; ++i) fetch(blockIdx.x + int64_t(i) * gridDim.x, i);
-  float dw[I][8], db[I][8];
+  // With four chunks a thread the sums of db do not fit the registers: they
+  // stay in shared memory, behind the ring, eight floats a thread and chunk as
+  // two planes of float4 (4096x14336 bf16: 146 us spilled, 82 so).
+  constexpr bool DB_SHARED = LAYER && I == 4;
+  float4* db_at = reinterpret_cast<float4*>(ring + slots * slot_bytes) + t;
+  float dw[I][8], db[DB_SHARED ? 1 : I][8];
 #pragma unroll
-  for (int i = 0; i < I; ++i)
+  for (int i = 0; i < I; ++i) {
 #pragma unroll
-    for (int j = 0; j < 8; ++j) dw[i][j] = db[i][j] = 0.0f;
+    for (int j = 0; j < 8; ++j) dw[i][j] = 0.0f;
+    if constexpr (DB_SHARED) {
+      db_at[2 * i * nt] = db_at[(2 * i + 1) * nt] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    } else {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) db[i][j] = 0.0f;
+    }
+  }
   // The weight stays in registers where there is room, else comes from L1.
   constexpr bool KEEP = I <= 2;
   Raw8<WT> kept[KEEP ? I : 1];
@@ -569,9 +707,16 @@ __global__ void __launch_bounds__(512) norm_grad_ring(const NGrad a) {
       for (int j = 0; j < 8; ++j) {
         const float d = dr[i][j], h = (xr[i][j] - m) * rs, g = d * w[j];   // zero past the end
         dw[i][j] += d * h;
-        db[i][j] += d;
+        if constexpr (!DB_SHARED) db[i][j] += d;
         s1 += g;
         s2 += g * h;
+      }
+      if constexpr (DB_SHARED) {
+        float4 lo = db_at[2 * i * nt], hi = db_at[(2 * i + 1) * nt];
+        lo.x += dr[i][0]; lo.y += dr[i][1]; lo.z += dr[i][2]; lo.w += dr[i][3];
+        hi.x += dr[i][4]; hi.y += dr[i][5]; hi.z += dr[i][6]; hi.w += dr[i][7];
+        db_at[2 * i * nt] = lo;
+        db_at[(2 * i + 1) * nt] = hi;
       }
     }
     // Both sums at once: lanes 0-15 of a warp take s1, lanes 16-31 s2.  Two
@@ -604,23 +749,19 @@ __global__ void __launch_bounds__(512) norm_grad_ring(const NGrad a) {
         store8(static_cast<XT*>(a.dx) + r * a.cols, c, cols, true, f);
     }
   }
-  if (!ok && t == 0) {   // the copies in flight land before shared memory is released
-    const uint64_t t0 = global_ns();
-    for (int i = 0; i < slots; ++i) {
-      const int64_t rounds = (a.rows - blockIdx.x + gridDim.x - 1) / gridDim.x;   // rows fetched
-      if (i >= rounds) break;
-      const int64_t last = (rounds - 1 - i) / slots;   // the slot's last phase
-      while (!mbar_try_wait(smem_u32(&full[i]), last & 1) && global_ns() - t0 < a.timeout_ns) {
-      }
-    }
-  }
+  if (!ok && t == 0) drain_ring(full, slots, a.rows, a.timeout_ns);
   float* part = a.part + int64_t(blockIdx.x) * 2 * a.cols;
 #pragma unroll
   for (int i = 0; i < I; ++i) {
     const int c = 8 * (t + i * nt);
     if (c >= cols) break;
     store8(part, c, cols, true, dw[i]);
-    if (LAYER) store8(part + cols, c, cols, true, db[i]);
+    if constexpr (DB_SHARED) {
+      *reinterpret_cast<float4*>(part + cols + c) = db_at[2 * i * nt];
+      *reinterpret_cast<float4*>(part + cols + c + 4) = db_at[(2 * i + 1) * nt];
+    } else if (LAYER) {
+      store8(part + cols, c, cols, true, db[i]);
+    }
   }
 }
 
@@ -714,50 +855,76 @@ RowPlan backward_plan(int64_t cols, int x_dtype) {
 
 int grad_ctas_per_sm(const RowPlan& p) { return std::max(1, (p.i == 1 ? 768 : 512) / p.nt); }
 
+// Shared memory behind the ring for the sums of db.
+int grad_db_bytes(const RowPlan& p) { return p.i == 4 ? p.nt * 4 * 32 : 0; }
+
 // Rows in flight of a CTA of norm_grad_ring, 0 where it does not apply: the
 // shared memory of an SM (208 KB of it) split among its CTAs.
 int grad_slots(const RowPlan& p, int64_t cols, int x_dtype) {
   const int64_t row = cols * (x_dtype == MXQ_OUT_BF16 ? 2 : 4);
   if (p.warp || !p.i || cols % 8 != 0) return 0;
-  const int64_t fit = (208 * 1024 / grad_ctas_per_sm(p)) / (2 * row);
+  const int64_t fit = (208 * 1024 / grad_ctas_per_sm(p) - grad_db_bytes(p)) / (2 * row);
   return fit < 2 ? 0 : static_cast<int>(std::min<int64_t>(fit, N_MAX_SLOTS));
 }
 
 // Sets of partial sums.  Register kernels: one per CTA, as many CTAs as the
 // registers let an SM hold at once (about 768, 512 and 512 threads with one,
-// two and four chunks each).  Longer rows: enough that the column sums fill the
+// two and four chunks each), but with few rows no more than one an SM or one
+// for eight rows, since each costs a set of sums to write and to join
+// (517x1001 fp32: 11.2 us against 10.6).  Longer rows: enough that the column sums fill the
 // device.
 int grad_splits(int64_t rows, int64_t cols, int x_dtype) {
   const RowPlan p = backward_plan(cols, x_dtype);
   if (p.i) {
     const int64_t want = int64_t(grad_ctas_per_sm(p)) * sm_count();
-    return static_cast<int>(std::min<int64_t>(p.warp ? (rows + 7) / 8 : rows, want));
+    const int64_t few = std::max<int64_t>(sm_count(), rows / (p.warp ? 64 : 8));
+    return static_cast<int>(std::min(std::min<int64_t>(p.warp ? (rows + 7) / 8 : rows, want), few));
   }
   const int64_t want = std::max<int64_t>(1, 8 * sm_count() / ((cols + 255) / 256));
   return static_cast<int>(std::min<int64_t>(std::min<int64_t>(rows, want), 512));
 }
 
-// A launch that may start while the previous kernel on the stream drains; the
-// kernels wait for it before their first global access.
-template <typename K, typename A>
-bool launch_early(K kernel, unsigned grid, int threads, size_t smem, cudaStream_t st, const A& a) {
-  cudaLaunchConfig_t cfg = {};
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.gridDim = dim3(grid, 1, 1);
-  cfg.blockDim = dim3(static_cast<unsigned>(threads), 1, 1);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = st;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  if (cudaLaunchKernelEx(&cfg, kernel, a) == cudaSuccess) return true;
-  cudaGetLastError();
-  return false;
+// Persistent CTAs for norm_ring: four chunks a thread, 512 threads an SM.  Two
+// chunks and 1024 threads leave twice the reductions per element (8192x4096
+// bf16, layer norm 30.6 us against 24.7, RMS to codes 31.1 against 24.2).  Rows
+// of up to 1024 columns, a warp each either way, gain from the ring but for RMS
+// norm to codes (32768x1024: layer norm 33.6 us without, 26.5 with it, to codes
+// 36.8 and 32.6; RMS to codes 21.8 and 25.6).
+constexpr int N_RING_I = 4;
+struct RingPlan {
+  int nt, ctas, slots;   // slots == 0: not for these rows
+};
+
+RingPlan forward_ring(int64_t rows, int64_t cols, int64_t size, bool rms_codes) {
+  const int64_t chunks = (cols + 7) / 8;
+  RingPlan p = {0, 0, 0};
+  if (cols % 8 != 0 || chunks <= (rms_codes ? 128 : 64) || chunks > 512 * N_RING_I) return p;
+  p.nt = static_cast<int>(((chunks + N_RING_I - 1) / N_RING_I + 31) / 32 * 32);
+  const int per_sm = std::max(1, 512 / p.nt);
+  p.ctas = per_sm * sm_count();
+  const int64_t fit = (200 * 1024 / per_sm) / (cols * size);
+  if (rows >= 2 * p.ctas && fit >= 2)
+    p.slots = static_cast<int>(std::min<int64_t>(fit, N_MAX_SLOTS));
+  return p;
 }
 
 template <typename XT, typename WT, bool LAYER, int FMT>
-mxq_status launch_forward(const NArgs& a, cudaStream_t st) {
+bool launch_norm_ring(const NArgs& a, const RingPlan& p, cudaStream_t st) {
+  const size_t smem = size_t(p.slots) * a.cols * sizeof(XT);
+  return ensure_dynamic_smem(reinterpret_cast<const void*>(norm_ring<XT, WT, LAYER, FMT, N_RING_I>),
+                             static_cast<int>(smem)) &&
+         launch_early(norm_ring<XT, WT, LAYER, FMT, N_RING_I>, static_cast<unsigned>(p.ctas), p.nt,
+                      smem, st, a);
+}
+
+template <typename XT, typename WT, bool LAYER, int FMT>
+mxq_status launch_forward(NArgs a, cudaStream_t st) {
+  const RingPlan ring = forward_ring(a.rows, a.cols, sizeof(XT), !LAYER && FMT >= 0);
+  if (ring.slots) {
+    a.slots = ring.slots;
+    a.timeout_ns = wait_timeout_ns();
+    return launch_norm_ring<XT, WT, LAYER, FMT>(a, ring, st) ? launch_status() : MXQ_ERR_CUDA;
+  }
   const RowPlan p = forward_plan(a.rows, a.cols);
   const unsigned rows = static_cast<unsigned>(a.rows), groups = (rows + 7) / 8;
   bool ok;
@@ -800,7 +967,7 @@ mxq_status run_backward(const NGrad& a, cudaStream_t st) {
     ok = p.i == 1 ? launch_early(norm_grad_regs<XT, WT, LAYER, true, 1>, grid, 256, smem, st, a)
                   : launch_early(norm_grad_regs<XT, WT, LAYER, true, 2>, grid, 256, smem, st, a);
   } else if (p.i && a.slots) {
-    const size_t smem = size_t(a.slots) * 2 * a.cols * sizeof(XT);
+    const size_t smem = size_t(a.slots) * 2 * a.cols * sizeof(XT) + grad_db_bytes(p);
     if (p.i == 1) ok = launch_ring<XT, WT, LAYER, 1>(a, p.nt, smem, st);
     else if (p.i == 2) ok = launch_ring<XT, WT, LAYER, 2>(a, p.nt, smem, st);
     else if constexpr (std::is_same<XT, __nv_bfloat16>::value)
