@@ -12,6 +12,11 @@
 // The variance is taken about the mean (two passes over the row), not as a
 // difference of moments, so that a large common offset costs no digits.  Sums
 // over rows run in a fixed order: no atomics.
+//
+// Bound by HBM; a row's reductions must not keep the loads waiting, hence the
+// rings below.  Measured, 8192x4096 bf16: RMS forward 22 us (0.90 of the copy
+// rate), layer norm forward 24.7 us (0.80), RMS to codes 24.2 us, layer norm
+// backward 38.9 us with the join of the column sums (0.76).
 #include <type_traits>
 
 #include "fp8_common.cuh"
