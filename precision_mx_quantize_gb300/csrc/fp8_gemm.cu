@@ -34,7 +34,10 @@
 // and the next MMAs' start take about 1600 cycles, and tensor memory holds two
 // accumulators, so a K block takes 800 (1250 with line scales).  Three of 160
 // columns were slower still: the accumulation warps' fixed cost per block
-// weighs more (8192x6144x4096 176 us).  Measured: 8192x6144x4096, tile scales,
+// weighs more (8192x6144x4096 176 us); so were sixteen accumulation warps of 64
+// columns (165 us, and 913-946 with line scales).  In runs of seconds the card's
+// power limit (1400 W) binds as well and both shapes below take 5 % longer.
+// Measured: 8192x6144x4096, tile scales,
 // bf16 out 149 us (2.77 PFLOP/s, 0.71 of twice the bf16 rate; the MMAs alone,
 // nothing read back, 118 us); 28672x4096x8192, line scales, fp32 out 943 us
 // (2.04 PFLOP/s, 0.53).
