@@ -984,9 +984,10 @@ mxq_status run_backward(const NGrad& a, cudaStream_t st) {
     else if constexpr (std::is_same<XT, __nv_bfloat16>::value)
       ok = launch_early(norm_grad_regs<XT, WT, LAYER, false, 4>, grid, p.nt, 0, st, a);
   } else {
-    norm_grad_rows<XT, WT, LAYER><<<static_cast<unsigned>(a.rows), 256, 0, st>>>(a);
+    // the column sums first: dx may take the place of x or dy
     const unsigned groups = static_cast<unsigned>((a.cols + 255) / 256);
     norm_grad_cols<XT, LAYER><<<dim3(groups, grid), 256, 0, st>>>(a);
+    norm_grad_rows<XT, WT, LAYER><<<static_cast<unsigned>(a.rows), 256, 0, st>>>(a);
   }
   if (!ok) return MXQ_ERR_CUDA;
   const JoinArgs j{a.part, a.cols, a.splits, a.dweight, a.dbias};

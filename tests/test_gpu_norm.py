@@ -259,3 +259,21 @@ def test_same_inputs_give_the_same_bits():
     for _ in range(3):
         again = mxq.layer_norm_backward(dy, x, w, mean, rstd)
         assert all(torch.equal(p, q) for p, q in zip(first, again))
+
+
+@pytest.mark.parametrize("dt", [torch.bfloat16, torch.float32], ids=str)
+@pytest.mark.parametrize("size", [(5, 64), (9, 1001), (2000, 2048), (1300, 4096), (6, 9000),
+                                  (7, 20001), (4, 20000)], ids=str)
+def test_in_place(size, dt):
+    # y over x, dx over dy or x: the bits of separate buffers
+    x, w, b, dy = (t.cuda() for t in _inputs(*size, dt, torch.float32, seed=3))
+    y, mean, rstd = mxq.layer_norm(x, w, b)
+    want = mxq.layer_norm_backward(dy, x, w, mean, rstd)
+    for over in ("dy", "x"):
+        t = {"dy": dy.clone(), "x": x.clone()}
+        got = mxq.layer_norm_backward(t["dy"], t["x"], w, mean, rstd, out=t[over])
+        assert got[0] is t[over]
+        assert all(torch.equal(p, q) for p, q in zip(got, want))
+    t = x.clone()
+    assert torch.equal(mxq.layer_norm(t, w, b, out=t)[0], y)
+    mxq.check()
