@@ -16,10 +16,12 @@
 //
 // Bound by HBM: 2 bytes read and one written per element and layout.  A CTA per
 // tile, four (128x128 tiles with both codes: three) of them on an SM: 28672x4096
-// weight 73 us, 0.95 of the copy rate; 8192x4096 activation, both layouts, 25.8
+// weight 71 us, 0.97 of the copy rate; 8192x4096 activation, both layouts, 25.8
 // us, 0.77 (its 2048 tiles make 3.4 waves).  Persistent CTAs whose next tile
 // comes by TMA under the conversion ran 8192x4096 in 24.1 us and the weight in
-// 84: not kept.
+// 84: not kept.  Rows that start between 16-byte boundaries are cut out of
+// aligned loads: 8001x4097 along rows 23.4 us (element by element 33.4), both
+// layouts 30.9 (44.0).
 #include "fp8_common.cuh"
 #include "mxq_host.h"
 
@@ -41,13 +43,13 @@ struct QArgs {
   float* scales_c;
   int64_t pitch_r, pitch_c;  // bytes between code lines
   int64_t lines_r, lines_c;  // floats between scale rows
-  int32_t vec;               // rows of x are 16-byte aligned
 };
 
 // Magnitudes of a bf16 pair without the sign bits.
 MXQ_DEV uint32_t mag2(uint32_t w) { return w & 0x7FFF7FFFu; }
 
-template <int MODE, int FR, int FC>
+// VEC: rows of x start at 16-byte boundaries.
+template <int MODE, int FR, int FC, bool VEC>
 __global__ void __launch_bounds__(256, MODE == Q_TILES ? 3 : 4) fp8_quant_kernel(const QArgs a) {
   constexpr bool ROW = MODE == Q_ROW || MODE == Q_DUAL;
   constexpr bool COL = MODE == Q_COL || MODE == Q_DUAL;
@@ -68,21 +70,61 @@ __global__ void __launch_bounds__(256, MODE == Q_TILES ? 3 : 4) fp8_quant_kernel
   griddep_launch_dependents();
   uint32_t v[8][4];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const int64_t r = row + i;
-    v[i][0] = v[i][1] = v[i][2] = v[i][3] = 0u;
-    if (r < a.rows && col < a.cols) {
-      const __nv_bfloat16* p = a.x + r * a.cols + col;
-      if (a.vec) {   // cols % 8 == 0: the whole chunk is inside the row
-        if (MXQ_IN_BOUNDS(col + 8 <= a.cols, &g_err_fp8_quant, SITE_B_FP8_LOAD)) {
-          const uint4 w = *reinterpret_cast<const uint4*>(p);
-          v[i][0] = w.x; v[i][1] = w.y; v[i][2] = w.z; v[i][3] = w.w;
-        }
-      } else {
-        const uint16_t* q = reinterpret_cast<const uint16_t*>(p);
+  for (int i = 0; i < 8; ++i) v[i][0] = v[i][1] = v[i][2] = v[i][3] = 0u;
+  if constexpr (VEC) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const int64_t r = row + i;
+      // cols % 8 == 0: the whole chunk is inside the row
+      if (r < a.rows && col < a.cols &&
+          MXQ_IN_BOUNDS(col + 8 <= a.cols, &g_err_fp8_quant, SITE_B_FP8_LOAD)) {
+        const uint4 w = *reinterpret_cast<const uint4*>(a.x + r * a.cols + col);
+        v[i][0] = w.x; v[i][1] = w.y; v[i][2] = w.z; v[i][3] = w.w;
+      }
+    }
+  } else {
+    // rows that start anywhere: four at a time, as the registers allow
+    const int64_t n = a.rows * a.cols;
+    constexpr int REACH = Across<__nv_bfloat16>::REACH;
+#pragma unroll
+    for (int i0 = 0; i0 < 8; i0 += 4) {
+      Across<__nv_bfloat16> t[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        t[i].clear();
+        const int64_t r = row + i0 + i, at = r * a.cols + col;
+        if (r < a.rows && col < a.cols && at + REACH <= n &&
+            MXQ_IN_BOUNDS(at >= 0, &g_err_fp8_quant, SITE_B_FP8_LOAD))
+          t[i].load(a.x, at);
+      }
+#pragma unroll
+      for (int i = 0; i < 4; ++i) t[i].cut((row + i0 + i) * a.cols + col, v[i0 + i]);
+    }
+    if (col < a.cols && (min(row + 8, a.rows) - 1) * a.cols + col + REACH > n) {
+      // the last elements of x
+      for (int i = 0; i < 8; ++i) {
+        const int64_t r = row + i, at = r * a.cols + col;
+        if (r >= a.rows || at + REACH <= n) continue;
+        uint32_t w[4] = {0u, 0u, 0u, 0u};
 #pragma unroll
         for (int j = 0; j < 8; ++j)
-          if (col + j < a.cols) v[i][j >> 1] |= static_cast<uint32_t>(q[j]) << (16 * (j & 1));
+          if (at + j < n)
+            w[j >> 1] |= static_cast<uint32_t>(reinterpret_cast<const uint16_t*>(a.x)[at + j])
+                         << (16 * (j & 1));
+#pragma unroll
+        for (int k = 0; k < 8; ++k)   // v keeps compile-time indices
+          if (k == i) {
+            v[k][0] = w[0]; v[k][1] = w[1]; v[k][2] = w[2]; v[k][3] = w[3];
+          }
+      }
+    }
+    if (col + 8 > a.cols) {   // the next row's elements
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const int64_t left = a.cols - col - 2 * j;
+        const uint32_t keep = left >= 2 ? ~0u : left == 1 ? 0xFFFFu : 0u;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i][j] &= keep;
       }
     }
   }
@@ -223,9 +265,12 @@ template <int MODE, int FR, int FC>
 mxq_status launch(const QArgs& a, void* stream) {
   const int64_t n = (a.rows + 127) / 128 * a.n_ct;
   if (n >= (int64_t(1) << 31)) return MXQ_ERR_ARG;
-  return launch_early(fp8_quant_kernel<MODE, FR, FC>, static_cast<unsigned>(n), 256, 0,
-                      static_cast<cudaStream_t>(stream), a)
-             ? launch_status() : MXQ_ERR_CUDA;
+  const cudaStream_t st = static_cast<cudaStream_t>(stream);
+  const unsigned ctas = static_cast<unsigned>(n);
+  const bool ok = a.cols % 8 == 0
+                      ? launch_early(fp8_quant_kernel<MODE, FR, FC, true>, ctas, 256, 0, st, a)
+                      : launch_early(fp8_quant_kernel<MODE, FR, FC, false>, ctas, 256, 0, st, a);
+  return ok ? launch_status() : MXQ_ERR_CUDA;
 }
 
 mxq_status check_input(const void* x, int64_t rows, int64_t cols) {
@@ -250,7 +295,6 @@ QArgs args(const void* x, int64_t rows, int64_t cols) {
   a.pitch_c = fp8_pitch(rows);
   a.lines_r = fp8_lines(rows);
   a.lines_c = fp8_lines(cols);
-  a.vec = cols % 8 == 0;
   return a;
 }
 
