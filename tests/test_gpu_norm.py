@@ -277,3 +277,42 @@ def test_in_place(size, dt):
     t = x.clone()
     assert torch.equal(mxq.layer_norm(t, w, b, out=t)[0], y)
     mxq.check()
+
+
+# Rows that start between 16-byte boundaries: enough of them for the persistent
+# kernels, every place of the last chunk and of the last 16-byte word.
+ODD = [(1000, 4097), (4900, 1003), (700, 8190), (3, 16383), (307, 15000)]
+ODD += [(9, c) for c in range(513, 521)] + [(3, c) for c in range(9, 17)]
+
+
+@pytest.mark.parametrize("kind", ["layer", "rms"])
+@pytest.mark.parametrize("types", [TYPES[1], TYPES[2]], ids=str)
+@pytest.mark.parametrize("size", ODD, ids=str)
+def test_unaligned_rows(size, types, kind):
+    test_forward(size, types, kind)
+    test_forward_to_codes(size, types, "e4m3", kind)
+    test_backward(size, types, kind)
+
+
+@pytest.mark.parametrize("dt", [torch.bfloat16, torch.float32], ids=str)
+def test_unaligned_rows_leave_their_surroundings(dt):
+    # x in a longer buffer: NaN right behind it changes nothing, and y and dx in
+    # one write nothing behind them
+    for rows, cols in ((1000, 4097), (9, 517), (12, 1001), (5, 77)):
+        x, w, b, dy = (t.cuda() for t in _inputs(rows, cols, dt, torch.float32, seed=4))
+        n = rows * cols
+
+        def inside(t, value):
+            long = torch.full((n + 64,), value, device="cuda", dtype=dt)
+            long[:n] = t.flatten()
+            return long, long[:n].view(rows, cols)
+
+        y, mean, rstd = mxq.layer_norm(x, w, b)
+        want = mxq.layer_norm_backward(dy, x, w, mean, rstd)
+        (_, xl), (_, dyl) = inside(x, float("nan")), inside(dy, float("nan"))
+        (yb, yl), (db, dl) = inside(x, 7.0), inside(x, 7.0)
+        assert torch.equal(mxq.layer_norm(xl, w, b, out=yl)[0], y)
+        got = mxq.layer_norm_backward(dyl, xl, w, mean, rstd, out=dl)
+        mxq.check()
+        assert all(torch.equal(p, q) for p, q in zip(got, want))
+        assert (yb[n:] == 7).all() and (db[n:] == 7).all()
