@@ -625,6 +625,20 @@ MXQ_DEV void copy_out(const FArgs& a, uint32_t out, int quad, int lane, int64_t 
   }
 }
 
+// A barrier of `threads` threads that says, to all of them alike, whether any of
+// them saw the CTA abort: on their own readings of the flag some would leave and
+// some wait for them.
+MXQ_DEV bool sync_any(int id, int threads, bool v) {
+  uint32_t any;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %3, 0;\n\t"
+      "barrier.cta.red.or.pred q, %1, %2, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+      : "=r"(any)
+      : "r"(id), "r"(threads), "r"(static_cast<uint32_t>(v))
+      : "memory");
+  return any != 0;
+}
+
 MXQ_DEV void tma_store_2d(const CUtensorMap* map, uint32_t src, int32_t x, int32_t y) {
   asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.tile.bulk_group [%0, {%2, %3}], [%1];" ::"l"(
                    reinterpret_cast<uint64_t>(map)),
@@ -913,7 +927,6 @@ __global__ void __launch_bounds__(P_THREADS, 1)
         __syncwarp();
         arrive_if(lane == 0, bars + 64 + 8 * (grp & 1));   // sc_empty
       }
-      if (__any_sync(~0u, *abort_flag)) break;
       int mp, nt;
       tile_coords(t, p, mp, nt);
       const int row0 = (mp * 2 + static_cast<int>(rank)) * 128, col0 = nt * 256 + h * 128;
@@ -924,11 +937,14 @@ __global__ void __launch_bounds__(P_THREADS, 1)
       const bool bf16 = a.out_bf16 != 0;
       const uint32_t mine = smem_u32(out) + h * 32768;
       const bool first = threadIdx.x % 128 == 0;   // issues and tracks the copies
+      bool aborted = false;
 #pragma unroll
       for (int pass = 0; pass < 2; ++pass) {
         if (pass && bf16) break;
         if (first) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
-        asm volatile("bar.sync %0, 128;" ::"r"(1 + h) : "memory");
+        // (the half's threads meet here before either pass)
+        aborted = sync_any(1 + h, 128, *abort_flag != 0);
+        if (aborted) break;
         stage_out<LINES>(acc, mine, quad, lane, bf16, pass);
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
         asm volatile("bar.sync %0, 128;" ::"r"(1 + h) : "memory");
@@ -941,6 +957,7 @@ __global__ void __launch_bounds__(P_THREADS, 1)
           asm volatile("cp.async.bulk.commit_group;" ::: "memory");
         }
       }
+      if (aborted) break;
     }
     if (threadIdx.x % 128 == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
   }
