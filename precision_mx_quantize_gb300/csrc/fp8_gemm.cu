@@ -29,6 +29,9 @@
 //               registers for the whole K loop, adds each K block with one
 //               multiply-add per element (line scales of B: one more multiply),
 //               and hands them to a TMA store through shared memory.
+// Few tiles with a long K are shared: up to four pairs of a cluster take a part
+// of the K blocks each and join their sums in order through distributed shared
+// memory (512x4096x14336 31 us, 46 without).
 // Bound by the round trip of an accumulator: MMAs (512 cycles), commit, the
 // read-back with its additions (360 cycles for a warp's 128 columns), hand-over
 // and the next MMAs' start take about 1600 cycles, and tensor memory holds two
@@ -454,7 +457,16 @@ struct PArgs {
   int32_t n_mp, n_nt, n_tiles;   // 256-row and 256-column tiles
   int32_t group, group_n;        // tile order (tile_coords)
   int32_t tma_out;               // rows of C are 16-byte multiples: tiles leave by TMA
+  int32_t split;                 // pairs of a cluster that share a tile's K blocks
 };
+
+// Pairs of a cluster that share a tile leave their sums in shared memory, rows of
+// 256 columns this many floats apart: the stores below then meet no bank twice,
+// and rows keep to 16 bytes.
+constexpr int P_MAX_SPLIT = 4;
+template <bool LINES>
+constexpr int part_pitch() { return LINES ? 264 : 260; }
+static_assert(128 * 264 * 4 <= Pair<true>::STAGES * P_STAGE + Pair<true>::OUT, "over the ring");
 
 MXQ_DEV void mma_f8_pair(uint32_t d_tmem, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accum) {
   asm volatile(
@@ -625,6 +637,53 @@ MXQ_DEV void copy_out(const FArgs& a, uint32_t out, int quad, int lane, int64_t 
   }
 }
 
+// Two neighbouring elements of C from an even column on.
+MXQ_DEV void store2(const FArgs& a, int64_t row, int64_t col, float x, float y) {
+  if (col >= a.N) return;
+  const int64_t at = row * a.N + col;
+  const bool two = col + 1 < a.N;
+  if (a.out_bf16) {
+    __nv_bfloat16* c = static_cast<__nv_bfloat16*>(a.C) + at;
+    if (a.N % 2 == 0) {
+      *reinterpret_cast<uint32_t*>(c) = bf16x2(x, y);
+    } else {
+      c[0] = __float2bfloat16_rn(x);
+      if (two) c[1] = __float2bfloat16_rn(y);
+    }
+  } else {
+    float* c = static_cast<float*>(a.C) + at;
+    if (a.N % 2 == 0) {
+      *reinterpret_cast<float2*>(c) = make_float2(x, y);
+    } else {
+      c[0] = x;
+      if (two) c[1] = y;
+    }
+  }
+}
+
+// Four, from a column that is a multiple of four.
+MXQ_DEV void store4(const FArgs& a, int64_t row, int64_t col, float4 v) {
+  if (col >= a.N || !MXQ_IN_BOUNDS(row < a.M, &g_err_fp8_gemm, SITE_B_FP8_GEMM)) return;
+  if (a.N % 4 == 0) {
+    const int64_t at = row * a.N + col;
+    if (a.out_bf16)
+      *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(a.C) + at) =
+          make_uint2(bf16x2(v.x, v.y), bf16x2(v.z, v.w));
+    else
+      *reinterpret_cast<float4*>(static_cast<float*>(a.C) + at) = v;
+  } else {
+    store2(a, row, col, v.x, v.y);
+    store2(a, row, col + 2, v.z, v.w);
+  }
+}
+
+MXQ_DEV float4 ld_cluster4(uint32_t addr) {
+  float4 v;
+  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(addr) : "memory");
+  return v;
+}
+
 // A barrier of `threads` threads that says, to all of them alike, whether any of
 // them saw the CTA abort: on their own readings of the flag some would leave and
 // some wait for them.
@@ -646,12 +705,14 @@ MXQ_DEV void tma_store_2d(const CUtensorMap* map, uint32_t src, int32_t x, int32
                : "memory");
 }
 
-template <bool LINES>
+// SPLIT: a.split pairs of a cluster share the K blocks of one tile and join their
+// sums in order through distributed shared memory.
+template <bool LINES, bool SPLIT>
 __global__ void __launch_bounds__(P_THREADS, 1)
     fp8_gemm_pair(const __grid_constant__ CUtensorMap ta, const __grid_constant__ CUtensorMap tb,
                   const __grid_constant__ CUtensorMap tc, const PArgs p) {
   using P = Pair<LINES>;
-  constexpr int S = P::STAGES;
+  constexpr int S = P::STAGES, PITCH = part_pitch<LINES>();
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~static_cast<uintptr_t>(1023));
@@ -672,7 +733,11 @@ __global__ void __launch_bounds__(P_THREADS, 1)
 
   const FArgs& a = p.f;
   const int warp = warp_index(), lane = threadIdx.x & 31;
-  const uint32_t rank = cluster_rank();
+  const uint32_t crank = cluster_rank();
+  const uint32_t rank = SPLIT ? crank & 1 : crank;     // in the pair
+  const uint32_t first_rank = crank - rank;            // the leader's in the cluster
+  const int pair = crank >> 1, split = SPLIT ? p.split : 1;
+  const uint16_t both = static_cast<uint16_t>(0x3 << first_rank);
   const bool leader = rank == 0;
   if (threadIdx.x == 0) {
     prefetch_tmap(&ta);
@@ -699,9 +764,12 @@ __global__ void __launch_bounds__(P_THREADS, 1)
   tc_fence_after();
   griddep_wait();
   griddep_launch_dependents();
-  const int cid = blockIdx.x >> 1, ncl = gridDim.x >> 1;
+  const int cid = blockIdx.x / (2 * split), ncl = gridDim.x / (2 * split);
   const uint32_t tmem = *tmem_slot;
-  const int nk = a.nk, n_tiles = p.n_tiles;
+  // this pair's K blocks
+  const int k0 = SPLIT ? static_cast<int>(int64_t(a.nk) * pair / split) : 0;
+  const int nk = SPLIT ? static_cast<int>(int64_t(a.nk) * (pair + 1) / split) - k0 : a.nk;
+  const int n_tiles = p.n_tiles;
   const uint64_t tmo = a.timeout_ns;
 
   if (warp < 4) {
@@ -713,7 +781,7 @@ __global__ void __launch_bounds__(P_THREADS, 1)
     const bool one = elect_one();
     if (warp == 0) {
       // ---------------- TMA producer (both CTAs) ----------------
-      const uint32_t full0 = map_to_rank(smem_u32(&full[0]), 0);
+      const uint32_t full0 = map_to_rank(smem_u32(&full[0]), first_rank);
       uint32_t s = 0, phase = 0, issued = 0;
       bool ok = true;
       for (int t = cid; t < n_tiles && ok; t += ncl) {
@@ -730,16 +798,17 @@ __global__ void __launch_bounds__(P_THREADS, 1)
           const uint32_t st = smem_u32(smem + s * P_STAGE), bar = full0 + s * 8;
           if (one) {
             if (leader) mbar_arrive_expect_tx(smem_u32(&full[s]), 2 * P_STAGE);
-            tma_load_2d_pair(st, &ta, bar, kb * 128, ra);
-            tma_load_2d_pair(st + P_OPERAND, &tb, bar, kb * 128, rb);
-            tma_load_2d_pair(st + P_OPERAND + P_OPERAND / 2, &tb, bar, kb * 128, rb + 128);
+            tma_load_2d_pair(st, &ta, bar, (k0 + kb) * 128, ra);
+            tma_load_2d_pair(st + P_OPERAND, &tb, bar, (k0 + kb) * 128, rb);
+            tma_load_2d_pair(st + P_OPERAND + P_OPERAND / 2, &tb, bar, (k0 + kb) * 128, rb + 128);
           }
           ++issued;
           if (++s == S) { s = 0; phase ^= 1; }
         }
       }
       if (one && !leader) {
-        st_cluster_u32(map_to_rank(smem_u32(const_cast<uint32_t*>(peer_issued)), 0), issued);
+        st_cluster_u32(map_to_rank(smem_u32(const_cast<uint32_t*>(peer_issued)), first_rank),
+                       issued);
       } else if (one && !ok) {
         // Every copy of both CTAs signals the leader's stage barriers; before
         // the final cluster barrier the leader waits (bounded) for the copies
@@ -781,20 +850,20 @@ __global__ void __launch_bounds__(P_THREADS, 1)
               mma_f8_pair(d, ad + 2, bd + 2, idesc, 1u);
               mma_f8_pair(d, ad + 4, bd + 4, idesc, 1u);
               mma_f8_pair(d, ad + 6, bd + 6, idesc, 1u);
-              tc_commit_pair_mc(smem_u32(&acc_full[2 * b]), 0x3);
+              tc_commit_pair_mc(smem_u32(&acc_full[2 * b]), both);
               constexpr uint32_t kHalf = (P_OPERAND / 2) >> 4;   // columns 128-255
               mma_f8_pair(d + 128, ad, bd + kHalf, idesc, 0u);
               mma_f8_pair(d + 128, ad + 2, bd + kHalf + 2, idesc, 1u);
               mma_f8_pair(d + 128, ad + 4, bd + kHalf + 4, idesc, 1u);
               mma_f8_pair(d + 128, ad + 6, bd + kHalf + 6, idesc, 1u);
-              tc_commit_pair_mc(smem_u32(&acc_full[2 * b + 1]), 0x3);
-              tc_commit_pair_mc(smem_u32(&empty[s]), 0x3);
+              tc_commit_pair_mc(smem_u32(&acc_full[2 * b + 1]), both);
+              tc_commit_pair_mc(smem_u32(&empty[s]), both);
             }
             if (++s == S) { s = 0; phase ^= 1; }
           }
         }
         if (one) {   // every MMA is complete before teardown
-          tc_commit_pair_mc(smem_u32(drain), 0x1);
+          tc_commit_pair_mc(smem_u32(drain), static_cast<uint16_t>(0x1 << first_rank));
           if (!mbar_wait(smem_u32(drain), 0, tmo))
             record_error(&g_err_fp8_gemm, MXQ_ERR_TIMEOUT, SITE_FP8_DRAIN);
         }
@@ -827,19 +896,19 @@ __global__ void __launch_bounds__(P_THREADS, 1)
               const float4 zero = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
               va[u] = zero;
               if (kb < nk && a_in)
-                va[u] = *reinterpret_cast<const float4*>(a.sA + kb * a.lines_a + ra);
+                va[u] = *reinterpret_cast<const float4*>(a.sA + (k0 + kb) * a.lines_a + ra);
               if constexpr (LINES) {
-                const float* sb = a.sB + kb * a.lines_b + cb + 4 * lane;
+                const float* sb = a.sB + (k0 + kb) * a.lines_b + cb + 4 * lane;
                 vb[u] = vc[u] = zero;
                 if (kb < nk && cb + 4 * lane < a.lines_b)
                   vb[u] = *reinterpret_cast<const float4*>(sb);
                 if (kb < nk && cb + 128 + 4 * lane < a.lines_b)
                   vc[u] = *reinterpret_cast<const float4*>(sb + 128);
               } else {
-                const float* sb = a.sB + (cb >> 7) * nk + kb;
+                const float* sb = a.sB + (cb >> 7) * a.nk + k0 + kb;
                 s0[u] = s1[u] = 0.0f;
                 if (kb < nk && cb < a.N) s0[u] = sb[0];
-                if (kb < nk && cb + 128 < a.N) s1[u] = sb[nk];
+                if (kb < nk && cb + 128 < a.N) s1[u] = sb[a.nk];
               }
             }
 #pragma unroll
@@ -872,7 +941,7 @@ __global__ void __launch_bounds__(P_THREADS, 1)
     // every shared address is an offset from one register.
     const int quad = warp & 3, h = (warp - 4) >> 2;
     const uint32_t bars = smem_u32(acc_full), sc = smem_u32(scales);
-    const uint32_t empty_leader = map_to_rank(smem_u32(acc_empty), 0);
+    const uint32_t empty_leader = map_to_rank(smem_u32(acc_empty), first_rank);
     const uint32_t taddr0 = tmem + (static_cast<uint32_t>(quad * 32) << 16) + h * 128;
     const uint32_t row_at = 4 * ((LINES ? 0 : h * 128) + quad * 32 + (LINES ? lane >> 2 : lane));
     const uint32_t col_at = 4 * (128 + h * 128 + 2 * (lane & 3));
@@ -931,6 +1000,23 @@ __global__ void __launch_bounds__(P_THREADS, 1)
       tile_coords(t, p, mp, nt);
       const int row0 = (mp * 2 + static_cast<int>(rank)) * 128, col0 = nt * 256 + h * 128;
       if (!MXQ_IN_BOUNDS(mp < p.n_mp && nt < p.n_nt, &g_err_fp8_gemm, SITE_B_FP8_GEMM)) continue;
+      if constexpr (SPLIT) {
+        // over the ring and the staging area: the last accumulators of both
+        // halves are complete, so no MMA or copy of this CTA is left
+        if (sync_any(3, 256, *abort_flag != 0)) break;
+        const uint32_t part = smem_u32(smem) + (quad * 32 * PITCH + h * 128) * 4;
+#pragma unroll
+        for (int j = 0; j < 128; j += LINES ? 2 : 4) {
+          const uint32_t to =
+              part + (acc_row<LINES>(j, lane) * PITCH + acc_col<LINES>(j, lane)) * 4;
+          if constexpr (LINES)
+            sts(to, __float_as_uint(acc[j]), __float_as_uint(acc[j + 1]));
+          else
+            sts(to, __float_as_uint(acc[j]), __float_as_uint(acc[j + 1]),
+                __float_as_uint(acc[j + 2]), __float_as_uint(acc[j + 3]));
+        }
+        break;   // a cluster has one tile
+      }
       // The half tile goes through shared memory and leaves by TMA, under the
       // next tile's K loop: stored from the registers it took as long as three
       // K blocks, and the MMAs only run two ahead.
@@ -961,39 +1047,101 @@ __global__ void __launch_bounds__(P_THREADS, 1)
     }
     if (threadIdx.x % 128 == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
   }
+  if constexpr (SPLIT) {
+    cluster_sync();
+    // Each pair adds up a share of the rows, over the pairs in order.
+    if (warp >= 4 && !*abort_flag) {
+      int mp, nt;
+      tile_coords(cid, p, mp, nt);
+      const int64_t row0 = (int64_t(mp) * 2 + rank) * 128, col0 = int64_t(nt) * 256 + 4 * lane;
+      const int end = 128 * (pair + 1) / split;
+      // two rows at a time, eight rows apart
+      for (int r = 128 * pair / split + warp - 4; r < end; r += 16) {
+        float4 v[2][2][P_MAX_SPLIT];
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+          const int row = r + 8 * (u >> 1);
+          const uint32_t mine = smem_u32(smem) + (row * PITCH + 4 * lane + 128 * (u & 1)) * 4;
+#pragma unroll
+          for (int q = 0; q < P_MAX_SPLIT; ++q)
+            v[u >> 1][u & 1][q] = q < split && row < end
+                                      ? ld_cluster4(map_to_rank(mine, 2 * q + rank))
+                                      : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        }
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+          const float4* t = v[u >> 1][u & 1];
+          const int row = r + 8 * (u >> 1);
+          float4 x = t[0];
+#pragma unroll
+          for (int q = 1; q < P_MAX_SPLIT; ++q) {
+            x.x += t[q].x;
+            x.y += t[q].y;
+            x.z += t[q].z;
+            x.w += t[q].w;
+          }
+          if (row < end && row0 + row < a.M) store4(a, row0 + row, col0 + 128 * (u & 1), x);
+        }
+      }
+    }
+  }
   tc_fence_before();
-  cluster_sync();   // no CTA leaves while its peer may still signal it
+  cluster_sync();   // no CTA leaves while another may still signal it or read its sums
   tc_fence_after();
   if (warp == 1) tmem_dealloc_pair(tmem, 512);
 }
 
-// Clusters of the pair kernel that fit on the device at once, cached per
-// device; 0 if they cannot be had, or if the kernel was built with fewer
-// registers than its warpgroups share out among themselves.
+// A launch of the pair kernel, but for its grid; `attr` holds two.
 template <bool LINES>
-int pair_clusters(cudaLaunchConfig_t cfg) {
+cudaLaunchConfig_t pair_config(cudaLaunchAttribute* attr, int split, void* stream) {
+  cudaLaunchConfig_t cfg = {};
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = 2 * split;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  // persistent grid: it may start while the previous kernel on the stream
+  // drains, and waits for it in the kernel
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
+  cfg.blockDim = dim3(P_THREADS, 1, 1);
+  cfg.dynamicSmemBytes = Pair<LINES>::SMEM;
+  cfg.stream = static_cast<cudaStream_t>(stream);
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  return cfg;
+}
+
+// Clusters of `split` pairs that fit on the device at once, cached per device;
+// 0 if they cannot be had, or if the kernel was built with fewer registers than
+// its warpgroups share out among themselves.
+template <bool LINES>
+int pair_clusters(int split) {
   static std::mutex mu;
-  static int cached[64] = {0};
+  static int cached[64][P_MAX_SPLIT + 1];   // clusters + 1; 0: not asked yet
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 0;
   std::lock_guard<std::mutex> lock(mu);
-  if (cached[dev] == 0) {
+  int& known = cached[dev][split];
+  if (known == 0) {
+    const auto kernel = split > 1 ? fp8_gemm_pair<LINES, true> : fp8_gemm_pair<LINES, false>;
     cudaFuncAttributes fa;
-    if (cudaFuncGetAttributes(&fa, fp8_gemm_pair<LINES>) != cudaSuccess ||
-        fa.numRegs < P_MIN_REGS) {
+    if (!ensure_dynamic_smem(reinterpret_cast<const void*>(kernel), Pair<LINES>::SMEM) ||
+        cudaFuncGetAttributes(&fa, kernel) != cudaSuccess || fa.numRegs < P_MIN_REGS) {
       cudaGetLastError();
       return 0;
     }
+    cudaLaunchAttribute attr[2];
+    cudaLaunchConfig_t cfg = pair_config<LINES>(attr, split, nullptr);
     cfg.numAttrs = 1;   // the cluster dimension
-    cfg.gridDim = dim3(static_cast<unsigned>(2 * sm_count()), 1, 1);
+    cfg.gridDim = dim3(static_cast<unsigned>(sm_count() / (2 * split) * 2 * split), 1, 1);
     int n = 0;
-    if (cudaOccupancyMaxActiveClusters(&n, fp8_gemm_pair<LINES>, &cfg) != cudaSuccess || n <= 0) {
+    if (cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) != cudaSuccess || n < 0) {
       cudaGetLastError();
-      n = sm_count() / 2;
+      n = split > 1 ? 0 : sm_count() / 2;
     }
-    cached[dev] = n;
+    known = n + 1;
   }
-  return cached[dev];
+  return known - 1;
 }
 
 // The 2-D map of `lines` code lines of K elements, in boxes of 128 x `box`.
@@ -1020,23 +1168,45 @@ uint32_t lanes_split(int64_t tiles, int nk) {
 
 int lanes_tokens(int64_t M) { return M <= 16 ? 16 : M <= 32 ? 32 : 64; }
 
-// Which kernel: modeled times in microseconds, fitted to measurements -- a K
-// block takes 0.45 us on a CTA pair, 0.85 or (up to 32 tokens) 0.55 us with two
-// few-token CTAs an SM, a join 3 us, a tile whose rows of C no TMA store takes
-// 5 us.  Lanes against pairs, measured: 64x28672x4096 24 and 33 us, 128x4096x4096
-// 12 and 16, 256x4096x4096 19 and 16, 512x4096x4096 21 and 17, 1024x1024x1024 7.6
-// and 7.6, 2048x2048x2048 25 and 12.
-bool pairs_win(int64_t M, int64_t N, int nk, bool tma_out) {
+// Which kernel, and how many pairs to a tile: modeled times in microseconds,
+// fitted to measurements.  Pairs: a K block 0.365 us (line scales 0.56), a tile
+// 1, or 6 where no TMA store takes the rows of C, a launch 4.5, a join 5; so
+// that few tiles with a long K share each tile among up to four pairs, while
+// all of them still run at once.  Lanes: a K block 0.7 or (up to 32 tokens)
+// 0.55 with two CTAs an SM, a wave 3, a join 3.  Measured with one, and with as
+// many pairs to a tile as this takes: 512x4096x14336 46.3 and 31.0 us (line
+// scales 69.7 and 42.8), 484x2592x12534 40.6 and 22.5, 256x4096x4096 16.5 and
+// 13.4.  Lanes against pairs: 64x28672x4096 25.7 and 33, 128x4096x4096 12.0 and
+// 13.1, 333x1001x1234 8.3 and 11.4.
+double pair_time(int64_t tiles, int nk, bool lines, bool tma_out, int clusters, int split) {
+  if (clusters <= 0) return 1e30;
+  const double block = lines ? 0.56 : 0.365;
+  if (split == 1)
+    return 4.5 + std::ceil(tiles / double(clusters)) * ((tma_out ? 1.0 : 6.0) + block * nk);
+  if (tiles > clusters || nk < 4 * split) return 1e30;
+  return 10.5 + block * ((nk + split - 1) / split);
+}
+
+// Pairs to a tile, 0: the lanes kernel.
+template <bool LINES>
+int choose_split(int64_t M, int64_t N, int nk, bool tma_out) {
   const int64_t sms = sm_count(), t = lanes_tokens(M);
   const int64_t pair_tiles = ((M + 255) / 256) * ((N + 255) / 256);
   const int64_t lane_tiles = ((M + t - 1) / t) * ((N + 127) / 128);
-  const uint32_t split = lanes_split(lane_tiles, nk);
-  const double pair_waves = std::ceil(pair_tiles / double(sms / 2));
-  const double lane_waves = std::ceil(lane_tiles * split / double(2 * sms));
-  const double pair_us = 1.0 + pair_waves * ((tma_out ? 1.0 : 6.0) + 0.45 * nk);
-  const double lane_us = (split > 1 ? 3.0 : 0.0) +
-                         lane_waves * (0.5 + (t == 64 ? 0.85 : 0.55) * nk / split);
-  return pair_us < lane_us;
+  const uint32_t share = lanes_split(lane_tiles, nk);
+  const double lane_waves = std::ceil(lane_tiles * share / double(2 * sms));
+  double best = (share > 1 ? 3.0 : 0.0) +
+                lane_waves * (3.0 + (t == 64 ? 0.7 : 0.55) * nk / share);
+  int split = 0;
+  for (int s = 1; s <= P_MAX_SPLIT; ++s) {
+    if (s > 1 && pair_tiles * s > sms / 2) break;
+    const double us = pair_time(pair_tiles, nk, LINES, tma_out, pair_clusters<LINES>(s), s);
+    if (us < best) {
+      best = us;
+      split = s;
+    }
+  }
+  return split;
 }
 
 template <int T>
@@ -1074,11 +1244,9 @@ mxq_status launch_lanes(const void* A, const void* B, int64_t K, FArgs a, void* 
 
 template <bool LINES>
 mxq_status launch_pair(const void* A, const void* B, int64_t K, const FArgs& f, uint32_t idesc_fmt,
-                       void* stream) {
+                       int split, void* stream) {
   CUtensorMap ta, tb;
   if (!code_map(&ta, A, f.M, K, 128) || !code_map(&tb, B, f.N, K, 64)) return MXQ_ERR_CUDA;
-  const void* kernel = reinterpret_cast<const void*>(fp8_gemm_pair<LINES>);
-  if (!ensure_dynamic_smem(kernel, Pair<LINES>::SMEM)) return MXQ_ERR_CUDA;
   PArgs p = {};
   p.f = f;
   p.f.idesc_fmt = idesc_fmt;
@@ -1087,6 +1255,7 @@ mxq_status launch_pair(const void* A, const void* B, int64_t K, const FArgs& f, 
   p.n_mp = static_cast<int32_t>(n_mp);
   p.n_nt = static_cast<int32_t>(n_nt);
   p.n_tiles = p.n_mp * p.n_nt;
+  p.split = split;
   choose_raster(p.n_mp, p.n_nt, double(f.M) * K, double(f.N) * K, 256.0 * K, p.group, p.group_n);
   const int e = f.out_bf16 ? 2 : 4;
   CUtensorMap tc = {};
@@ -1098,25 +1267,16 @@ mxq_status launch_pair(const void* A, const void* B, int64_t K, const FArgs& f, 
                     static_cast<uint64_t>(f.N * e), static_cast<uint32_t>(128 / e), 128,
                     CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_NONE) != CUDA_SUCCESS)
     return MXQ_ERR_CUDA;
-  cudaLaunchConfig_t cfg = {};
   cudaLaunchAttribute attr[2];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = 2;
-  attr[0].val.clusterDim.y = 1;
-  attr[0].val.clusterDim.z = 1;
-  // persistent grid: it may start while the previous kernel on the stream
-  // drains, and waits for it in the kernel
-  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[1].val.programmaticStreamSerializationAllowed = 1;
-  cfg.blockDim = dim3(P_THREADS, 1, 1);
-  cfg.dynamicSmemBytes = Pair<LINES>::SMEM;
-  cfg.stream = static_cast<cudaStream_t>(stream);
-  cfg.attrs = attr;
-  cfg.numAttrs = 2;
-  const int clusters = pair_clusters<LINES>(cfg);
+  cudaLaunchConfig_t cfg = pair_config<LINES>(attr, split, stream);
+  const int clusters = pair_clusters<LINES>(split);
   if (clusters <= 0) return MXQ_ERR_CUDA;
-  cfg.gridDim = dim3(static_cast<unsigned>(2 * std::min(p.n_tiles, clusters)), 1, 1);
-  if (cudaLaunchKernelEx(&cfg, fp8_gemm_pair<LINES>, ta, tb, tc, p) != cudaSuccess) {
+  const int tiles = split > 1 ? p.n_tiles : std::min(p.n_tiles, clusters);
+  cfg.gridDim = dim3(static_cast<unsigned>(tiles * 2 * split), 1, 1);
+  const cudaError_t e_launch =
+      split > 1 ? cudaLaunchKernelEx(&cfg, fp8_gemm_pair<LINES, true>, ta, tb, tc, p)
+                : cudaLaunchKernelEx(&cfg, fp8_gemm_pair<LINES, false>, ta, tb, tc, p);
+  if (e_launch != cudaSuccess) {
     cudaGetLastError();
     return MXQ_ERR_CUDA;
   }
@@ -1172,10 +1332,13 @@ extern "C" mxq_status mxq_fp8_gemm(const void* A, const float* sA, int fmt_a, co
   a.out_bf16 = out_dtype == MXQ_OUT_BF16;
   a.timeout_ns = wait_timeout_ns();
   const uint32_t e5a = fmt_a == MXQ_E5M2, e5b = fmt_b == MXQ_E5M2;
-  if (pairs_win(M, N, a.nk, N * (a.out_bf16 ? 2 : 4) % 16 == 0)) {
+  const bool tma_out = N * (a.out_bf16 ? 2 : 4) % 16 == 0;
+  const int split = a.tiles ? choose_split<false>(M, N, a.nk, tma_out)
+                            : choose_split<true>(M, N, a.nk, tma_out);
+  if (split) {
     const uint32_t types = e5a << 7 | e5b << 10;
-    return a.tiles ? launch_pair<false>(A, B, K, a, types, stream)
-                   : launch_pair<true>(A, B, K, a, types, stream);
+    return a.tiles ? launch_pair<false>(A, B, K, a, types, split, stream)
+                   : launch_pair<true>(A, B, K, a, types, split, stream);
   }
   // the lines of B are the MMA's rows (its A operand)
   a.idesc_fmt = e5b << 7 | e5a << 10;

@@ -253,3 +253,17 @@ def test_runs_on_the_current_stream():
     B, sB, _, _ = mxq.fp8_quantize_tiles(w)
     assert torch.equal(c, mxq.fp8_gemm(A, sA, B, sB, 600, 384, 512, out_dtype=torch.float32))
     mxq.check()
+
+
+# few tiles and a long K: two, three and four CTA pairs share a tile
+SHARED = [(1024, 2100, 2900), (500, 2600, 1700), (300, 520, 4096), (257, 513, 2061), (700, 2049, 3600)]
+
+
+@pytest.mark.parametrize("kind", ["tile", "line"])
+@pytest.mark.parametrize("shape", SHARED, ids=lambda s: "x".join(map(str, s)))
+def test_product_of_few_tiles_and_long_k(shape, kind):
+    m, n, k = shape
+    ops = _operands(m, n, k, "e4m3", "e5m2", kind, m + n)
+    first = _check(ops, m, n, k, "e4m3", "e5m2", kind, torch.float32)
+    _check(ops, m, n, k, "e4m3", "e5m2", kind, torch.bfloat16)
+    assert np.array_equal(_product(ops, m, n, k, "e4m3", "e5m2", kind, torch.float32), first)
