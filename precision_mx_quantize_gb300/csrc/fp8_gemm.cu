@@ -456,7 +456,6 @@ struct PArgs {
   FArgs f;
   int32_t n_mp, n_nt, n_tiles;   // 256-row and 256-column tiles
   int32_t group, group_n;        // tile order (tile_coords)
-  int32_t tma_out;               // rows of C are 16-byte multiples: tiles leave by TMA
   int32_t split;                 // pairs of a cluster that share a tile's K blocks
 };
 
@@ -607,31 +606,62 @@ MXQ_DEV void stage_out(const float (&acc)[128], uint32_t out, int quad, int lane
   }
 }
 
+MXQ_DEV uint32_t lds16(uint32_t addr) {
+  uint16_t v;
+  asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v) : "r"(addr));
+  return v;
+}
+
 // Copies a staged pass out to rows of C that no tensor map can describe (not
 // 16-byte multiples): each warp its 32 rows, neighbouring lanes neighbouring
-// columns.  bf16 goes in pairs where N is even.
-MXQ_DEV void copy_out(const FArgs& a, uint32_t out, int quad, int lane, int64_t row0, int64_t col0,
-                      bool bf16) {
-  const bool pairs = bf16 && a.N % 2 == 0;
-  const int per = pairs ? 2 : 1, steps = bf16 && !pairs ? 4 : 2, shift = bf16 ? 1 : 2;
-#pragma unroll 4
-  for (int i = 0; i < 32; ++i) {
-    const int r = quad * 32 + i;
-    const int64_t to = (row0 + r) * a.N + col0;
+// columns, in 4-byte stores (bf16 with an odd N: from the row's first even place
+// in C on).  Four rows are read before any is stored: where each store waited
+// for its own shared-memory load, 4096x4095x512 with fp32 out took 79 us against
+// 44 (sixteen rows 48; 4096x4096x512, by TMA, 21).
+template <bool BF16>
+MXQ_DEV void copy_out(const FArgs& a, uint32_t out, int quad, int lane, int64_t row0,
+                      int64_t col0) {
+  constexpr int ROWS = 4;
+  const bool odd = BF16 && (a.N & 1);
+#pragma unroll 1
+  for (int i0 = 0; i0 < 32; i0 += ROWS) {
+    uint32_t v[ROWS][2], head[ROWS];
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      const int c = (k * 32 + lane) * per, byte = c << shift;
-      if (k >= steps || row0 + r >= a.M || col0 + c >= a.N) continue;
-      const uint32_t at = out + (byte >> 7) * 16384 + r * 128 + ((byte & 127) ^ ((r & 7) << 4));
-      if (bf16 && !pairs) {
-        uint16_t v;
-        asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v) : "r"(at));
-        static_cast<uint16_t*>(a.C)[to + c] = v;
+    for (int i = 0; i < ROWS; ++i) {
+      const int r = quad * 32 + i0 + i, skew = (r & 7) << 4;
+      const int shift = odd ? static_cast<int>((row0 + r) & 1) : 0;   // col0 * 2 is even
+      auto at = [&](int byte) { return out + (byte >> 7) * 16384 + r * 128 + ((byte & 127) ^ skew); };
+      head[i] = odd ? lds16(at(0)) : 0u;
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        const int byte = (k * 32 + lane) * 4 + 2 * shift;
+        if (odd)
+          v[i][k] = lds16(at(byte)) | lds16(at(min(byte + 2, 254))) << 16;
+        else
+          v[i][k] = __float_as_uint(lds32(at(byte)));
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < ROWS; ++i) {
+      const int64_t row = row0 + quad * 32 + i0 + i;
+      const int shift = odd ? static_cast<int>(row & 1) : 0;
+      if (row >= a.M) continue;
+      if constexpr (BF16) {
+        uint16_t* to = static_cast<uint16_t*>(a.C) + row * a.N + col0;
+        if (shift && lane == 0) to[0] = static_cast<uint16_t>(head[i]);
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          const int c = (k * 32 + lane) * 2 + shift;
+          if (c < 127 && col0 + c + 1 < a.N)
+            *reinterpret_cast<uint32_t*>(to + c) = v[i][k];
+          else if (c < 128 && col0 + c < a.N)
+            to[c] = static_cast<uint16_t>(v[i][k]);
+        }
       } else {
-        uint32_t v;
-        asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(at));
-        if (bf16) *reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(a.C) + to + c) = v;
-        else static_cast<uint32_t*>(a.C)[to + c] = v;
+        uint32_t* to = static_cast<uint32_t*>(a.C) + row * a.N + col0;
+#pragma unroll
+        for (int k = 0; k < 2; ++k)
+          if (col0 + k * 32 + lane < a.N) to[k * 32 + lane] = v[i][k];
       }
     }
   }
@@ -705,14 +735,20 @@ MXQ_DEV void tma_store_2d(const CUtensorMap* map, uint32_t src, int32_t x, int32
                : "memory");
 }
 
-// SPLIT: a.split pairs of a cluster share the K blocks of one tile and join their
-// sums in order through distributed shared memory.
-template <bool LINES, bool SPLIT>
+// How the sums of a tile leave: by TMA where the rows of C are 16-byte multiples,
+// else copied; or shared, by p.split pairs of a cluster that take a part of the
+// K blocks each and join their sums in order through distributed shared memory.
+// A kernel each: with the copies in it, the one for TMA spilled registers
+// (8192x6144x4096 153 us against 151).
+enum : int { P_TMA = 0, P_COPY = 1, P_SHARED = 2 };
+
+template <bool LINES, int OUT>
 __global__ void __launch_bounds__(P_THREADS, 1)
     fp8_gemm_pair(const __grid_constant__ CUtensorMap ta, const __grid_constant__ CUtensorMap tb,
                   const __grid_constant__ CUtensorMap tc, const PArgs p) {
   using P = Pair<LINES>;
   constexpr int S = P::STAGES, PITCH = part_pitch<LINES>();
+  constexpr bool SPLIT = OUT == P_SHARED;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~static_cast<uintptr_t>(1023));
@@ -742,7 +778,7 @@ __global__ void __launch_bounds__(P_THREADS, 1)
   if (threadIdx.x == 0) {
     prefetch_tmap(&ta);
     prefetch_tmap(&tb);
-    if (p.tma_out) prefetch_tmap(&tc);
+    if (OUT == P_TMA) prefetch_tmap(&tc);
     for (int s = 0; s < S; ++s) {
       mbar_init(smem_u32(&full[s]), 1);    // leader: one arrival, bytes of both CTAs
       mbar_init(smem_u32(&empty[s]), 1);
@@ -1035,8 +1071,9 @@ __global__ void __launch_bounds__(P_THREADS, 1)
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
         asm volatile("bar.sync %0, 128;" ::"r"(1 + h) : "memory");
         const int wide = bf16 ? 64 : 32, x = col0 + 64 * pass;
-        if (!p.tma_out) {
-          copy_out(a, mine, quad, lane, row0, x, bf16);
+        if constexpr (OUT == P_COPY) {
+          if (bf16) copy_out<true>(a, mine, quad, lane, row0, x);
+          else copy_out<false>(a, mine, quad, lane, row0, x);
         } else if (first && row0 < a.M) {
           if (x < a.N) tma_store_2d(&tc, mine, x, row0);
           if (x + wide < a.N) tma_store_2d(&tc, mine + 16384, x + wide, row0);
@@ -1111,9 +1148,16 @@ cudaLaunchConfig_t pair_config(cudaLaunchAttribute* attr, int split, void* strea
   return cfg;
 }
 
+template <bool LINES>
+auto pair_kernel(int out) {
+  return out == P_TMA    ? fp8_gemm_pair<LINES, P_TMA>
+         : out == P_COPY ? fp8_gemm_pair<LINES, P_COPY>
+                         : fp8_gemm_pair<LINES, P_SHARED>;
+}
+
 // Clusters of `split` pairs that fit on the device at once, cached per device;
-// 0 if they cannot be had, or if the kernel was built with fewer registers than
-// its warpgroups share out among themselves.
+// 0 if they cannot be had, or if a kernel was built with fewer registers than its
+// warpgroups share out among themselves.
 template <bool LINES>
 int pair_clusters(int split) {
   static std::mutex mu;
@@ -1123,19 +1167,22 @@ int pair_clusters(int split) {
   std::lock_guard<std::mutex> lock(mu);
   int& known = cached[dev][split];
   if (known == 0) {
-    const auto kernel = split > 1 ? fp8_gemm_pair<LINES, true> : fp8_gemm_pair<LINES, false>;
-    cudaFuncAttributes fa;
-    if (!ensure_dynamic_smem(reinterpret_cast<const void*>(kernel), Pair<LINES>::SMEM) ||
-        cudaFuncGetAttributes(&fa, kernel) != cudaSuccess || fa.numRegs < P_MIN_REGS) {
-      cudaGetLastError();
-      return 0;
+    for (int out = split > 1 ? P_SHARED : P_TMA; out <= (split > 1 ? P_SHARED : P_COPY); ++out) {
+      cudaFuncAttributes fa;
+      if (!ensure_dynamic_smem(reinterpret_cast<const void*>(pair_kernel<LINES>(out)),
+                               Pair<LINES>::SMEM) ||
+          cudaFuncGetAttributes(&fa, pair_kernel<LINES>(out)) != cudaSuccess ||
+          fa.numRegs < P_MIN_REGS) {
+        cudaGetLastError();
+        return 0;
+      }
     }
     cudaLaunchAttribute attr[2];
     cudaLaunchConfig_t cfg = pair_config<LINES>(attr, split, nullptr);
     cfg.numAttrs = 1;   // the cluster dimension
     cfg.gridDim = dim3(static_cast<unsigned>(sm_count() / (2 * split) * 2 * split), 1, 1);
     int n = 0;
-    if (cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) != cudaSuccess || n < 0) {
+    if (cudaOccupancyMaxActiveClusters(&n, pair_kernel<LINES>(split > 1 ? P_SHARED : P_TMA), &cfg) != cudaSuccess || n < 0) {
       cudaGetLastError();
       n = split > 1 ? 0 : sm_count() / 2;
     }
@@ -1259,8 +1306,8 @@ mxq_status launch_pair(const void* A, const void* B, int64_t K, const FArgs& f, 
   choose_raster(p.n_mp, p.n_nt, double(f.M) * K, double(f.N) * K, 256.0 * K, p.group, p.group_n);
   const int e = f.out_bf16 ? 2 : 4;
   CUtensorMap tc = {};
-  p.tma_out = f.N * e % 16 == 0;
-  if (p.tma_out &&
+  const int out = split > 1 ? P_SHARED : f.N * e % 16 == 0 ? P_TMA : P_COPY;
+  if (out == P_TMA &&
       tensor_map_2d(&tc, f.out_bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
                                     : CU_TENSOR_MAP_DATA_TYPE_FLOAT32,
                     f.C, static_cast<uint64_t>(f.N), static_cast<uint64_t>(f.M),
@@ -1273,10 +1320,7 @@ mxq_status launch_pair(const void* A, const void* B, int64_t K, const FArgs& f, 
   if (clusters <= 0) return MXQ_ERR_CUDA;
   const int tiles = split > 1 ? p.n_tiles : std::min(p.n_tiles, clusters);
   cfg.gridDim = dim3(static_cast<unsigned>(tiles * 2 * split), 1, 1);
-  const cudaError_t e_launch =
-      split > 1 ? cudaLaunchKernelEx(&cfg, fp8_gemm_pair<LINES, true>, ta, tb, tc, p)
-                : cudaLaunchKernelEx(&cfg, fp8_gemm_pair<LINES, false>, ta, tb, tc, p);
-  if (e_launch != cudaSuccess) {
+  if (cudaLaunchKernelEx(&cfg, pair_kernel<LINES>(out), ta, tb, tc, p) != cudaSuccess) {
     cudaGetLastError();
     return MXQ_ERR_CUDA;
   }
