@@ -38,12 +38,11 @@
 // accumulators, so a K block takes 800 (1250 with line scales).  Three of 160
 // columns were slower still: the accumulation warps' fixed cost per block
 // weighs more (8192x6144x4096 176 us); so were sixteen accumulation warps of 64
-// columns (165 us, and 913-946 with line scales).  In runs of seconds the card's
-// power limit (1400 W) binds as well and both shapes below take 5 % longer.
-// Measured: 8192x6144x4096, tile scales,
-// bf16 out 149 us (2.77 PFLOP/s, 0.71 of twice the bf16 rate; the MMAs alone,
-// nothing read back, 118 us); 28672x4096x8192, line scales, fp32 out 943 us
-// (2.04 PFLOP/s, 0.53).
+// columns (165 us; with line scales no different).  In runs of seconds the
+// card's power limit (1400 W) binds as well, for 5 % more.  Measured:
+// 8192x6144x4096, tile scales, bf16 out 151 us (2.73 PFLOP/s, 0.70 of twice the
+// bf16 rate; the MMAs alone, nothing read back, 118 us); 28672x4096x8192, line
+// scales, fp32 out 935-980 us (2.0 PFLOP/s, 0.52).
 #include <string.h>
 
 #include <mutex>
