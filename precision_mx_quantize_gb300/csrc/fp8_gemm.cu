@@ -611,12 +611,18 @@ MXQ_DEV uint32_t lds16(uint32_t addr) {
   return v;
 }
 
+// An element that copy_out is about to store; its row and column are in C.
+MXQ_DEV bool copy_in_bounds(const FArgs& a, int64_t row, int64_t col) {
+  return MXQ_IN_BOUNDS(row < a.M && col < a.N, &g_err_fp8_gemm, SITE_B_FP8_GEMM);
+}
+
 // Copies a staged pass out to rows of C that no tensor map can describe (not
 // 16-byte multiples): each warp its 32 rows, neighbouring lanes neighbouring
 // columns, in 4-byte stores (bf16 with an odd N: from the row's first even place
 // in C on).  Four rows are read before any is stored: where each store waited
 // for its own shared-memory load, 4096x4095x512 with fp32 out took 79 us against
-// 44 (sixteen rows 48; 4096x4096x512, by TMA, 21).
+// 44 (sixteen rows 48; 4096x4096x512, by TMA, 21).  col0 < N: the first element of
+// an odd row is stored without a test of its column.
 template <bool BF16>
 MXQ_DEV void copy_out(const FArgs& a, uint32_t out, int quad, int lane, int64_t row0,
                       int64_t col0) {
@@ -647,20 +653,24 @@ MXQ_DEV void copy_out(const FArgs& a, uint32_t out, int quad, int lane, int64_t 
       if (row >= a.M) continue;
       if constexpr (BF16) {
         uint16_t* to = static_cast<uint16_t*>(a.C) + row * a.N + col0;
-        if (shift && lane == 0) to[0] = static_cast<uint16_t>(head[i]);
+        if (shift && lane == 0 && copy_in_bounds(a, row, col0))
+          to[0] = static_cast<uint16_t>(head[i]);
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
           const int c = (k * 32 + lane) * 2 + shift;
-          if (c < 127 && col0 + c + 1 < a.N)
-            *reinterpret_cast<uint32_t*>(to + c) = v[i][k];
-          else if (c < 128 && col0 + c < a.N)
-            to[c] = static_cast<uint16_t>(v[i][k]);
+          if (c < 127 && col0 + c + 1 < a.N) {
+            if (copy_in_bounds(a, row, col0 + c + 1))
+              *reinterpret_cast<uint32_t*>(to + c) = v[i][k];
+          } else if (c < 128 && col0 + c < a.N) {
+            if (copy_in_bounds(a, row, col0 + c)) to[c] = static_cast<uint16_t>(v[i][k]);
+          }
         }
       } else {
         uint32_t* to = static_cast<uint32_t*>(a.C) + row * a.N + col0;
 #pragma unroll
         for (int k = 0; k < 2; ++k)
-          if (col0 + k * 32 + lane < a.N) to[k * 32 + lane] = v[i][k];
+          if (col0 + k * 32 + lane < a.N && copy_in_bounds(a, row, col0 + k * 32 + lane))
+            to[k * 32 + lane] = v[i][k];
       }
     }
   }
@@ -1071,8 +1081,10 @@ __global__ void __launch_bounds__(P_THREADS, 1)
         asm volatile("bar.sync %0, 128;" ::"r"(1 + h) : "memory");
         const int wide = bf16 ? 64 : 32, x = col0 + 64 * pass;
         if constexpr (OUT == P_COPY) {
-          if (bf16) copy_out<true>(a, mine, quad, lane, row0, x);
-          else copy_out<false>(a, mine, quad, lane, row0, x);
+          if (x < a.N) {   // the tile's right part may lie past N whole
+            if (bf16) copy_out<true>(a, mine, quad, lane, row0, x);
+            else copy_out<false>(a, mine, quad, lane, row0, x);
+          }
         } else if (first && row0 < a.M) {
           if (x < a.N) tma_store_2d(&tc, mine, x, row0);
           if (x + wide < a.N) tma_store_2d(&tc, mine + 16384, x + wide, row0);
