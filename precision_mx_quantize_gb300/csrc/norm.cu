@@ -39,6 +39,7 @@ struct NArgs {
   float* scales;
   int64_t rows, cols, pitch, lines;
   float eps;
+  int32_t center;     // LAYER kernels: 0 for an RMS norm with a bias, whose mean is taken as 0
   int32_t vec;
   int32_t slots;      // norm_ring: rows in flight
   uint64_t timeout_ns;
@@ -110,7 +111,7 @@ __global__ void __launch_bounds__(256) norm_rows(const NArgs a) {
 #pragma unroll
       for (int j = 0; j < 8; ++j) s += f[j];
     }
-    mean = cta_sum(s, buf) * inv_n;
+    mean = a.center ? cta_sum(s, buf) * inv_n : 0.0f;
   }
   float s = 0.0f;
   for (int64_t c = threadIdx.x; c < n_chunks; c += blockDim.x) {
@@ -205,6 +206,7 @@ __global__ void __launch_bounds__(WARP ? 256 : 512) norm_regs(const NArgs a) {
 #pragma unroll
       for (int j = 0; j < 8; ++j) s += raw[i][j];   // zero past the row's end
     mean = row_sum(s, 0) * inv_n;
+    if (!a.center) mean = 0.0f;
     s = 0.0f;
   }
 #pragma unroll
@@ -314,6 +316,7 @@ __global__ void __launch_bounds__(512) norm_ring(const NArgs a) {
 #pragma unroll
         for (int j = 0; j < 8; ++j) s += raw[i][j];   // zero past the row's end
       mean = row_sum(s, 0) * inv_n;
+      if (!a.center) mean = 0.0f;
       s = 0.0f;
     }
 #pragma unroll
@@ -478,6 +481,10 @@ extern "C" mxq_status mxq_norm_forward(const mxq_norm_args* p, void* stream) {
   a.lines = fp8_lines(p->rows);
   a.eps = p->eps;
   a.vec = p->cols % 8 == 0;
-  return dispatch(p->x_dtype, p->w_dtype, p->kind,
+  // The kernels without a mean hold no bias in registers: an RMS norm with one
+  // runs those of the layer norm.
+  a.center = p->kind == MXQ_NORM_LAYER;
+  const int kind = p->bias ? MXQ_NORM_LAYER : p->kind;
+  return dispatch(p->x_dtype, p->w_dtype, kind,
                   Forward{a, p->fmt, static_cast<cudaStream_t>(stream)});
 }
