@@ -486,6 +486,16 @@ void mxq_set_wait_timeout_ns(uint64_t ns);
  */
 mxq_status mxq_debug_expire_wait(uint64_t limit_ns, void* stream);
 
+/*
+ * Test hook: mxq_fp8_gemm in a kernel of the caller's choice, whatever the
+ * sizes.  pairs: 0, 128 lines of B by up to 64 lines of A on one CTA; 1 to 4,
+ * 256x256 tiles with that many CTA pairs to each.  MXQ_ERR_ARG where the pairs
+ * outnumber the K blocks or do not fit the device together.
+ */
+mxq_status mxq_debug_fp8_gemm(const void* A, const float* sA, int fmt_a, const void* B,
+                              const float* sB, int fmt_b, int b_scales, int64_t M, int64_t N,
+                              int64_t K, void* C, int out_dtype, int pairs, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

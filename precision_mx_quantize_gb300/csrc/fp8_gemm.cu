@@ -1338,25 +1338,12 @@ mxq_status launch_pair(const void* A, const void* B, int64_t K, const FArgs& f, 
   return launch_status();
 }
 
-}  // namespace
+// The kernel of a product: F_CHOOSE, 0 for lanes, or the pairs to a tile.
+constexpr int F_CHOOSE = -1;
 
-uint32_t take_fp8_gemm_error() {
-  uint32_t h = 0;
-  if (cudaMemcpyFromSymbol(&h, g_err_fp8_gemm, sizeof(h)) != cudaSuccess) return MXQ_ERR_CUDA;
-  if (h) {
-    const uint32_t z = 0;
-    cudaMemcpyToSymbol(g_err_fp8_gemm, &z, sizeof(z));
-  }
-  return h;
-}
-
-}  // namespace mxq
-
-using namespace mxq;
-
-extern "C" mxq_status mxq_fp8_gemm(const void* A, const float* sA, int fmt_a, const void* B,
-                                   const float* sB, int fmt_b, int b_scales, int64_t M, int64_t N,
-                                   int64_t K, void* C, int out_dtype, void* stream) {
+mxq_status product(const void* A, const float* sA, int fmt_a, const void* B, const float* sB,
+                   int fmt_b, int b_scales, int64_t M, int64_t N, int64_t K, void* C,
+                   int out_dtype, int form, void* stream) {
   const int64_t lim = int64_t(1) << 31;
   if (M < 0 || N < 0 || K < 0 || M >= lim || N >= lim || K >= lim) return MXQ_ERR_ARG;
   if (!is_fp8(fmt_a) || !is_fp8(fmt_b)) return MXQ_ERR_ARG;
@@ -1387,9 +1374,15 @@ extern "C" mxq_status mxq_fp8_gemm(const void* A, const float* sA, int fmt_a, co
   a.out_bf16 = out_dtype == MXQ_OUT_BF16;
   a.timeout_ns = wait_timeout_ns();
   const uint32_t e5a = fmt_a == MXQ_E5M2, e5b = fmt_b == MXQ_E5M2;
-  const bool tma_out = N * (a.out_bf16 ? 2 : 4) % 16 == 0;
-  const int split = a.tiles ? choose_split<false>(M, N, a.nk, tma_out)
-                            : choose_split<true>(M, N, a.nk, tma_out);
+  int split = form;
+  if (form == F_CHOOSE) {
+    const bool tma_out = N * (a.out_bf16 ? 2 : 4) % 16 == 0;
+    split = a.tiles ? choose_split<false>(M, N, a.nk, tma_out)
+                    : choose_split<true>(M, N, a.nk, tma_out);
+  } else if (split > 0) {
+    const int clusters = a.tiles ? pair_clusters<false>(split) : pair_clusters<true>(split);
+    if (a.nk < split || clusters <= 0) return MXQ_ERR_ARG;
+  }
   if (split) {
     const uint32_t types = e5a << 7 | e5b << 10;
     return a.tiles ? launch_pair<false>(A, B, K, a, types, split, stream)
@@ -1402,4 +1395,34 @@ extern "C" mxq_status mxq_fp8_gemm(const void* A, const float* sA, int fmt_a, co
     case 32: return launch_lanes<32>(A, B, K, a, stream);
     default: return launch_lanes<64>(A, B, K, a, stream);
   }
+}
+
+}  // namespace
+
+uint32_t take_fp8_gemm_error() {
+  uint32_t h = 0;
+  if (cudaMemcpyFromSymbol(&h, g_err_fp8_gemm, sizeof(h)) != cudaSuccess) return MXQ_ERR_CUDA;
+  if (h) {
+    const uint32_t z = 0;
+    cudaMemcpyToSymbol(g_err_fp8_gemm, &z, sizeof(z));
+  }
+  return h;
+}
+
+}  // namespace mxq
+
+using namespace mxq;
+
+extern "C" mxq_status mxq_fp8_gemm(const void* A, const float* sA, int fmt_a, const void* B,
+                                   const float* sB, int fmt_b, int b_scales, int64_t M, int64_t N,
+                                   int64_t K, void* C, int out_dtype, void* stream) {
+  return product(A, sA, fmt_a, B, sB, fmt_b, b_scales, M, N, K, C, out_dtype, F_CHOOSE, stream);
+}
+
+extern "C" mxq_status mxq_debug_fp8_gemm(const void* A, const float* sA, int fmt_a, const void* B,
+                                         const float* sB, int fmt_b, int b_scales, int64_t M,
+                                         int64_t N, int64_t K, void* C, int out_dtype, int pairs,
+                                         void* stream) {
+  if (pairs < 0 || pairs > P_MAX_SPLIT) return MXQ_ERR_ARG;
+  return product(A, sA, fmt_a, B, sB, fmt_b, b_scales, M, N, K, C, out_dtype, pairs, stream);
 }

@@ -81,6 +81,7 @@ SIGNATURES = [
     ("mxq_check", _I, [_P]),
     ("mxq_set_wait_timeout_ns", None, [_U64]),
     ("mxq_debug_expire_wait", _I, [_U64, _P]),
+    ("mxq_debug_fp8_gemm", _I, [_P, _P, _I, _P, _P, _I, _I, _I64, _I64, _I64, _P, _I, _I, _P]),
 ]
 
 class GemmProblem(ctypes.Structure):
