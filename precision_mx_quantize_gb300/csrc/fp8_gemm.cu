@@ -678,7 +678,7 @@ MXQ_DEV void copy_out(const FArgs& a, uint32_t out, int quad, int lane, int64_t 
 
 // Two neighbouring elements of C from an even column on.
 MXQ_DEV void store2(const FArgs& a, int64_t row, int64_t col, float x, float y) {
-  if (col >= a.N) return;
+  if (col >= a.N || !MXQ_IN_BOUNDS(row < a.M, &g_err_fp8_gemm, SITE_B_FP8_GEMM)) return;
   const int64_t at = row * a.N + col;
   const bool two = col + 1 < a.N;
   if (a.out_bf16) {

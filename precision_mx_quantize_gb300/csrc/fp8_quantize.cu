@@ -234,7 +234,8 @@ __global__ void __launch_bounds__(256, MODE == Q_TILES ? 3 : 4) fp8_quant_kernel
     float scale, mul;
     fp8_scale<FR>(bf16lo(mag2(m)), scale, mul);
     const int64_t n_rt = (a.rows + 127) / 128;
-    if (tid == 0) {
+    if (tid == 0 &&
+        MXQ_IN_BOUNDS(rt < n_rt && ct < a.n_ct, &g_err_fp8_quant, SITE_B_FP8_SCALES)) {
       a.scales_r[rt * a.n_ct + ct] = scale;
       if (a.codes_c) a.scales_c[ct * n_rt + rt] = scale;
     }

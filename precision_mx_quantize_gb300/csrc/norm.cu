@@ -48,6 +48,7 @@ struct NArgs {
 // The scale of block kb of row r; the last row also writes those of the
 // padding lines (an all-zero block's).
 MXQ_DEV void store_scale(const NArgs& a, int64_t kb, int64_t r, float scale) {
+  if (!MXQ_IN_BOUNDS(kb * F_BLOCK < a.cols && r < a.rows, &g_err_norm, SITE_B_NORM)) return;
   float* s = a.scales + kb * a.lines;
   s[r] = scale;
   if (r == a.rows - 1)
@@ -121,7 +122,7 @@ __global__ void __launch_bounds__(256) norm_rows(const NArgs a) {
       if (8 * c + j < cols) s += (f[j] - mean) * (f[j] - mean);
   }
   const float rstd = 1.0f / sqrtf(cta_sum(s, buf) * inv_n + a.eps);
-  if (threadIdx.x == 0) {
+  if (threadIdx.x == 0 && MXQ_IN_BOUNDS(r < a.rows, &g_err_norm, SITE_B_NORM)) {
     if (LAYER && a.mean) a.mean[r] = mean;
     if (a.rstd) a.rstd[r] = rstd;
   }
@@ -139,7 +140,8 @@ __global__ void __launch_bounds__(256) norm_rows(const NArgs a) {
       if (!vec)
         for (int j = 0; j < 8; ++j)
           if (8 * c + j >= cols) f[j] = 0.0f;
-      if (a.y) store8(static_cast<XT*>(a.y) + r * cols, 8 * c, cols, vec, f);
+      if (a.y && MXQ_IN_BOUNDS(r < a.rows && 8 * c < cols, &g_err_norm, SITE_B_NORM))
+        store8(static_cast<XT*>(a.y) + r * cols, 8 * c, cols, vec, f);
     }
     if constexpr (FMT >= 0) {
       float chunk[1][8];
@@ -222,7 +224,7 @@ __global__ void __launch_bounds__(WARP ? 256 : 512) norm_regs(const NArgs a) {
     }
   }
   const float rstd = 1.0f / sqrtf(row_sum(s, 1) * inv_n + a.eps);
-  if (t == 0) {
+  if (t == 0 && MXQ_IN_BOUNDS(r < a.rows, &g_err_norm, SITE_B_NORM)) {
     if (LAYER && a.mean) a.mean[r] = mean;
     if (a.rstd) a.rstd[r] = rstd;
   }
@@ -267,9 +269,12 @@ __global__ void __launch_bounds__(512) norm_ring(const NArgs a) {
   griddep_wait();
   griddep_launch_dependents();
   auto fetch = [&](int64_t r, int slot) {   // one thread
-    if (r >= a.rows || !MXQ_IN_BOUNDS(slot < slots, &g_err_norm, SITE_B_NORM)) return;
+    if (r >= a.rows) return;
     const uint32_t bar = smem_u32(&full[slot]);
     const RowCopy<XT, VEC> c(all, r, a.rows, a.cols);
+    if (!MXQ_IN_BOUNDS(slot < slots && c.inside(all, n) && c.bytes <= row_bytes, &g_err_norm,
+                       SITE_B_NORM))
+      return;
     mbar_arrive_expect_tx(bar, c.bytes);
     bulk_load(smem_u32(ring) + slot * row_bytes, c.src, c.bytes, bar);
   };

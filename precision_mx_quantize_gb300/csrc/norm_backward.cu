@@ -27,6 +27,11 @@ struct NGrad {
   uint64_t timeout_ns;
 };
 
+// This CTA's set of partial sums is one of those the workspace holds.
+MXQ_DEV bool part_in_bounds(const NGrad& a) {
+  return MXQ_IN_BOUNDS(blockIdx.x < a.splits, &g_err_norm_grad, SITE_B_NORM_GRAD);
+}
+
 // dx of one row per CTA (rows of any length).
 template <typename XT, typename WT, bool LAYER>
 __global__ void __launch_bounds__(256) norm_grad_rows(const NGrad a) {
@@ -59,7 +64,8 @@ __global__ void __launch_bounds__(256) norm_grad_rows(const NGrad a) {
 #pragma unroll
     for (int j = 0; j < 8; ++j)
       f[j] = rstd * (g[j] * wf[j] - c1 - (f[j] - mean) * rstd * c2);
-    store8(static_cast<XT*>(a.dx) + r * cols, 8 * c, cols, vec, f);
+    if (MXQ_IN_BOUNDS(r < a.rows && 8 * c < cols, &g_err_norm_grad, SITE_B_NORM_GRAD))
+      store8(static_cast<XT*>(a.dx) + r * cols, 8 * c, cols, vec, f);
   }
 }
 
@@ -155,7 +161,7 @@ __global__ void __launch_bounds__(256) norm_grad_regs(const NGrad a) {
       for (int q = 0; q < 8; ++q) v += sums[q * 8 * I * 32 + e];
       // element e: lane e % 32, chunk and place e / 32
       const int c = 8 * ((e & 31) + (e >> 8) * 32) + ((e >> 5) & 7);
-      if (c < cols) part[k * cols + c] = v;
+      if (c < cols && part_in_bounds(a)) part[k * cols + c] = v;
     }
   }
 }
@@ -186,9 +192,13 @@ __global__ void __launch_bounds__(512) norm_grad_ring(const NGrad a) {
   griddep_wait();
   griddep_launch_dependents();
   auto fetch = [&](int64_t r, int slot) {   // one thread
-    if (r >= a.rows || !MXQ_IN_BOUNDS(slot < slots, &g_err_norm_grad, SITE_B_NORM_GRAD)) return;
+    if (r >= a.rows) return;
     const uint32_t bar = smem_u32(&full[slot]), dst = smem_u32(ring) + slot * slot_bytes;
     const RowCopy<XT, VEC> cx(all_x, r, a.rows, a.cols), cd(all_dy, r, a.rows, a.cols);
+    if (!MXQ_IN_BOUNDS(slot < slots && cx.inside(all_x, n) && cd.inside(all_dy, n) &&
+                           cx.bytes <= row_bytes,
+                       &g_err_norm_grad, SITE_B_NORM_GRAD))
+      return;
     mbar_arrive_expect_tx(bar, cx.bytes + cd.bytes);
     bulk_load(dst, cx.src, cx.bytes, bar);
     bulk_load(dst + row_bytes, cd.src, cd.bytes, bar);
@@ -304,7 +314,7 @@ __global__ void __launch_bounds__(512) norm_grad_ring(const NGrad a) {
 #pragma unroll
   for (int i = 0; i < I; ++i) {
     const int c = 8 * (t + i * nt);
-    if (c >= cols) break;
+    if (c >= cols || !part_in_bounds(a)) break;
     store8(part, c, cols, VEC, dw[i]);
     if constexpr (DB_SHARED) {
       const float4 lo = db_at[2 * i * nt], hi = db_at[(2 * i + 1) * nt];
@@ -332,6 +342,8 @@ __global__ void __launch_bounds__(256) norm_grad_cols(const NGrad a) {
     db += g;
   }
   float* p = a.part + int64_t(blockIdx.y) * 2 * a.cols;
+  if (!MXQ_IN_BOUNDS(c < a.cols && blockIdx.y < a.splits, &g_err_norm_grad, SITE_B_NORM_GRAD))
+    return;
   p[c] = dw;
   p[a.cols + c] = db;
 }

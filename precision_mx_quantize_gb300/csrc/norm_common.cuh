@@ -235,6 +235,10 @@ struct RowCopy {
       bytes = static_cast<uint32_t>((end - first) * sizeof(XT));
     }
   }
+  // Whether the copy lies in the n elements from x on.
+  MXQ_DEV bool inside(const XT* x, int64_t n) const {
+    return src >= x && src + bytes / sizeof(XT) <= x + n;
+  }
 };
 
 MXQ_DEV float warp_sum(float v) {
