@@ -396,6 +396,13 @@ mxq_status mxq_fp8_quantize_tiles(const void* x, int64_t rows, int64_t cols, int
  * MXQ_OUT_BF16, 16-byte aligned.  Any M, N, K below 2^31: M == 0 or N == 0 is
  * a no-op, K == 0 writes zeros.  The bytes between K and the pitch are not
  * read.  No workspace.
+ * Range of the scales: which of the three factors of a block meet first depends
+ * on the sizes.  C is as exact as the fp32 sums are where sA * sB, and the
+ * inner sum times sB, are normal fp32 values (or the sum is zero).  A product
+ * sA * sB below 2^-126 may be rounded to a multiple of 2^-149, which leaves an
+ * error of up to 2^-150 times the inner sum; a block of zeros, whose scale is
+ * 2^-126, adds zero all the same.  Where sA * sB is 2^128 or more, C may be
+ * infinite or NaN.
  */
 mxq_status mxq_fp8_gemm(const void* A, const float* sA, int fmt_a, const void* B, const float* sB,
                         int fmt_b, int b_scales, int64_t M, int64_t N, int64_t K, void* C,

@@ -503,7 +503,12 @@ MXQ_DEV uint32_t step16(int c) {
   return LINES ? (c >> 1) * 32 + (static_cast<uint32_t>((c & 1) * 16) << 16) : 16 * c;
 }
 
-// acc += s * v for a row of tile scales.
+// acc += s * v for a row of tile scales.  s is the product of the row's scale and
+// the tile's, formed once for the row's 128 columns: one operation an element.
+// A subnormal s has lost digits, an infinite one makes a NaN of a zero sum; the
+// header states that range.  Taking the factors in turn where s is not normal
+// cost every call a tenth (8192x6144x4096: 169 us against 152) and those with
+// rows of zeros, whose scale is 2^-126, a third (208).
 MXQ_DEV void add16(float* acc, const uint32_t (&v)[16], float s) {
 #pragma unroll
   for (int j = 0; j < 16; ++j) acc[j] = __fmaf_rn(__uint_as_float(v[j]), s, acc[j]);
