@@ -7,10 +7,12 @@ It strings the operators together as a training step and a server use them:
 * forward(): norm, both layouts of its output from one read (the rows feed the
   forward product, the columns wait for the weight gradient), product;
 * backward(): both layouts of dy, the input gradient against W^T's codes, the
-  weight gradient in fp32, the norm's backward pass;
+  weight gradient in fp32, the norm's backward pass (an fp32 residual stream gets
+  its gradient from an fp32 input-gradient product);
 * infer(): the norm writes the product's operand directly.
 
-Host code only: every operation is one of mxq's calls on the current stream.
+Host code only: every operation is one of mxq's calls on the current stream, but
+for the rounding of an fp32 norm output to the quantizer's bf16.
 """
 
 from __future__ import annotations
@@ -41,13 +43,13 @@ class Fp8NormLinear:
         self.operands = mxq.fp8_quantize_tiles(self.weight, out=self.operands)
 
     def forward(self, x):
-        """x [tokens, in] -> (y [tokens, out] bf16, what backward() needs)."""
+        """x [tokens, in] bf16 or fp32 -> (y [tokens, out] bf16, what backward() needs)."""
         if self.kind == "layer":
             h, mean, rstd = mxq.layer_norm(x, self.norm_weight, self.norm_bias, self.eps)
         else:
             h, rstd = mxq.rms_norm(x, self.norm_weight, self.eps)
             mean = None
-        hr, hrs, hc, hcs = mxq.fp8_quantize_dual(h)
+        hr, hrs, hc, hcs = mxq.fp8_quantize_dual(h.to(torch.bfloat16))
         w, ws = self.operands[:2]
         y = mxq.fp8_gemm(hr, hrs, w, ws, x.shape[0], self.out_features, self.in_features)
         return y, (x, mean, rstd, hc, hcs)
@@ -59,7 +61,7 @@ class Fp8NormLinear:
         T, N, K, g = x.shape[0], self.out_features, self.in_features, self.grad_fmt
         dr, drs, dc, dcs = mxq.fp8_quantize_dual(dy, g, g)
         wt, wts = self.operands[2:]
-        dh = mxq.fp8_gemm(dr, drs, wt, wts, T, K, N, fmt_a=g)
+        dh = mxq.fp8_gemm(dr, drs, wt, wts, T, K, N, fmt_a=g, out_dtype=x.dtype)
         dweight = mxq.fp8_gemm(dc, dcs, hc, hcs, N, K, T, fmt_a=g, b_scales="line",
                                out_dtype=torch.float32)
         if self.kind == "layer":
