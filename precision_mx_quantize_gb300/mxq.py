@@ -16,6 +16,7 @@ front of it ``layer_norm``, ``rms_norm``, their ``_quantize`` and
 
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import functools
 import os
@@ -776,12 +777,20 @@ def rms_norm_quantize(x: torch.Tensor, weight, eps=1e-5, fmt="e4m3", out=None):
 
 
 @functools.lru_cache(maxsize=4096)
-def _norm_backward_workspace(rows, cols):
-    return int(mxq_norm_backward_workspace_size(rows, cols))
+def _norm_backward_workspace(rows, cols, index):
+    """Bytes on the device of that index (None: no GPU in play): they depend on its
+    number of SMs, and the library asks the current device."""
+    with contextlib.nullcontext() if index is None else torch.cuda.device(index):
+        return int(mxq_norm_backward_workspace_size(rows, cols))
 
 
 def norm_backward_workspace(rows, cols, device):
-    return torch.empty(max(_norm_backward_workspace(rows, cols), 256), dtype=torch.uint8,
+    """A workspace of layer_norm_backward and rms_norm_backward on a CUDA device."""
+    device = torch.device(device)
+    index = device.index
+    if index is None and device.type == "cuda":
+        index = torch.cuda.current_device()
+    return torch.empty(max(_norm_backward_workspace(rows, cols, index), 256), dtype=torch.uint8,
                        device=device)
 
 
