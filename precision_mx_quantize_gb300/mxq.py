@@ -740,6 +740,9 @@ def _norm_forward(x, weight, bias, eps, kind, fmt, with_y, out):
             _need_fp8(codes, scales, R, C, "line", dev)
     rstd = torch.empty(R, dtype=torch.float32, device=x.device)
     mean = torch.empty_like(rstd) if kind == NORM_LAYER else None
+    if C == 0:   # the library writes nothing: the mean of no elements, 0 / 0
+        for stat in (rstd,) if mean is None else (mean, rstd):
+            stat.fill_(float("nan"))
     a = _NORM_ARGS.pack(x.data_ptr(), weight.data_ptr(), 0 if bias is None else bias.data_ptr(),
                         y.data_ptr() if with_y else 0, 0 if mean is None else mean.data_ptr(),
                         rstd.data_ptr(), 0 if with_y else codes.data_ptr(),
