@@ -438,7 +438,8 @@ typedef struct {
 /*
  * The forward pass; with codes set it also writes (or, y == NULL, only writes)
  * the product's operand, quantized from the fp32 values by the rule above.
- * x, weight, bias, y and codes must be 16-byte aligned.  y may be x itself.
+ * x, weight, bias, y, codes and scales must be 16-byte aligned, mean and rstd
+ * 4-byte.  y may be x itself.
  * rows == 0 or cols == 0 is a no-op.
  */
 mxq_status mxq_norm_forward(const mxq_norm_args* args, void* stream);
@@ -466,6 +467,7 @@ typedef struct {
  *   g = dy * weight,  dx = rstd * (g - mean(g) - h * mean(g h))   (RMS: no mean(g))
  *   dweight = sum over rows of dy * h,  dbias = sum over rows of dy
  * The row sums are taken in a fixed order: the same inputs give the same bits.
+ * dy, x, weight and dx must be 16-byte aligned, the fp32 vectors 4-byte.
  * dx may be dy or x itself.  rows == 0 writes zero gradients; cols == 0 is a no-op.
  */
 mxq_status mxq_norm_backward(const mxq_norm_grad_args* args, void* stream);

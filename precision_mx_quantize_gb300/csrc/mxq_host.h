@@ -62,6 +62,7 @@ inline int64_t fp8_pitch(int64_t blocked) { return (blocked + 15) / 16 * 16; }
 inline int64_t fp8_lines(int64_t lines) { return (lines + 3) / 4 * 4; }
 
 inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+inline bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
 
 // A launch that may start while the previous kernel on the stream drains; the
 // kernels wait for it before their first global access.

@@ -469,7 +469,7 @@ extern "C" mxq_status mxq_norm_forward(const mxq_norm_args* p, void* stream) {
   if (p->rows == 0 || p->cols == 0) return MXQ_OK;
   if (!p->x || !p->weight || (!p->y && !p->codes)) return MXQ_ERR_ARG;
   if (!aligned16(p->x) || !aligned16(p->weight) || !aligned16(p->bias) || !aligned16(p->y) ||
-      !aligned16(p->codes) || !aligned16(p->scales))
+      !aligned16(p->codes) || !aligned16(p->scales) || !aligned4(p->mean) || !aligned4(p->rstd))
     return MXQ_ERR_ALIGN;
   NArgs a = {};
   a.x = p->x;

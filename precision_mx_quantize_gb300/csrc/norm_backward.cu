@@ -511,6 +511,7 @@ extern "C" mxq_status mxq_norm_backward(const mxq_norm_grad_args* p, void* strea
   if (st != MXQ_OK) return st;
   if (p->cols == 0) return MXQ_OK;
   if (!p->dweight) return MXQ_ERR_ARG;
+  if (!aligned4(p->dweight) || !aligned4(p->dbias)) return MXQ_ERR_ALIGN;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   if (p->rows == 0) {
     const size_t bytes = static_cast<size_t>(p->cols) * sizeof(float);
@@ -521,7 +522,8 @@ extern "C" mxq_status mxq_norm_backward(const mxq_norm_grad_args* p, void* strea
   if (!p->dy || !p->x || !p->weight || !p->rstd || !p->dx || !p->workspace) return MXQ_ERR_ARG;
   if (p->dbias && p->kind != MXQ_NORM_LAYER) return MXQ_ERR_ARG;
   if (p->kind == MXQ_NORM_LAYER && !p->mean) return MXQ_ERR_ARG;
-  if (!aligned16(p->dy) || !aligned16(p->x) || !aligned16(p->weight) || !aligned16(p->dx))
+  if (!aligned16(p->dy) || !aligned16(p->x) || !aligned16(p->weight) || !aligned16(p->dx) ||
+      !aligned4(p->mean) || !aligned4(p->rstd))
     return MXQ_ERR_ALIGN;
   if ((reinterpret_cast<uintptr_t>(p->workspace) & 255u) != 0) return MXQ_ERR_ALIGN;
   if (p->workspace_bytes < mxq_norm_backward_workspace_size(p->rows, p->cols))
