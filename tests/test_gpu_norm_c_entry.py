@@ -67,3 +67,21 @@ def test_rms_norm_with_a_bias_to_codes(size):
     step = np.repeat(to_np(scales)[:, :size[0]].T.astype(np.float64), 128, 1)[:, :size[1]]
     tol = np.maximum(2.0 ** -4 * (np.abs(ey) + ty), 2.0 ** -10 * step) + ty + 4 * 2.0 ** -24 * np.abs(ey)
     assert (np.abs(got - ey) <= tol).all()
+
+
+@pytest.mark.parametrize("kind", ["layer", "rms"])
+@pytest.mark.parametrize("types", [TYPES[0], TYPES[3]], ids=str)
+@pytest.mark.parametrize("size", SIZES, ids=str)
+def test_output_and_codes_from_one_call(size, types, kind):
+    # y within its bound, the codes those of the call that writes codes alone
+    x, w, b, _ = _inputs(*size, *types, seed=sum(size))
+    b = b if kind == "layer" else None
+    xg, wg, bg = x.cuda(), w.cuda(), None if b is None else b.cuda()
+    y, codes, scales, rstd = _forward(kind, xg, wg, bg, True, "e4m3")
+    ey, _, er, ty, _, dr = _bounds(x, w, b, kind)
+    if types[0] is torch.bfloat16:
+        ty = ty + 2.0 ** -8 * (np.abs(ey) + ty)
+    assert (np.abs(_f(y) - ey) <= ty).all()
+    assert (np.abs(_f(rstd) - er) <= dr * er).all()
+    _, alone, alone_scales, _ = _forward(kind, xg, wg, bg, False, "e4m3")
+    assert torch.equal(codes, alone) and torch.equal(scales, alone_scales)
