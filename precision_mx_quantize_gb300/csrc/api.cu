@@ -165,17 +165,24 @@ bool ensure_dynamic_smem(const void* kernel, int bytes) {
     int dev, bytes;
   };
   static std::mutex mu;
-  static Done done[256];
+  constexpr int kMax = 4096;   // one a kernel and device: 150 kernels on 27 devices
+  static Done done[kMax];
   static int n_done = 0;
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess) return false;
   std::lock_guard<std::mutex> lock(mu);
-  for (int i = 0; i < n_done; ++i)
-    if (done[i].kernel == kernel && done[i].dev == dev && done[i].bytes >= bytes) return true;
+  Done* d = nullptr;
+  for (int i = 0; i < n_done && !d; ++i)
+    if (done[i].kernel == kernel && done[i].dev == dev) d = &done[i];
+  // The limit only ever grows: another thread may be about to launch the kernel
+  // with the size it asked for.
+  if (d && d->bytes >= bytes) return true;
+  if (!d && n_done == kMax) return false;
   if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) !=
       cudaSuccess)
     return false;
-  if (n_done < 256) done[n_done++] = Done{kernel, dev, bytes};
+  if (d) d->bytes = bytes;
+  else done[n_done++] = Done{kernel, dev, bytes};
   return true;
 }
 

@@ -37,8 +37,8 @@ CUresult tensor_map_3d(CUtensorMap* out, CUtensorMapDataType dtype, const void* 
                        uint32_t box0, uint32_t box1, uint32_t box2, CUtensorMapSwizzle swizzle,
                        CUtensorMapL2promotion l2);
 
-// cudaFuncSetAttribute(MaxDynamicSharedMemorySize) for `kernel` on the
-// current device, done once per (kernel, device, size).
+// Raises `kernel`'s limit of dynamic shared memory on the current device to at
+// least `bytes`; it is never lowered.
 bool ensure_dynamic_smem(const void* kernel, int bytes);
 
 // The one-pass quantizer when either output is E5M2 (its own translation
