@@ -313,17 +313,14 @@ def _on_gpu(t):
     return t.is_cuda
 
 
-def _need(t, name, dtype, numel, dev=None, row=None):
+def _need(t, name, dtype, numel, dev=None):
     """Raise unless t is a contiguous CUDA tensor of `dtype` (None: any) with
-    at least `numel` elements, on device index `dev` when given, and, when it
-    has rows (a flat tensor is a plain buffer), rows of `row` elements when
-    given: the library would read others with the wrong pitch.  Cheap on
+    at least `numel` elements, on device index `dev` when given.  Cheap on
     the success path (the binding runs it on every call): one combined test,
     and the detailed checks only to word the error."""
     try:
         if ((dtype is None or t.dtype is dtype) and t.numel() >= numel and t.is_contiguous()
-                and _on_gpu(t) and (dev is None or t.get_device() == dev)
-                and (row is None or t.dim() < 2 or t.size(-1) == row)):
+                and _on_gpu(t) and (dev is None or t.get_device() == dev)):
             return
     except AttributeError:
         pass
@@ -339,8 +336,21 @@ def _need(t, name, dtype, numel, dev=None, row=None):
         raise ValueError(f"{name} must be on a CUDA device (the library has no CPU path)")
     if dev is not None and t.get_device() != dev:
         raise ValueError(f"{name} is on device {t.get_device()}, the inputs on {dev}")
-    if row is not None and t.dim() > 1 and t.size(-1) != row:
-        raise ValueError(f"{name} has rows of {t.size(-1)} elements; they must hold {row}")
+
+
+def _need_rows(t, name, dtype, shape, dev=None):
+    """The same for a tensor of the shape [rows, length], or a flat buffer of as many
+    elements, or one with more rows.  Rows of another length are refused: the
+    library would read them with the wrong pitch."""
+    try:
+        if (t.shape == shape and t.dtype is dtype and t.is_contiguous() and _on_gpu(t)
+                and (dev is None or t.get_device() == dev)):
+            return
+    except AttributeError:
+        pass
+    _need(t, name, dtype, shape[0] * shape[1], dev)
+    if t.dim() > 1 and t.size(-1) != shape[1]:
+        raise ValueError(f"{name} has rows of {t.size(-1)} elements; they must hold {shape[1]}")
 
 
 def _need_input(x):
@@ -608,8 +618,8 @@ def _need_fp8(codes, scales, lines, blocked, kind, dev, tag=""):
     """The code and scale buffers of `lines` lines of `blocked` elements: shaped as
     fp8_shapes says (more lines of codes may follow), or flat."""
     cs, ss = fp8_shapes(lines, blocked, kind)
-    _need(codes, "codes" + tag, torch.uint8, cs[0] * cs[1], dev, cs[1])
-    _need(scales, "scales" + tag, torch.float32, ss[0] * ss[1], dev, ss[1])
+    _need_rows(codes, "codes" + tag, torch.uint8, cs, dev)
+    _need_rows(scales, "scales" + tag, torch.float32, ss, dev)
 
 
 def fp8_quantize(x: torch.Tensor, axis="row", fmt="e4m3", out=None):
@@ -681,17 +691,17 @@ def fp8_gemm(A, sA, B, sB, M, N, K, fmt_a="e4m3", fmt_b="e4m3", b_scales="tile",
     od = _out_code(out_dtype)
     fa, fb, bs = FP8_FMTS[fmt_a], FP8_FMTS[fmt_b], B_SCALES[b_scales]
     M, N, K = int(M), int(N), int(K)
-    (m, pa), (ka, la) = fp8_shapes(M, K)
-    (n, pb), (kb, lb) = fp8_shapes(N, K, bs)
-    _need(A, "codes_A", torch.uint8, m * pa, None, pa)
+    ca, ra = fp8_shapes(M, K)
+    cb, rb = fp8_shapes(N, K, bs)
+    _need_rows(A, "codes_A", torch.uint8, ca)
     dev = A.get_device()
-    _need(sA, "scales_A", torch.float32, ka * la, dev, la)
-    _need(B, "codes_B", torch.uint8, n * pb, dev, pb)
-    _need(sB, "scales_B", torch.float32, kb * lb, dev, lb)
+    _need_rows(sA, "scales_A", torch.float32, ra, dev)
+    _need_rows(B, "codes_B", torch.uint8, cb, dev)
+    _need_rows(sB, "scales_B", torch.float32, rb, dev)
     if out is None:
         out = torch.empty((M, N), dtype=out_dtype, device=A.device)
     else:
-        _need(out, "out", out_dtype, M * N, dev, N)
+        _need_rows(out, "out", out_dtype, (M, N), dev)
     _ok(mxq_fp8_gemm(A.data_ptr(), sA.data_ptr(), fa, B.data_ptr(), sB.data_ptr(), fb, bs, M, N, K,
                      out.data_ptr(), od, _stream(dev)), "mxq_fp8_gemm")
     return out
@@ -730,7 +740,7 @@ def _norm_forward(x, weight, bias, eps, kind, fmt, with_y, out):
             y = torch.empty_like(x)
         else:
             y = out
-            _need(y, "out", x.dtype, R * C, dev, C)
+            _need_rows(y, "out", x.dtype, (R, C), dev)
     else:
         f = FP8_FMTS[fmt]
         if out is None:
@@ -800,7 +810,7 @@ def norm_backward_workspace(rows, cols, device):
 def _norm_backward(dy, x, weight, mean, rstd, kind, out, workspace):
     dev, xd, wd = _need_norm(x, weight, None)
     R, C = x.shape
-    _need(dy, "dy", x.dtype, R * C, dev, C)
+    _need_rows(dy, "dy", x.dtype, (R, C), dev)
     _need(rstd, "rstd", torch.float32, R, dev)
     if kind == NORM_LAYER:
         _need(mean, "mean", torch.float32, R, dev)
@@ -808,7 +818,7 @@ def _norm_backward(dy, x, weight, mean, rstd, kind, out, workspace):
         dx = torch.empty_like(x)
     else:
         dx = out
-        _need(dx, "out", x.dtype, R * C, dev, C)
+        _need_rows(dx, "out", x.dtype, (R, C), dev)
     if workspace is None:
         workspace = norm_backward_workspace(R, C, x.device)
     else:
