@@ -446,8 +446,10 @@ def _own(s):
         dy, dw = mxq.expert_combine_backward(s["dout"], s["y"], s["row_of"], s["offsets"],
                                              s["counts"], s["weights"], out=s["out_buffer"])
         return {"dy": dy, "dweights": dw}
-    mxq.adamw_step(s["params"], s["grads"], s["states"], s["step"], LR, (BETA1, BETA2), EPS, DECAY,
-                   weights=s["copies"])
+    if "plan" not in s:   # a program makes it once, for as long as it trains these tensors
+        s["plan"] = mxq.adamw_plan(s["params"], s["states"], weights=s["copies"],
+                                   weight_decay=DECAY)
+    mxq.adamw_step(s["plan"], s["grads"], s["step"], LR, betas=(BETA1, BETA2), eps=EPS)
     return _adamw_out(s)
 
 
