@@ -475,10 +475,177 @@ mxq_status mxq_norm_backward(const mxq_norm_grad_args* args, void* stream);
 /* Bytes of workspace mxq_norm_backward needs (0 on bad arguments or rows == 0). */
 size_t mxq_norm_backward_workspace_size(int64_t rows, int64_t cols);
 
+/* ---------------------------------------------------------------------------
+ * Layers of experts
+ * ---------------------------------------------------------------------------
+ * A router gives each of `tokens` tokens `topk` of `experts` experts (its
+ * choices).  The experts work on a buffer of rows sorted by expert: expert e holds
+ * rows offsets[e] to offsets[e + 1], in the order of the choices, and zeros behind
+ * them up to the next multiple of `align`.  offsets and counts live on the device,
+ * so no call waits for the routing.  experts: 1 to 1024.
+ */
+
+/*
+ * The order of n = tokens * topk choices.  ids [n]: the experts, 32- or 64-bit
+ * (id_bytes 4 or 8); a choice outside [0, experts) goes to no expert.
+ *   counts[e]   choices of expert e
+ *   offsets[e]  sum over e' < e of counts[e'] rounded up to align; [experts + 1]
+ *   row_of[i]   row of choice i: offsets[ids[i]] plus the earlier choices of the
+ *               same expert; -1 for one that goes to no expert
+ * A buffer of n + min(experts, n) * (align - 1) rows, rounded up to align, holds
+ * any routing.  The same ids give the same rows.  align: 1 to 4096.
+ * workspace: mxq_expert_order_workspace_size() bytes, 4-byte aligned (may be NULL
+ * where that is 0).  n == 0 writes zero offsets and counts.
+ */
+mxq_status mxq_expert_order(const void* ids, int id_bytes, int64_t n, int experts, int align,
+                            int32_t* row_of, int32_t* offsets, int32_t* counts, void* workspace,
+                            size_t workspace_bytes, void* stream);
+
+/* Bytes of workspace mxq_expert_order needs (0 also on bad arguments). */
+size_t mxq_expert_order_workspace_size(int64_t n, int experts);
+
+/* Arguments of the three calls below (host memory, read during the call). */
+typedef struct {
+  const void* x;            /* [tokens][cols]                                   */
+  const void* y;            /* [rows][cols]                                     */
+  void* out;                /* see the calls                                    */
+  const int32_t* row_of;    /* [tokens][topk], as mxq_expert_order writes it    */
+  const int32_t* offsets;   /* [experts + 1]                                    */
+  const int32_t* counts;    /* [experts]                                        */
+  const float* weights;     /* [tokens][topk], or NULL: ones                    */
+  float* dweights;          /* [tokens][topk]                                   */
+  int64_t tokens, rows, cols;
+  int topk;                 /* 1 to 1024                                        */
+  int experts;
+  int dtype;                /* of x, y and out: MXQ_OUT_F32 or MXQ_OUT_BF16     */
+} mxq_expert_rows_args;
+
+/*
+ * out[row_of[t][j]] = weights[t][j] * x[t] for every choice that has a row, and
+ * zeros in the experts' padding; out [rows][cols].  Rows from offsets[experts] on
+ * are left as they were.  Reads x, row_of, offsets, counts, weights.
+ * One fp32 product and one rounding per element.  x and out must be 16-byte
+ * aligned, and so in the calls below.  Two choices never share a row; a row_of
+ * outside the buffer is left out and reported by mxq_check (MXQ_ERR_ARG).
+ */
+mxq_status mxq_expert_gather(const mxq_expert_rows_args* args, void* stream);
+
+/*
+ * out[t] = sum over j of weights[t][j] * y[row_of[t][j]], out [tokens][cols]: in
+ * fp32, in the order of j, rounded once.  A choice without a row adds nothing; a
+ * token without rows gets zeros.  Reads y, row_of, weights.  With weights NULL it
+ * is the gradient of mxq_expert_gather.
+ */
+mxq_status mxq_expert_combine(const mxq_expert_rows_args* args, void* stream);
+
+/*
+ * Gradients of mxq_expert_combine, x holding that of its sums:
+ *   out[row_of[t][j]] = weights[t][j] * x[t]   (padding and later rows as in
+ *                                               mxq_expert_gather)
+ *   dweights[t][j] = sum over columns of x[t] * y[row_of[t][j]], 0 without a row
+ * The sums are taken in a fixed order.  out may be y itself.
+ */
+mxq_status mxq_expert_combine_backward(const mxq_expert_rows_args* args, void* stream);
+
+/* Arguments of the products grouped by expert (host memory, read during the call). */
+typedef struct {
+  const void* A;            /* codes                                            */
+  const uint8_t* sA;        /* their E8M0 scales, row-major, any alignment      */
+  const void* B;
+  const uint8_t* sB;
+  const int32_t* offsets;   /* [experts + 1], device                            */
+  void* C;
+  void* workspace;          /* 256-byte aligned                                 */
+  size_t workspace_bytes;
+  int64_t rows;             /* of the buffer; offsets lie in [0, rows]          */
+  int64_t M;                /* mxq_gemm_experts_wgrad only                      */
+  int64_t N;
+  int64_t K;                /* mxq_gemm_experts only                            */
+  int experts;
+  int fmt;                  /* of A and B: MXQ_E4M3, MXQ_E5M2 or MXQ_E2M1       */
+  int out_dtype;            /* of C: MXQ_OUT_F32 or MXQ_OUT_BF16                */
+  int b_scale_layout;       /* mxq_gemm_experts only: mxq_scale_layout of sB    */
+} mxq_experts_args;
+
+/*
+ * C[r] = dec(A[r]) dec(B[e])^T for the rows r of every expert e: mxq_gemm with the
+ * weight that each row's expert has.
+ * A: codes [rows][K], sA [rows][K/32]; B: codes [experts][N][K]; sB: [experts][N]
+ * [K/32], or, MXQ_SCALES_TC, one buffer of mxq_scales_tc_bytes(N, K) bytes for
+ * every expert, one after another (K % 128 == 0, E2M1 % 256; 16-byte aligned).
+ * C: [rows][N]; rows that no expert holds are left as they were.
+ * K % 32 == 0; N % 4 == 0 (fp32) or N % 8 == 0 (bf16); any rows and offsets.
+ * Offsets that fall or leave [0, rows] are moved to the nearest that do not, and
+ * reported by mxq_check (MXQ_ERR_ARG).
+ * rows == 0 is a no-op.
+ */
+mxq_status mxq_gemm_experts(const mxq_experts_args* args, void* stream);
+
+/*
+ * C[e] = dec(A[:, r]) dec(B[:, r])^T over the rows r of every expert e: the weight
+ * gradients.  A: codes [M][rows], sA [M][rows/32]; B: codes [N][rows], sB
+ * [N][rows/32], as MXQ_COLWISE_T writes both.  C: [experts][M][N]; zeros for an
+ * expert without rows.
+ * rows % 32 == 0 and offsets multiples of 32 (E2M1: 64), so that no block of 32
+ * spans two experts: align of mxq_expert_order.  Offsets that are not, or that fall
+ * or leave [0, rows], are moved down and reported as above.  N as above.
+ */
+mxq_status mxq_gemm_experts_wgrad(const mxq_experts_args* args, void* stream);
+
+/* Bytes of workspace the two calls need (0 on bad arguments). */
+size_t mxq_gemm_experts_workspace_size(int64_t rows, int64_t N, int64_t K, int experts, int fmt,
+                                       int b_scale_layout);
+size_t mxq_gemm_experts_wgrad_workspace_size(int64_t rows, int64_t M, int64_t N, int experts,
+                                             int fmt);
+
+/* ---------------------------------------------------------------------------
+ * AdamW
+ * ---------------------------------------------------------------------------
+ * One step over many tensors.  With g the gradient times *grad_scale_at, t the step:
+ *   m = beta1 m + (1 - beta1) g,   v = beta2 v + (1 - beta2) g^2
+ *   p = p - lr weight_decay p
+ *         - lr / (1 - beta1^t) * m / (sqrt(v / (1 - beta2^t)) + eps)
+ * in fp32.  state_bits 32: m and v in fp32.  state_bits 8: m and r = sqrt(v) as E4M3
+ * codes with one fp32 scale per 128 elements by the rule of the block-128 format
+ * (the last block of a tensor shorter); an r above zero keeps at least the smallest
+ * code, 2^-9 of its scale.  p's step uses m and v before that rounding.  A block
+ * with a NaN or an infinity has scale NaN from then on.
+ */
+typedef struct {
+  float* param;             /* [n]                                              */
+  void* m;                  /* [n] fp32, or codes                               */
+  void* v;                  /* [n] fp32, or codes of r                          */
+  float* m_scale;           /* state_bits 8: [ceil(n / 128)]                    */
+  float* r_scale;
+  void* copy;               /* bf16 [n]: receives the rounded param; or NULL    */
+  int64_t n;
+  float weight_decay;
+} mxq_adamw_tensor;
+
+typedef struct {
+  double lr, beta1, beta2, eps;   /* 0 <= beta < 1, eps >= 0                    */
+  int64_t step;             /* t, from 1 on                                     */
+  const float* lr_at;       /* device, read in place of lr; or NULL             */
+  const int64_t* step_at;   /* device, read in place of step; or NULL           */
+  const float* grad_scale_at;  /* device; NULL: 1.  NaN or an infinity there    */
+                            /* leaves every tensor as it is                     */
+  int grad_dtype;           /* MXQ_OUT_F32 or MXQ_OUT_BF16                      */
+  int state_bits;           /* 32 or 8                                          */
+} mxq_adamw_args;
+
+/*
+ * tensors [count], grads [count] (device pointers) in host memory, read during the
+ * call.  Any n; fp32 data 4-byte, bf16 2-byte aligned (16 for full speed).  No two
+ * buffers of a call overlap.  No workspace.
+ */
+mxq_status mxq_adamw(const mxq_adamw_tensor* tensors, const void* const* grads, int count,
+                     const mxq_adamw_args* args, void* stream);
+
 /*
  * Synchronizes `stream`, then reports and clears device-side errors recorded
  * by earlier calls on any stream (MXQ_ERR_TIMEOUT when a bounded wait inside
- * a kernel gave up), or MXQ_ERR_CUDA when the stream reports a CUDA error.
+ * a kernel gave up, MXQ_ERR_ARG when a kernel found an argument in device memory
+ * invalid), or MXQ_ERR_CUDA when the stream reports a CUDA error.
  */
 mxq_status mxq_check(void* stream);
 

@@ -218,7 +218,8 @@ extern "C" mxq_status mxq_check(void* stream) {
   if (cudaGetLastError() != cudaSuccess) return MXQ_ERR_CUDA;
   const uint32_t words[] = {take_quant_error(), take_quant_e5m2_error(), take_ablation_error(),
                              take_gemm_error(),  take_fp8_quant_error(),  take_fp8_gemm_error(),
-                             take_norm_error(),  take_norm_grad_error(),  take_debug_error()};
+                             take_norm_error(),  take_norm_grad_error(),  take_experts_error(),
+                             take_rows_error(),  take_adamw_error(),      take_debug_error()};
   for (uint32_t w : words)
     if (w) return static_cast<mxq_status>(w & 0xFFu);
   return MXQ_OK;

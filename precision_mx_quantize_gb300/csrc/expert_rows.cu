@@ -1,0 +1,474 @@
+// Rows of a buffer sorted by expert: which row each choice of the router gets, tokens
+// gathered into the rows, rows summed back into the tokens, and that sum's gradients.
+//
+// Order: a stable counting sort of the choices by expert.  With h(b, e) the choices of
+// expert e in block b of the choices,
+//   counts[e] = sum_b h(b, e),  offsets[e] = sum_{e' < e} ceil(counts[e'] / align) align,
+//   row of a choice = offsets[e] + sum_{b' < b} h(b', e) + its rank in its block.
+// Ranks come from votes between the lanes and sums over warps in a fixed order, never
+// from the order of atomics, so a routing always gives the same rows.
+//
+// Gather, combine and their gradients move rows: a team of 32 to 256 threads holds a
+// token and all rows of its choices, so that a token's row is read (or written) once.
+#include "fp8_common.cuh"
+#include "mxq_host.h"
+
+namespace mxq {
+
+__device__ uint32_t g_err_rows;
+
+namespace {
+
+constexpr int O_THREADS = 1024;
+constexpr int O_WARPS = O_THREADS / 32;
+constexpr int O_MAX_EXPERTS = 1024;
+constexpr int O_MIN_BLOCK = 4096;    // choices of a block, at least
+constexpr int O_MAX_BLOCKS = 152;
+
+struct OrderArgs {
+  const void* ids;
+  int64_t n;              // choices
+  int64_t block;          // choices of a block, a multiple of O_THREADS
+  int32_t wide;           // ids are 64-bit
+  int32_t experts, align;
+  int32_t *row_of, *offsets, *counts;
+  int32_t* hist;          // [blocks][experts]
+};
+
+// Expert of choice i, or -1 for one that goes to no expert.
+MXQ_DEV int expert_of(const OrderArgs& a, int64_t i) {
+  int64_t e = a.wide ? static_cast<const int64_t*>(a.ids)[i] : static_cast<const int32_t*>(a.ids)[i];
+  return e >= 0 && e < a.experts ? static_cast<int>(e) : -1;
+}
+
+__global__ void __launch_bounds__(O_THREADS) order_count(const OrderArgs a) {
+  extern __shared__ int32_t hist[];
+  griddep_wait();
+  griddep_launch_dependents();
+  for (int e = threadIdx.x; e < a.experts; e += O_THREADS) hist[e] = 0;
+  __syncthreads();
+  const int64_t first = blockIdx.x * a.block, end = min(first + a.block, a.n);
+  for (int64_t i = first + threadIdx.x; i < end; i += O_THREADS) {
+    const int e = expert_of(a, i);
+    if (e >= 0) atomicAdd(&hist[e], 1);
+  }
+  __syncthreads();
+  for (int e = threadIdx.x; e < a.experts; e += O_THREADS)
+    a.hist[int64_t(blockIdx.x) * a.experts + e] = hist[e];
+}
+
+// hist of all blocks -> offsets and counts (block 0) and the rows of this block's choices.
+__global__ void __launch_bounds__(O_THREADS) order_rows(const OrderArgs a) {
+  extern __shared__ int32_t next[];   // [warps][experts]: the warp's next row of an expert
+  __shared__ int32_t sums[O_WARPS];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int64_t part = a.block / O_WARPS;   // a warp's choices, a multiple of 32
+  const int64_t first = blockIdx.x * a.block + warp * part;
+  const int64_t end = min(first + part, a.n);
+  int32_t* mine = next + warp * a.experts;
+  griddep_wait();
+  griddep_launch_dependents();
+  for (int i = threadIdx.x; i < O_WARPS * a.experts; i += O_THREADS) next[i] = 0;
+  __syncthreads();
+  for (int64_t i = first; i < end; i += 32) {
+    const int e = i + lane < end ? expert_of(a, i + lane) : -1;
+    const uint32_t same = __match_any_sync(~0u, e);
+    if (e >= 0 && lane == __ffs(same) - 1) mine[e] += __popc(same);
+    __syncwarp();
+  }
+  __syncthreads();
+  const int e = threadIdx.x;
+  int before = 0, total = 0;
+  if (e < a.experts) {
+    if (gridDim.x == 1) {
+      for (int w = 0; w < O_WARPS; ++w) total += next[w * a.experts + e];
+    } else {
+      const int nb = static_cast<int>(gridDim.x);
+#pragma unroll 8
+      for (int b = 0; b < nb; ++b) {
+        const int h = a.hist[int64_t(b) * a.experts + e];
+        total += h;
+        if (b < static_cast<int>(blockIdx.x)) before += h;
+      }
+    }
+  }
+  const int rows = (total + a.align - 1) / a.align * a.align;
+  int upto = rows;   // inclusive sum over the experts
+#pragma unroll
+  for (int d = 1; d < 32; d <<= 1) {
+    const int o = __shfl_up_sync(~0u, upto, d);
+    if (lane >= d) upto += o;
+  }
+  if (lane == 31) sums[warp] = upto;
+  __syncthreads();
+  for (int w = 0; w < warp; ++w) upto += sums[w];
+  if (e < a.experts) {
+    if (blockIdx.x == 0) {
+      if (e == 0) a.offsets[0] = 0;
+      a.offsets[e + 1] = upto;
+      a.counts[e] = total;
+    }
+    int at = upto - rows + before;
+    for (int w = 0; w < O_WARPS; ++w) {
+      const int h = next[w * a.experts + e];
+      next[w * a.experts + e] = at;
+      at += h;
+    }
+  }
+  __syncthreads();
+  for (int64_t i = first; i < end; i += 32) {
+    const bool live = i + lane < end;
+    const int x = live ? expert_of(a, i + lane) : -1;
+    const uint32_t same = __match_any_sync(~0u, x);
+    const int rank = __popc(same & ((1u << lane) - 1u));
+    const int row = x >= 0 ? mine[x] + rank : -1;
+    __syncwarp();
+    if (x >= 0 && rank == 0) mine[x] += __popc(same);
+    __syncwarp();
+    if (live && MXQ_IN_BOUNDS(i + lane < a.n, &g_err_rows, SITE_B_EXPERT_ROWS))
+      a.row_of[i + lane] = row;
+  }
+}
+
+// ---- rows -------------------------------------------------------------------------
+
+struct RowsArgs {
+  const void* x;             // [tokens][cols]: the tokens, or the gradient of their sums
+  const void* y;             // [rows][cols]
+  void* out;                 // gather, combine_backward: [rows][cols]; combine: [tokens][cols]
+  const int32_t* row_of;     // [tokens][topk]
+  const int32_t *offsets, *counts;
+  const float* weights;      // [tokens][topk], or NULL: ones
+  float* dweights;           // [tokens][topk]
+  int64_t tokens, rows, cols;
+  int32_t topk, experts, team;
+};
+
+constexpr int R_THREADS = 256;
+constexpr int R_GROUP = 8;   // choices handled together
+
+// Row of a choice: -1 where it has none.  A row outside the buffer is reported and left out.
+MXQ_DEV int64_t row_at(const RowsArgs& a, int64_t t, int j) {
+  const int r = a.row_of[t * a.topk + j];
+  if (r >= a.rows) record_error(&g_err_rows, MXQ_ERR_ARG, SITE_EXPERT_ROW);
+  return r >= 0 && r < a.rows ? r : -1;
+}
+
+// W consecutive elements of a row: 16 bytes of it (rows on 16-byte boundaries), or one.
+template <typename T, int W>
+struct Piece {
+  float f[W];
+  MXQ_DEV void load(const T* p) {
+    if constexpr (W == 1) {
+      f[0] = static_cast<float>(*p);
+    } else if constexpr (sizeof(T) == 4) {
+      const float4 v = *reinterpret_cast<const float4*>(p);
+      f[0] = v.x; f[1] = v.y; f[2] = v.z; f[3] = v.w;
+    } else {
+      const uint4 v = *reinterpret_cast<const uint4*>(p);
+      f[0] = bf16lo(v.x); f[1] = bf16hi(v.x); f[2] = bf16lo(v.y); f[3] = bf16hi(v.y);
+      f[4] = bf16lo(v.z); f[5] = bf16hi(v.z); f[6] = bf16lo(v.w); f[7] = bf16hi(v.w);
+    }
+  }
+  MXQ_DEV void store(T* p) const {
+    if constexpr (W == 1) {
+      if constexpr (sizeof(T) == 4) *p = f[0];
+      else *p = __float2bfloat16_rn(f[0]);
+    } else if constexpr (sizeof(T) == 4) {
+      *reinterpret_cast<float4*>(p) = make_float4(f[0], f[1], f[2], f[3]);
+    } else {
+      uint32_t w[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const __nv_bfloat162 b = __floats2bfloat162_rn(f[2 * i], f[2 * i + 1]);
+        w[i] = *reinterpret_cast<const uint32_t*>(&b);
+      }
+      *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
+    }
+  }
+};
+
+// Zeros in the rows between an expert's choices and the next expert's rows, by the
+// teams behind the tokens'.
+template <typename T, int W>
+MXQ_DEV void clear_padding(const RowsArgs& a, int64_t e, int at) {
+  if (e >= a.experts) return;
+  Piece<T, W> zero;
+#pragma unroll
+  for (int i = 0; i < W; ++i) zero.f[i] = 0.0f;
+  const int64_t lo = max(int64_t(a.offsets[e]) + a.counts[e], int64_t(0));
+  const int64_t hi = min(int64_t(a.offsets[e + 1]), a.rows);
+  for (int64_t r = lo; r < hi; ++r)
+    for (int64_t c = int64_t(at) * W; c < a.cols; c += int64_t(a.team) * W)
+      zero.store(static_cast<T*>(a.out) + r * a.cols + c);
+}
+
+template <typename T, int W>
+__global__ void __launch_bounds__(R_THREADS) expert_gather(const RowsArgs a) {
+  griddep_wait();
+  griddep_launch_dependents();
+  const int at = threadIdx.x % a.team;
+  const int64_t t = int64_t(blockIdx.x) * (R_THREADS / a.team) + threadIdx.x / a.team;
+  if (t >= a.tokens) {
+    clear_padding<T, W>(a, t - a.tokens, at);
+    return;
+  }
+  const T* row = static_cast<const T*>(a.x) + t * a.cols;
+  for (int j0 = 0; j0 < a.topk; j0 += R_GROUP) {
+    int64_t to[R_GROUP];
+    float w[R_GROUP];
+#pragma unroll
+    for (int j = 0; j < R_GROUP; ++j) {
+      to[j] = j0 + j < a.topk ? row_at(a, t, j0 + j) : -1;
+      w[j] = a.weights && to[j] >= 0 ? a.weights[t * a.topk + j0 + j] : 1.0f;
+    }
+    for (int64_t c = int64_t(at) * W; c < a.cols; c += int64_t(a.team) * W) {
+      Piece<T, W> v;
+      v.load(row + c);
+#pragma unroll
+      for (int j = 0; j < R_GROUP; ++j) {
+        if (to[j] < 0) continue;
+        Piece<T, W> s;
+#pragma unroll
+        for (int i = 0; i < W; ++i) s.f[i] = v.f[i] * w[j];
+        s.store(static_cast<T*>(a.out) + to[j] * a.cols + c);
+      }
+    }
+  }
+}
+
+// out[t] = sum_j w[t][j] y[row of (t, j)], in the order of j, in fp32.
+template <typename T, int W>
+__global__ void __launch_bounds__(R_THREADS) expert_combine(const RowsArgs a) {
+  griddep_wait();
+  griddep_launch_dependents();
+  const int at = threadIdx.x % a.team;
+  const int64_t t = int64_t(blockIdx.x) * (R_THREADS / a.team) + threadIdx.x / a.team;
+  if (t >= a.tokens) return;
+  const T* y = static_cast<const T*>(a.y);
+  for (int64_t c = int64_t(at) * W; c < a.cols; c += int64_t(a.team) * W) {
+    Piece<T, W> sum;
+#pragma unroll
+    for (int i = 0; i < W; ++i) sum.f[i] = 0.0f;
+    for (int j0 = 0; j0 < a.topk; j0 += R_GROUP) {
+      Piece<T, W> v[R_GROUP];
+      float w[R_GROUP];
+#pragma unroll
+      for (int j = 0; j < R_GROUP; ++j) {
+        const int64_t r = j0 + j < a.topk ? row_at(a, t, j0 + j) : -1;
+        w[j] = 0.0f;
+#pragma unroll
+        for (int i = 0; i < W; ++i) v[j].f[i] = 0.0f;
+        if (r < 0) continue;
+        w[j] = a.weights ? a.weights[t * a.topk + j0 + j] : 1.0f;
+        v[j].load(y + r * a.cols + c);
+      }
+#pragma unroll
+      for (int j = 0; j < R_GROUP; ++j)
+#pragma unroll
+        for (int i = 0; i < W; ++i) sum.f[i] = fmaf(w[j], v[j].f[i], sum.f[i]);
+    }
+    sum.store(static_cast<T*>(a.out) + t * a.cols + c);
+  }
+}
+
+// out[row of (t, j)] = w[t][j] x[t],  dweights[t][j] = <x[t], y[row of (t, j)]>.
+template <typename T, int W>
+__global__ void __launch_bounds__(R_THREADS) expert_combine_backward(const RowsArgs a) {
+  __shared__ float part[R_THREADS / 32][R_GROUP];
+  griddep_wait();
+  griddep_launch_dependents();
+  const int at = threadIdx.x % a.team;
+  const int64_t t = int64_t(blockIdx.x) * (R_THREADS / a.team) + threadIdx.x / a.team;
+  if (t >= a.tokens) clear_padding<T, W>(a, t - a.tokens, at);
+  const bool live = t < a.tokens;
+  const T* row = static_cast<const T*>(a.x) + t * a.cols;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  for (int j0 = 0; j0 < a.topk; j0 += R_GROUP) {
+    int64_t to[R_GROUP];
+    float w[R_GROUP], dot[R_GROUP];
+#pragma unroll
+    for (int j = 0; j < R_GROUP; ++j) {
+      to[j] = live && j0 + j < a.topk ? row_at(a, t, j0 + j) : -1;
+      w[j] = a.weights && to[j] >= 0 ? a.weights[t * a.topk + j0 + j] : 1.0f;
+      dot[j] = 0.0f;
+    }
+    if (live)
+      for (int64_t c = int64_t(at) * W; c < a.cols; c += int64_t(a.team) * W) {
+        Piece<T, W> d;
+        d.load(row + c);
+#pragma unroll
+        for (int j = 0; j < R_GROUP; ++j) {
+          if (to[j] < 0) continue;
+          Piece<T, W> v, s;
+          v.load(static_cast<const T*>(a.y) + to[j] * a.cols + c);
+#pragma unroll
+          for (int i = 0; i < W; ++i) {
+            dot[j] = fmaf(d.f[i], v.f[i], dot[j]);
+            s.f[i] = d.f[i] * w[j];
+          }
+          s.store(static_cast<T*>(a.out) + to[j] * a.cols + c);
+        }
+      }
+    __syncthreads();   // the last group's sums have been read
+#pragma unroll
+    for (int j = 0; j < R_GROUP; ++j) {
+      float s = dot[j];
+#pragma unroll
+      for (int d = 16; d; d >>= 1) s += __shfl_xor_sync(~0u, s, d);
+      if (lane == 0) part[warp][j] = s;
+    }
+    __syncthreads();
+    if (live && at < R_GROUP && j0 + at < a.topk) {
+      float s = 0.0f;
+      for (int v = 0; v < a.team / 32; ++v) s += part[warp + v][at];
+      a.dweights[t * a.topk + j0 + at] = s;
+    }
+  }
+}
+
+enum RowsOp { GATHER, COMBINE, BACKWARD };
+
+template <typename T, int W>
+bool rows_launch(RowsOp op, unsigned grid, cudaStream_t st, const RowsArgs& a) {
+  switch (op) {
+    case GATHER: return launch_early(expert_gather<T, W>, grid, R_THREADS, 0, st, a);
+    case COMBINE: return launch_early(expert_combine<T, W>, grid, R_THREADS, 0, st, a);
+    default: return launch_early(expert_combine_backward<T, W>, grid, R_THREADS, 0, st, a);
+  }
+}
+
+mxq_status rows_run(RowsOp op, const mxq_expert_rows_args* q, void* stream) {
+  const int64_t lim = int64_t(1) << 31;
+  if (!q || q->tokens < 0 || q->rows < 0 || q->cols < 0 || q->topk < 1 || q->tokens >= lim ||
+      q->rows >= lim || q->cols >= lim || q->topk > 1024 || q->tokens * q->topk >= lim)
+    return MXQ_ERR_ARG;
+  if (q->dtype != MXQ_OUT_F32 && q->dtype != MXQ_OUT_BF16) return MXQ_ERR_ARG;
+  const bool pads = op != COMBINE;
+  if (pads && (q->experts < 1 || q->experts > O_MAX_EXPERTS)) return MXQ_ERR_ARG;
+  if (q->cols == 0 && op != BACKWARD) return MXQ_OK;
+  if (q->tokens == 0 && (!pads || q->rows == 0)) return MXQ_OK;
+  // an empty buffer of rows has no address
+  if (!q->row_of || (op != COMBINE && !q->x) || (op != GATHER && q->rows && !q->y) ||
+      ((op == COMBINE || q->rows) && !q->out) || (pads && (!q->offsets || !q->counts)) ||
+      (op == BACKWARD && !q->dweights))
+    return MXQ_ERR_ARG;
+  const void* words[] = {q->row_of, q->offsets, q->counts, q->weights, q->dweights};
+  for (const void* p : words)
+    if (!aligned4(p)) return MXQ_ERR_ALIGN;
+  const void* data[] = {q->x, q->y, q->out};
+  for (const void* p : data)
+    if (!aligned16(p)) return MXQ_ERR_ALIGN;
+  RowsArgs a = {};
+  a.x = q->x;
+  a.y = q->y;
+  a.out = q->out;
+  a.row_of = q->row_of;
+  a.offsets = q->offsets;
+  a.counts = q->counts;
+  a.weights = q->weights;
+  a.dweights = q->dweights;
+  a.tokens = q->tokens;
+  a.rows = q->rows;
+  a.cols = q->cols;
+  a.topk = q->topk;
+  a.experts = pads ? q->experts : 0;
+  const bool bf16 = q->dtype == MXQ_OUT_BF16;
+  const int width = bf16 ? 8 : 4;
+  const bool vec = q->cols % width == 0;
+  const int64_t pieces = vec ? q->cols / width : q->cols;
+  a.team = 32;
+  while (a.team < R_THREADS && a.team * 2 <= pieces) a.team *= 2;
+  const int per = R_THREADS / a.team;
+  const int64_t teams = a.tokens + a.experts;
+  const unsigned grid = static_cast<unsigned>((teams + per - 1) / per);
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  const bool ok = bf16 ? (vec ? rows_launch<__nv_bfloat16, 8>(op, grid, st, a)
+                              : rows_launch<__nv_bfloat16, 1>(op, grid, st, a))
+                       : (vec ? rows_launch<float, 4>(op, grid, st, a)
+                              : rows_launch<float, 1>(op, grid, st, a));
+  return ok ? launch_status() : MXQ_ERR_CUDA;
+}
+
+// Choices of a block and the number of blocks.
+void order_blocks(int64_t n, int64_t& block, int64_t& blocks) {
+  const int64_t even = (n + O_MAX_BLOCKS - 1) / O_MAX_BLOCKS;
+  block = std::max<int64_t>(O_MIN_BLOCK, (even + O_THREADS - 1) / O_THREADS * O_THREADS);
+  blocks = (n + block - 1) / block;
+}
+
+bool order_sizes_ok(int64_t n, int experts, int align) {
+  return n >= 0 && experts >= 1 && experts <= O_MAX_EXPERTS && align >= 1 && align <= 4096 &&
+         n + int64_t(experts) * align < (int64_t(1) << 31);
+}
+
+}  // namespace
+
+uint32_t take_rows_error() {
+  uint32_t h = 0;
+  if (cudaMemcpyFromSymbol(&h, g_err_rows, sizeof(h)) != cudaSuccess) return MXQ_ERR_CUDA;
+  if (h) {
+    const uint32_t z = 0;
+    cudaMemcpyToSymbol(g_err_rows, &z, sizeof(z));
+  }
+  return h;
+}
+
+}  // namespace mxq
+
+using namespace mxq;
+
+extern "C" size_t mxq_expert_order_workspace_size(int64_t n, int experts) {
+  if (!order_sizes_ok(n, experts, 1)) return 0;
+  int64_t block, blocks;
+  order_blocks(n, block, blocks);
+  return blocks > 1 ? static_cast<size_t>(blocks * experts * 4) : 0;
+}
+
+extern "C" mxq_status mxq_expert_order(const void* ids, int id_bytes, int64_t n, int experts,
+                                       int align, int32_t* row_of, int32_t* offsets,
+                                       int32_t* counts, void* workspace, size_t workspace_bytes,
+                                       void* stream) {
+  if (!order_sizes_ok(n, experts, align) || (id_bytes != 4 && id_bytes != 8)) return MXQ_ERR_ARG;
+  if (!offsets || !counts || (n > 0 && (!ids || !row_of))) return MXQ_ERR_ARG;
+  if ((reinterpret_cast<uintptr_t>(ids) & (id_bytes - 1)) != 0 || !aligned4(row_of) ||
+      !aligned4(offsets) || !aligned4(counts) || !aligned4(workspace))
+    return MXQ_ERR_ALIGN;
+  OrderArgs a = {};
+  int64_t blocks;
+  order_blocks(n, a.block, blocks);
+  if (blocks > 1) {
+    if (!workspace || workspace_bytes < static_cast<size_t>(blocks * experts * 4))
+      return MXQ_ERR_WORKSPACE;
+  }
+  a.ids = ids;
+  a.n = n;
+  a.wide = id_bytes == 8;
+  a.experts = experts;
+  a.align = align;
+  a.row_of = row_of;
+  a.offsets = offsets;
+  a.counts = counts;
+  a.hist = static_cast<int32_t*>(workspace);
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  const int smem = O_WARPS * experts * 4;
+  if (!ensure_dynamic_smem(reinterpret_cast<const void*>(order_rows), smem)) return MXQ_ERR_CUDA;
+  if (blocks > 1 && !launch_early(order_count, static_cast<unsigned>(blocks), O_THREADS,
+                                  size_t(experts) * 4, st, a))
+    return MXQ_ERR_CUDA;
+  const unsigned grid = static_cast<unsigned>(std::max<int64_t>(blocks, 1));
+  if (!launch_early(order_rows, grid, O_THREADS, smem, st, a)) return MXQ_ERR_CUDA;
+  return launch_status();
+}
+
+extern "C" mxq_status mxq_expert_gather(const mxq_expert_rows_args* args, void* stream) {
+  return rows_run(GATHER, args, stream);
+}
+
+extern "C" mxq_status mxq_expert_combine(const mxq_expert_rows_args* args, void* stream) {
+  return rows_run(COMBINE, args, stream);
+}
+
+extern "C" mxq_status mxq_expert_combine_backward(const mxq_expert_rows_args* args, void* stream) {
+  return rows_run(BACKWARD, args, stream);
+}

@@ -55,6 +55,11 @@ enum : uint32_t {
   SITE_B_FP8_GEMM = 30,      // block-128 GEMM stores of C
   SITE_B_NORM = 31,          // norm loads and stores
   SITE_B_NORM_GRAD = 32,     // norm backward partial sums and gradients
+  SITE_EXPERT_OFFSETS = 33,  // offsets of the experts' rows that no tile may follow
+  SITE_EXPERT_ROW = 34,      // a choice's row outside the buffer
+  SITE_B_EXPERT_CHUNKS = 35,  // scale chunks of the products grouped by expert
+  SITE_B_EXPERT_ROWS = 36,   // rows of the choices
+  SITE_B_ADAMW = 37,         // chunks of the AdamW step
 };
 
 MXQ_DEV void record_error(uint32_t* word, uint32_t status, uint32_t site) {

@@ -56,6 +56,9 @@ uint32_t take_fp8_quant_error();
 uint32_t take_fp8_gemm_error();
 uint32_t take_norm_error();
 uint32_t take_norm_grad_error();
+uint32_t take_experts_error();
+uint32_t take_rows_error();
+uint32_t take_adamw_error();
 
 // Block-128 FP8 buffers: code pitch, lines of a scale row.
 inline int64_t fp8_pitch(int64_t blocked) { return (blocked + 15) / 16 * 16; }

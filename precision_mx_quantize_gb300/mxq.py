@@ -11,7 +11,10 @@ statement: ``mx_quantize``, ``hadamard_mx_quantize``, ``mx_quantize_dual``,
 The FP8 recipe with one fp32 scale per block of 128 has ``fp8_quantize``,
 ``fp8_quantize_dual``, ``fp8_quantize_tiles`` and ``fp8_gemm``; the norms in
 front of it ``layer_norm``, ``rms_norm``, their ``_quantize`` and
-``_backward`` forms.
+``_backward`` forms.  Layers of experts have ``expert_order``, ``expert_gather``,
+``expert_combine``, ``expert_combine_backward``, ``mx_gemm_experts`` and
+``mx_gemm_experts_wgrad``; the optimizer's update ``adamw_state``, ``adamw_plan``
+and ``adamw_step``.
 """
 
 from __future__ import annotations
@@ -79,6 +82,16 @@ SIGNATURES = [
     ("mxq_norm_forward", _I, [_P, _P]),
     ("mxq_norm_backward", _I, [_P, _P]),
     ("mxq_norm_backward_workspace_size", _SZ, [_I64, _I64]),
+    ("mxq_expert_order", _I, [_P, _I, _I64, _I, _I, _P, _P, _P, _P, _SZ, _P]),
+    ("mxq_expert_order_workspace_size", _SZ, [_I64, _I]),
+    ("mxq_expert_gather", _I, [_P, _P]),
+    ("mxq_expert_combine", _I, [_P, _P]),
+    ("mxq_expert_combine_backward", _I, [_P, _P]),
+    ("mxq_gemm_experts", _I, [_P, _P]),
+    ("mxq_gemm_experts_wgrad", _I, [_P, _P]),
+    ("mxq_gemm_experts_workspace_size", _SZ, [_I64, _I64, _I64, _I, _I, _I]),
+    ("mxq_gemm_experts_wgrad_workspace_size", _SZ, [_I64, _I64, _I64, _I, _I]),
+    ("mxq_adamw", _I, [_P, _P, _I, _P, _P]),
     ("mxq_check", _I, [_P]),
     ("mxq_set_wait_timeout_ns", None, [_U64]),
     ("mxq_debug_expire_wait", _I, [_U64, _P]),
@@ -111,10 +124,50 @@ class NormGradArgs(ctypes.Structure):
                 ("x_dtype", ctypes.c_int), ("w_dtype", ctypes.c_int)]
 
 
-# The same two structures as native-layout formats: packing one takes a third
-# of the time of filling the ctypes mirror, which small calls notice.
+class ExpertRowsArgs(ctypes.Structure):
+    """mxq_expert_rows_args of the C header (field order and types as declared)."""
+    _fields_ = [("x", ctypes.c_void_p), ("y", ctypes.c_void_p), ("out", ctypes.c_void_p),
+                ("row_of", ctypes.c_void_p), ("offsets", ctypes.c_void_p),
+                ("counts", ctypes.c_void_p), ("weights", ctypes.c_void_p),
+                ("dweights", ctypes.c_void_p), ("tokens", ctypes.c_int64),
+                ("rows", ctypes.c_int64), ("cols", ctypes.c_int64), ("topk", ctypes.c_int),
+                ("experts", ctypes.c_int), ("dtype", ctypes.c_int)]
+
+
+class ExpertsArgs(ctypes.Structure):
+    """mxq_experts_args of the C header (field order and types as declared)."""
+    _fields_ = [("A", ctypes.c_void_p), ("sA", ctypes.c_void_p), ("B", ctypes.c_void_p),
+                ("sB", ctypes.c_void_p), ("offsets", ctypes.c_void_p), ("C", ctypes.c_void_p),
+                ("workspace", ctypes.c_void_p), ("workspace_bytes", ctypes.c_size_t),
+                ("rows", ctypes.c_int64), ("M", ctypes.c_int64), ("N", ctypes.c_int64),
+                ("K", ctypes.c_int64), ("experts", ctypes.c_int), ("fmt", ctypes.c_int),
+                ("out_dtype", ctypes.c_int), ("b_scale_layout", ctypes.c_int)]
+
+
+class AdamWTensor(ctypes.Structure):
+    """mxq_adamw_tensor of the C header (field order and types as declared)."""
+    _fields_ = [("param", ctypes.c_void_p), ("m", ctypes.c_void_p), ("v", ctypes.c_void_p),
+                ("m_scale", ctypes.c_void_p), ("r_scale", ctypes.c_void_p),
+                ("copy", ctypes.c_void_p), ("n", ctypes.c_int64),
+                ("weight_decay", ctypes.c_float)]
+
+
+class AdamWArgs(ctypes.Structure):
+    """mxq_adamw_args of the C header (field order and types as declared)."""
+    _fields_ = [("lr", ctypes.c_double), ("beta1", ctypes.c_double), ("beta2", ctypes.c_double),
+                ("eps", ctypes.c_double), ("step", ctypes.c_int64), ("lr_at", ctypes.c_void_p),
+                ("step_at", ctypes.c_void_p), ("grad_scale_at", ctypes.c_void_p),
+                ("grad_dtype", ctypes.c_int), ("state_bits", ctypes.c_int)]
+
+
+# The same structures as native-layout formats: packing one takes a third of the
+# time of filling the ctypes mirror, which small calls notice.
 _NORM_ARGS = struct.Struct("@8P2qf4i0q")
 _NORM_GRAD_ARGS = struct.Struct("@9PN2q3i0q")
+_EXPERT_ROWS_ARGS = struct.Struct("@8P3q3i0q")
+_EXPERTS_ARGS = struct.Struct("@7PN4q4i0q")
+_ADAMW_TENSOR = struct.Struct("@6Pqf0q")
+_ADAMW_ARGS = struct.Struct("@4dq3P2i0q")
 
 _lib = None
 _lock = threading.Lock()
@@ -280,6 +333,55 @@ def mxq_norm_backward(args, stream):
 
 def mxq_norm_backward_workspace_size(rows, cols):
     return lib().mxq_norm_backward_workspace_size(rows, cols)
+
+
+def mxq_expert_order(ids, id_bytes, n, experts, align, row_of, offsets, counts, workspace,
+                     ws_bytes, stream):
+    return lib().mxq_expert_order(ids, id_bytes, n, experts, align, row_of, offsets, counts,
+                                  workspace, ws_bytes, stream)
+
+
+def mxq_expert_order_workspace_size(n, experts):
+    return lib().mxq_expert_order_workspace_size(n, experts)
+
+
+def mxq_expert_gather(args, stream):
+    """args: address of an ExpertRowsArgs structure in host memory, or its bytes."""
+    return lib().mxq_expert_gather(args, stream)
+
+
+def mxq_expert_combine(args, stream):
+    """args: as mxq_expert_gather."""
+    return lib().mxq_expert_combine(args, stream)
+
+
+def mxq_expert_combine_backward(args, stream):
+    """args: as mxq_expert_gather."""
+    return lib().mxq_expert_combine_backward(args, stream)
+
+
+def mxq_gemm_experts(args, stream):
+    """args: address of an ExpertsArgs structure in host memory, or its bytes."""
+    return lib().mxq_gemm_experts(args, stream)
+
+
+def mxq_gemm_experts_wgrad(args, stream):
+    """args: as mxq_gemm_experts."""
+    return lib().mxq_gemm_experts_wgrad(args, stream)
+
+
+def mxq_gemm_experts_workspace_size(rows, N, K, experts, fmt, b_scale_layout):
+    return lib().mxq_gemm_experts_workspace_size(rows, N, K, experts, fmt, b_scale_layout)
+
+
+def mxq_gemm_experts_wgrad_workspace_size(rows, M, N, experts, fmt):
+    return lib().mxq_gemm_experts_wgrad_workspace_size(rows, M, N, experts, fmt)
+
+
+def mxq_adamw(tensors, grads, count, args, stream):
+    """tensors: address of `count` AdamWTensor structures in host memory, or their
+    bytes; grads: of as many device pointers; args: of an AdamWArgs structure."""
+    return lib().mxq_adamw(tensors, grads, count, args, stream)
 
 
 def mxq_check(stream=None):
@@ -843,3 +945,397 @@ def layer_norm_backward(dy, x, weight, mean, rstd, out=None, workspace=None):
 def rms_norm_backward(dy, x, weight, rstd, out=None, workspace=None):
     """Gradients of rms_norm from its statistics; returns (dx, dweight)."""
     return _norm_backward(dy, x, weight, None, rstd, NORM_RMS, out, workspace)[:2]
+
+
+# ---- layers of experts -----------------------------------------------------------------
+
+def expert_rows(choices: int, experts: int, align: int = 1) -> int:
+    """Rows of a buffer that holds any routing of `choices` choices, every expert's rows
+    padded to a multiple of `align`."""
+    n = choices + min(experts, choices) * (align - 1)
+    return (n + align - 1) // align * align
+
+
+@functools.lru_cache(maxsize=4096)
+def _order_workspace(n, experts):
+    return int(mxq_expert_order_workspace_size(n, experts))
+
+
+def expert_order(ids: torch.Tensor, experts: int, align: int = 1):
+    """Rows of the choices ids [tokens, topk] (int32 or int64, contiguous, on the GPU) in
+    a buffer sorted by expert; an id outside [0, experts) goes to no expert.  Returns
+    (row_of [tokens, topk], offsets [experts + 1], counts [experts]), all int32: expert
+    e holds rows offsets[e] to offsets[e + 1], its counts[e] choices in their order and
+    padding up to a multiple of `align`.  Nothing waits for the device."""
+    if not isinstance(ids, torch.Tensor) or ids.dim() != 2:
+        raise ValueError("ids must be a 2-D torch.Tensor [tokens, topk]")
+    if ids.dtype is not torch.int32 and ids.dtype is not torch.int64:
+        raise ValueError(f"ids must be torch.int32 or torch.int64, got {ids.dtype}")
+    _need(ids, "ids", None, 0)
+    experts, align = int(experts), int(align)
+    if not 1 <= experts <= 1024:
+        raise ValueError(f"experts must be 1 to 1024, got {experts}")
+    n, dev = ids.numel(), ids.get_device()
+    meta = torch.empty(n + 2 * experts + 1 + (_order_workspace(n, experts) + 3) // 4,
+                       dtype=torch.int32, device=ids.device)
+    row_of, offsets, counts, ws = meta.split_with_sizes(
+        [n, experts + 1, experts, meta.numel() - n - 2 * experts - 1])
+    _ok(mxq_expert_order(ids.data_ptr(), ids.element_size(), n, experts, align, row_of.data_ptr(),
+                         offsets.data_ptr(), counts.data_ptr(), ws.data_ptr(), 4 * ws.numel(),
+                         _stream(dev)), "mxq_expert_order")
+    return row_of.view(ids.shape), offsets, counts
+
+
+def _need_tokens(t, name):
+    """t: a contiguous 2-D bf16 or fp32 CUDA tensor; returns (device index, code of its
+    dtype)."""
+    if not isinstance(t, torch.Tensor) or t.dim() != 2:
+        raise ValueError(f"{name} must be a 2-D torch.Tensor")
+    _need(t, name, None, 0)
+    code = _FLOAT_CODES.get(t.dtype)
+    if code is None:
+        raise ValueError(f"{name} must be torch.float32 or torch.bfloat16, got {t.dtype}")
+    return t.get_device(), code
+
+
+def _need_choices(row_of, weights, dev, tokens=None):
+    """row_of [tokens, topk] and the weights beside it; returns its shape."""
+    _need(row_of, "row_of", torch.int32, 0, dev)
+    if row_of.dim() != 2 or (tokens is not None and row_of.shape[0] != tokens):
+        raise ValueError(f"row_of must be [tokens, topk], got {tuple(row_of.shape)}")
+    if weights is not None:
+        _need(weights, "weights", torch.float32, 0, dev)
+        if weights.shape != row_of.shape:
+            raise ValueError(f"weights must be {tuple(row_of.shape)}, got {tuple(weights.shape)}")
+    return row_of.shape
+
+
+def _need_offsets(offsets, counts, dev):
+    """Returns the number of experts."""
+    _need(counts, "counts", torch.int32, 1, dev)
+    experts = counts.numel()
+    _need(offsets, "offsets", torch.int32, experts + 1, dev)
+    if offsets.numel() != experts + 1:
+        raise ValueError(f"offsets holds {offsets.numel()} elements, counts {experts}")
+    return experts
+
+
+def expert_gather(x: torch.Tensor, row_of, offsets, counts, rows, weights=None, out=None):
+    """The tokens x [tokens, cols] (bf16 or fp32) at their choices' rows of a buffer
+    [rows, cols], times weights [tokens, topk] (fp32) where given; zeros in the experts'
+    padding.  row_of, offsets, counts: as expert_order returns them; rows: as
+    expert_rows says, or fewer where the program knows the routing.  Rows from
+    offsets[-1] on are not written.  Its gradient is expert_combine's sum (with the same
+    weights)."""
+    dev, code = _need_tokens(x, "x")
+    tokens, topk = _need_choices(row_of, weights, dev, x.shape[0])
+    experts = _need_offsets(offsets, counts, dev)
+    rows, cols = int(rows), x.shape[1]
+    if out is None:
+        out = torch.empty((rows, cols), dtype=x.dtype, device=x.device)
+    else:
+        _need_rows(out, "out", x.dtype, (rows, cols), dev)
+    a = _EXPERT_ROWS_ARGS.pack(x.data_ptr(), 0, out.data_ptr(), row_of.data_ptr(),
+                               offsets.data_ptr(), counts.data_ptr(),
+                               0 if weights is None else weights.data_ptr(), 0, tokens, rows, cols,
+                               topk, experts, code)
+    _ok(mxq_expert_gather(a, _stream(dev)), "mxq_expert_gather")
+    return out
+
+
+def expert_combine(y: torch.Tensor, row_of, weights=None, out=None):
+    """Sums of the rows y [rows, cols] (bf16 or fp32) back into the tokens: token t gets
+    sum_j weights[t, j] * y[row_of[t, j]] in fp32, rounded once (weights None: ones)."""
+    dev, code = _need_tokens(y, "y")
+    tokens, topk = _need_choices(row_of, weights, dev)
+    rows, cols = y.shape
+    if out is None:
+        out = torch.empty((tokens, cols), dtype=y.dtype, device=y.device)
+    else:
+        _need_rows(out, "out", y.dtype, (tokens, cols), dev)
+    a = _EXPERT_ROWS_ARGS.pack(0, y.data_ptr(), out.data_ptr(), row_of.data_ptr(), 0, 0,
+                               0 if weights is None else weights.data_ptr(), 0, tokens, rows, cols,
+                               topk, 0, code)
+    _ok(mxq_expert_combine(a, _stream(dev)), "mxq_expert_combine")
+    return out
+
+
+def expert_combine_backward(dout: torch.Tensor, y, row_of, offsets, counts, weights=None,
+                            out=None):
+    """Gradients of expert_combine: (dy [rows, cols] in y's dtype, dweights [tokens, topk]
+    in fp32).  The experts' padding of dy is zeros; rows from offsets[-1] on are not
+    written.  out: dy's buffer, which may be y."""
+    dev, code = _need_tokens(dout, "dout")
+    tokens, topk = _need_choices(row_of, weights, dev, dout.shape[0])
+    experts = _need_offsets(offsets, counts, dev)
+    cols = dout.shape[1]
+    if not isinstance(y, torch.Tensor) or y.dim() != 2 or y.shape[1] != cols:
+        raise ValueError(f"y must be a 2-D torch.Tensor with rows of {cols} elements")
+    rows = y.shape[0]
+    _need(y, "y", dout.dtype, 0, dev)
+    if out is None:
+        out = torch.empty_like(y)
+    else:
+        _need_rows(out, "out", y.dtype, (rows, cols), dev)
+    dweights = torch.empty((tokens, topk), dtype=torch.float32, device=y.device)
+    a = _EXPERT_ROWS_ARGS.pack(dout.data_ptr(), y.data_ptr(), out.data_ptr(), row_of.data_ptr(),
+                               offsets.data_ptr(), counts.data_ptr(),
+                               0 if weights is None else weights.data_ptr(), dweights.data_ptr(),
+                               tokens, rows, cols, topk, experts, code)
+    _ok(mxq_expert_combine_backward(a, _stream(dev)), "mxq_expert_combine_backward")
+    return out, dweights
+
+
+@functools.lru_cache(maxsize=4096)
+def _experts_workspace(rows, N, K, experts, fmt, b_scale_layout):
+    return int(mxq_gemm_experts_workspace_size(rows, N, K, experts, fmt, b_scale_layout))
+
+
+@functools.lru_cache(maxsize=4096)
+def _experts_wgrad_workspace(rows, M, N, experts, fmt):
+    return int(mxq_gemm_experts_wgrad_workspace_size(rows, M, N, experts, fmt))
+
+
+def gemm_experts_workspace(rows, N, K, experts, fmt, device, b_scale_layout="rowmajor"):
+    """A workspace of mx_gemm_experts."""
+    n = _experts_workspace(int(rows), int(N), int(K), int(experts), FMTS[fmt],
+                           SCALE_LAYOUTS[b_scale_layout])
+    return torch.empty(max(n, 256), dtype=torch.uint8, device=device)
+
+
+def gemm_experts_wgrad_workspace(rows, M, N, experts, fmt, device):
+    """A workspace of mx_gemm_experts_wgrad."""
+    n = _experts_wgrad_workspace(int(rows), int(M), int(N), int(experts), FMTS[fmt])
+    return torch.empty(max(n, 256), dtype=torch.uint8, device=device)
+
+
+def _need_experts(A, offsets):
+    """Returns (A's device index, the number of experts)."""
+    _need(A, "A", torch.uint8, 0)
+    dev = A.get_device()
+    _need(offsets, "offsets", torch.int32, 2, dev)
+    return dev, offsets.numel() - 1
+
+
+@functools.lru_cache(maxsize=4096)
+def _expert_scale_bytes(experts, N, K, fmt, b_scale_layout):
+    """Bytes of the scales of B [experts, N, K]."""
+    if b_scale_layout == SCALES_ROWMAJOR:
+        return experts * N * (K // 32)
+    n = int(mxq_scales_tc_bytes(N, K))
+    if n == 0 or (fmt == E2M1 and K % 256 != 0):
+        raise ValueError(f"no tensor-core scale layout for {N} lines x {K}")
+    return experts * n
+
+
+def mx_gemm_experts(A, sA, B, sB, offsets, fmt, rows, N, K, out_dtype=torch.float32, out=None,
+                    workspace=None, b_scale_layout="rowmajor"):
+    """C[r] = dec(A[r]) @ dec(B[e])^T for the rows r of every expert e, offsets[e] <= r <
+    offsets[e + 1], on the tensor cores; returns C [rows, N].
+
+    A: MX codes of the rows [rows, K] and their row-major scales; B: codes of the experts'
+    weights [experts, N, K] and their scales, row-major, or ("tc") in the tensor cores'
+    chunk layout, one buffer of mx_quantize(..., scale_layout="tc") per expert, one after
+    another.  offsets: int32 [experts + 1] on the device (expert_order).  Rows that no
+    expert holds are not written.  workspace: as gemm_experts_workspace returns it, for
+    callers that keep one."""
+    od, f, layout = _out_code(out_dtype), FMTS[fmt], SCALE_LAYOUTS[b_scale_layout]
+    dev, experts = _need_experts(A, offsets)
+    rows, N, K = int(rows), int(N), int(K)
+    kb = K // 2 if f == E2M1 else K
+    _need(A, "codes_A", torch.uint8, rows * kb, dev)
+    _need(sA, "scales_A", torch.uint8, rows * (K // 32), dev)
+    _need(B, "codes_B", torch.uint8, experts * N * kb, dev)
+    _need(sB, "scales_B", torch.uint8, _expert_scale_bytes(experts, N, K, f, layout), dev)
+    if out is None:
+        out = torch.empty((rows, N), dtype=out_dtype, device=A.device)
+    else:
+        _need_rows(out, "out", out_dtype, (rows, N), dev)
+    if workspace is None:
+        workspace = torch.empty(max(_experts_workspace(rows, N, K, experts, f, layout), 256),
+                                dtype=torch.uint8, device=A.device)
+    else:
+        _need(workspace, "workspace", torch.uint8, 0, dev)   # its size is checked by the library
+    a = _EXPERTS_ARGS.pack(A.data_ptr(), sA.data_ptr(), B.data_ptr(), sB.data_ptr(),
+                           offsets.data_ptr(), out.data_ptr(), workspace.data_ptr(),
+                           workspace.numel(), rows, 0, N, K, experts, f, od, layout)
+    _ok(mxq_gemm_experts(a, _stream(dev)), "mxq_gemm_experts")
+    return out
+
+
+def mx_gemm_experts_wgrad(A, sA, B, sB, offsets, fmt, M, N, rows, out_dtype=torch.float32,
+                          out=None, workspace=None):
+    """C[e] = dec(A[:, r]) @ dec(B[:, r])^T over the rows r of every expert e; returns C
+    [experts, M, N], zeros for an expert without rows.
+
+    A: codes [M, rows] and row-major scales, B: [N, rows], both as
+    mx_quantize(..., "col") writes them.  offsets: multiples of 32 (E2M1: 64), as
+    expert_order(..., align=32) gives them.  workspace: as
+    gemm_experts_wgrad_workspace returns it, for callers that keep one."""
+    od, f = _out_code(out_dtype), FMTS[fmt]
+    dev, experts = _need_experts(A, offsets)
+    rows, M, N = int(rows), int(M), int(N)
+    rb = rows // 2 if f == E2M1 else rows
+    _need(A, "codes_A", torch.uint8, M * rb, dev)
+    _need(sA, "scales_A", torch.uint8, M * (rows // 32), dev)
+    _need(B, "codes_B", torch.uint8, N * rb, dev)
+    _need(sB, "scales_B", torch.uint8, N * (rows // 32), dev)
+    if out is None:
+        out = torch.empty((experts, M, N), dtype=out_dtype, device=A.device)
+    else:
+        _need(out, "out", out_dtype, experts * M * N, dev)
+        if out.dim() > 1 and out.size(-1) != N:
+            raise ValueError(f"out has rows of {out.size(-1)} elements; they must hold {N}")
+    if workspace is None:
+        workspace = torch.empty(max(_experts_wgrad_workspace(rows, M, N, experts, f), 256),
+                                dtype=torch.uint8, device=A.device)
+    else:
+        _need(workspace, "workspace", torch.uint8, 0, dev)   # its size is checked by the library
+    a = _EXPERTS_ARGS.pack(A.data_ptr(), sA.data_ptr(), B.data_ptr(), sB.data_ptr(),
+                           offsets.data_ptr(), out.data_ptr(), workspace.data_ptr(),
+                           workspace.numel(), rows, M, N, 0, experts, f, od, SCALES_ROWMAJOR)
+    _ok(mxq_gemm_experts_wgrad(a, _stream(dev)), "mxq_gemm_experts_wgrad")
+    return out
+
+
+# ---- AdamW ---------------------------------------------------------------------------------
+
+def adamw_state(param: torch.Tensor, bits: int = 32):
+    """The moments of an AdamW step on `param`, at zero: (m, v) in fp32, or, bits 8,
+    ((codes, scales), (codes, scales)) of m and sqrt(v), E4M3 with one fp32 scale per
+    128 elements."""
+    if bits == 32:
+        return tuple(torch.zeros(param.shape, dtype=torch.float32, device=param.device)
+                     for _ in range(2))
+    if bits != 8:
+        raise ValueError(f"bits must be 32 or 8, got {bits}")
+    blocks = (param.numel() + 127) // 128
+    return tuple((torch.zeros(param.shape, dtype=torch.uint8, device=param.device),
+                  torch.full((blocks,), 2.0 ** -126, device=param.device)) for _ in range(2))
+
+
+def _overlap(buffers):
+    """The names of two of the (name, tensor) that share memory, or None."""
+    spans = sorted((t.data_ptr(), t.data_ptr() + t.numel() * t.element_size(), name)
+                   for name, t in buffers if t.numel())
+    for a, b in zip(spans, spans[1:]):
+        if b[0] < a[1]:
+            return a[2], b[2]
+    return None
+
+
+class AdamWPlan:
+    """The tensors that adamw_step updates, checked once.  It keeps the tensors; one whose
+    storage has moved since is looked up anew at the next step."""
+
+    def __init__(self, params, states, weights=None, weight_decay=0.0):
+        self.params, self.states = list(params), list(states)
+        self.weights = [None] * len(self.params) if weights is None else list(weights)
+        try:
+            self.weight_decay = [float(weight_decay)] * len(self.params)
+        except TypeError:
+            self.weight_decay = [float(w) for w in weight_decay]
+        if not (len(self.params) == len(self.states) == len(self.weights)
+                == len(self.weight_decay)):
+            raise ValueError(f"{len(self.params)} params, {len(self.states)} states, "
+                             f"{len(self.weights)} weights and {len(self.weight_decay)} "
+                             "weight decays")
+        self._check()
+
+    def _check(self):
+        bits, dev, buffers, table = None, None, [], []
+        for i, (p, state, w) in enumerate(zip(self.params, self.states, self.weights)):
+            _need(p, f"params[{i}]", torch.float32, 0, dev)
+            dev, n = p.get_device(), p.numel()
+            m, v = state
+            b = 32 if isinstance(m, torch.Tensor) else 8
+            if bits is not None and b != bits:
+                raise ValueError("the states of a plan are all in 32 or all in 8 bits")
+            bits = b
+            parts = [(f"params[{i}]", p)]
+            if b == 32:
+                for name, t in (("m", m), ("v", v)):
+                    _need(t, f"states[{i}].{name}", torch.float32, n, dev)
+                    parts.append((f"states[{i}].{name}", t))
+                addresses = [m.data_ptr(), v.data_ptr(), 0, 0]
+            else:
+                for name, (codes, scales) in (("m", m), ("v", v)):
+                    _need(codes, f"states[{i}].{name}[0]", torch.uint8, n, dev)
+                    _need(scales, f"states[{i}].{name}[1]", torch.float32, (n + 127) // 128, dev)
+                    parts += [(f"states[{i}].{name}[0]", codes), (f"states[{i}].{name}[1]", scales)]
+                addresses = [m[0].data_ptr(), v[0].data_ptr(), m[1].data_ptr(), v[1].data_ptr()]
+            if w is not None:
+                _need(w, f"weights[{i}]", torch.bfloat16, n, dev)
+                parts.append((f"weights[{i}]", w))
+            buffers += parts
+            table.append(_ADAMW_TENSOR.pack(p.data_ptr(), *addresses, _ptr(w) or 0, n,
+                                            self.weight_decay[i]))
+        twice = _overlap(buffers)
+        if twice:
+            raise ValueError(f"{twice[0]} and {twice[1]} share memory")
+        self.bits, self.device = bits or 32, dev
+        self.numels = [p.numel() for p in self.params]
+        self._tensors = [t for _, t in buffers]
+        self._places = list(map(torch.Tensor.data_ptr, self._tensors))
+        self._table = b"".join(table)
+        self._written = set(self._places)
+
+    def table(self):
+        """The tensors' part of a launch; taken anew where a tensor has moved."""
+        if list(map(torch.Tensor.data_ptr, self._tensors)) != self._places:
+            self._check()
+        return self._table
+
+
+def adamw_plan(params, states, weights=None, weight_decay=0.0):
+    """A plan of adamw_step: contiguous fp32 CUDA tensors `params`, for each what
+    adamw_state returned, and for each a bf16 tensor of its size that receives the
+    rounded parameter (the quantizers' input), or None.  weight_decay: one number, or one
+    per tensor.  No two of them may share memory."""
+    return AdamWPlan(params, states, weights, weight_decay)
+
+
+def _scalar(value, name, dtype, dev):
+    """(number, device address or 0) of a number or a 1-element CUDA tensor."""
+    if not isinstance(value, torch.Tensor):
+        return value, 0
+    _need(value, name, dtype, 1, dev)
+    return 1, value.data_ptr()
+
+
+def adamw_step(plan: AdamWPlan, grads, step, lr, betas=(0.9, 0.999), eps=1e-8, grad_scale=None):
+    """One AdamW step of the plan's tensors, in place.  grads: one contiguous tensor per
+    parameter, all fp32 or all bf16; step: 1 at the first step.  step (int64), lr (fp32)
+    and grad_scale (fp32; a factor of the gradients, NaN or infinity to leave everything
+    as it is) may be 1-element CUDA tensors, which a captured launch reads anew."""
+    grads = list(grads)
+    if len(grads) != len(plan.params):
+        raise ValueError(f"{len(grads)} grads for {len(plan.params)} params")
+    if not grads:
+        return
+    table, dev = plan.table(), plan.device
+    dtype = grads[0].dtype if isinstance(grads[0], torch.Tensor) else None
+    code = _FLOAT_CODES.get(dtype)
+    if code is None:
+        raise ValueError(f"grads must be torch.float32 or torch.bfloat16, got {dtype}")
+    places = []
+    for i, (g, n) in enumerate(zip(grads, plan.numels)):
+        try:
+            if not (g.dtype is dtype and g.numel() == n and g.is_contiguous()
+                    and g.get_device() == dev):
+                raise AttributeError
+        except AttributeError:
+            _need(g, f"grads[{i}]", dtype, n, dev)
+            raise ValueError(f"grads[{i}] holds {g.numel()} elements, its parameter {n}") from None
+        places.append(g.data_ptr())
+    if not plan._written.isdisjoint(p for p in places if p):
+        raise ValueError("a gradient shares memory with a parameter or its state")
+    t, t_at = _scalar(step, "step", torch.int64, dev)
+    rate, rate_at = _scalar(lr, "lr", torch.float32, dev)
+    scale_at = 0
+    if grad_scale is not None:
+        _need(grad_scale, "grad_scale", torch.float32, 1, dev)
+        scale_at = grad_scale.data_ptr()
+    a = _ADAMW_ARGS.pack(rate, betas[0], betas[1], eps, t, rate_at, t_at, scale_at, code, plan.bits)
+    _ok(mxq_adamw(table, struct.pack(f"@{len(places)}P", *places), len(places), a, _stream(dev)),
+        "mxq_adamw")
