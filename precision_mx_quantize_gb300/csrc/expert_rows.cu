@@ -147,173 +147,250 @@ struct RowsArgs {
 constexpr int R_THREADS = 256;
 constexpr int R_GROUP = 8;   // choices handled together
 
-// Row of a choice: -1 where it has none.  A row outside the buffer is reported and left out.
-MXQ_DEV int64_t row_at(const RowsArgs& a, int64_t t, int j) {
-  const int r = a.row_of[t * a.topk + j];
-  if (r >= a.rows) record_error(&g_err_rows, MXQ_ERR_ARG, SITE_EXPERT_ROW);
-  return r >= 0 && r < a.rows ? r : -1;
-}
+// Rows of up to R_GROUP choices of a token from j0 on and their weights; -1 and weight 0
+// where a choice has no row, so that what follows needs no branches.  A row outside the
+// buffer is reported and left out.
+struct Choices {
+  int32_t row[R_GROUP];
+  float w[R_GROUP];
+  MXQ_DEV void load(const RowsArgs& a, int64_t t, int j0, bool live) {
+#pragma unroll
+    for (int j = 0; j < R_GROUP; ++j) {
+      const bool is = live && j0 + j < a.topk;
+      row[j] = is ? a.row_of[t * a.topk + j0 + j] : -1;
+      w[j] = is && a.weights ? a.weights[t * a.topk + j0 + j] : 1.0f;
+    }
+    bool bad = false;
+#pragma unroll
+    for (int j = 0; j < R_GROUP; ++j) {
+      if (row[j] >= a.rows) {
+        bad = true;
+        row[j] = -1;
+      }
+      if (row[j] < 0) w[j] = 0.0f;
+    }
+    if (bad) record_error(&g_err_rows, MXQ_ERR_ARG, SITE_EXPERT_ROW);
+  }
+};
 
-// W consecutive elements of a row: 16 bytes of it (rows on 16-byte boundaries), or one.
-template <typename T, int W>
-struct Piece {
-  float f[W];
-  MXQ_DEV void load(const T* p) {
-    if constexpr (W == 1) {
-      f[0] = static_cast<float>(*p);
-    } else if constexpr (sizeof(T) == 4) {
-      const float4 v = *reinterpret_cast<const float4*>(p);
-      f[0] = v.x; f[1] = v.y; f[2] = v.z; f[3] = v.w;
-    } else {
-      const uint4 v = *reinterpret_cast<const uint4*>(p);
-      f[0] = bf16lo(v.x); f[1] = bf16hi(v.x); f[2] = bf16lo(v.y); f[3] = bf16hi(v.y);
-      f[4] = bf16lo(v.z); f[5] = bf16hi(v.z); f[6] = bf16lo(v.w); f[7] = bf16hi(v.w);
+// Eight bf16 or four fp32 elements of a row, as they lie in memory.  VEC: 16 consecutive
+// bytes (rows on 16-byte boundaries).  Else one element in every `stride`, so that the
+// accesses of neighbouring threads still touch neighbouring elements; `left` elements of
+// the row remain from p on.
+template <typename T, bool VEC>
+struct Piece;
+
+template <typename T>
+struct Piece<T, true> {
+  static constexpr int N = 16 / sizeof(T);
+  static constexpr int REACH = N;   // elements from a thread's piece to its neighbour's
+  uint4 v;
+  MXQ_DEV void load(const T* p, int, int64_t) { v = *reinterpret_cast<const uint4*>(p); }
+  MXQ_DEV void clear() { v = make_uint4(0u, 0u, 0u, 0u); }
+  MXQ_DEV void store(T* p, int, int64_t) const { *reinterpret_cast<uint4*>(p) = v; }
+  MXQ_DEV void get(float (&f)[N]) const {
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      if constexpr (sizeof(T) == 4) f[i] = __uint_as_float(w[i]);
+      else f[i] = i & 1 ? bf16hi(w[i >> 1]) : bf16lo(w[i >> 1]);
     }
   }
-  MXQ_DEV void store(T* p) const {
-    if constexpr (W == 1) {
-      if constexpr (sizeof(T) == 4) *p = f[0];
-      else *p = __float2bfloat16_rn(f[0]);
-    } else if constexpr (sizeof(T) == 4) {
-      *reinterpret_cast<float4*>(p) = make_float4(f[0], f[1], f[2], f[3]);
-    } else {
-      uint32_t w[4];
+  MXQ_DEV void set(const float (&f)[N]) {
+    uint32_t w[4];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
+    for (int i = 0; i < 4; ++i) {
+      if constexpr (sizeof(T) == 4) {
+        w[i] = __float_as_uint(f[i]);
+      } else {
         const __nv_bfloat162 b = __floats2bfloat162_rn(f[2 * i], f[2 * i + 1]);
         w[i] = *reinterpret_cast<const uint32_t*>(&b);
       }
-      *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
+    }
+    v = make_uint4(w[0], w[1], w[2], w[3]);
+  }
+};
+
+template <typename T>
+struct Piece<T, false> {
+  static constexpr int N = 4;
+  static constexpr int REACH = 1;
+  T v[N];
+  MXQ_DEV void load(const T* p, int stride, int64_t left) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) v[i] = i * stride < left ? p[i * stride] : T(0.0f);
+  }
+  MXQ_DEV void clear() {
+#pragma unroll
+    for (int i = 0; i < N; ++i) v[i] = T(0.0f);
+  }
+  MXQ_DEV void store(T* p, int stride, int64_t left) const {
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+      if (i * stride < left) p[i * stride] = v[i];
+  }
+  MXQ_DEV void get(float (&f)[N]) const {
+#pragma unroll
+    for (int i = 0; i < N; ++i) f[i] = static_cast<float>(v[i]);
+  }
+  MXQ_DEV void set(const float (&f)[N]) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      if constexpr (sizeof(T) == 4) v[i] = f[i];
+      else v[i] = __float2bfloat16_rn(f[i]);
     }
   }
 };
 
 // Zeros in the rows between an expert's choices and the next expert's rows, by the
 // teams behind the tokens'.
-template <typename T, int W>
+template <typename T, bool VEC>
 MXQ_DEV void clear_padding(const RowsArgs& a, int64_t e, int at) {
+  using P = Piece<T, VEC>;
   if (e >= a.experts) return;
-  Piece<T, W> zero;
-#pragma unroll
-  for (int i = 0; i < W; ++i) zero.f[i] = 0.0f;
+  P zero;
+  zero.clear();
   const int64_t lo = max(int64_t(a.offsets[e]) + a.counts[e], int64_t(0));
   const int64_t hi = min(int64_t(a.offsets[e + 1]), a.rows);
   for (int64_t r = lo; r < hi; ++r)
-    for (int64_t c = int64_t(at) * W; c < a.cols; c += int64_t(a.team) * W)
-      zero.store(static_cast<T*>(a.out) + r * a.cols + c);
+    for (int64_t c = int64_t(at) * P::REACH; c < a.cols; c += int64_t(a.team) * P::N)
+      zero.store(static_cast<T*>(a.out) + r * a.cols + c, a.team, a.cols - c);
 }
 
-template <typename T, int W>
+// The token (or, past them, the expert whose padding is cleared) of a thread's team and
+// the thread's place in it.
+MXQ_DEV int64_t team_token(const RowsArgs& a, int& at) {
+  at = threadIdx.x & (a.team - 1);
+  return int64_t(blockIdx.x) * (R_THREADS / a.team) + threadIdx.x / a.team;
+}
+
+template <typename T, bool VEC>
 __global__ void __launch_bounds__(R_THREADS) expert_gather(const RowsArgs a) {
+  using P = Piece<T, VEC>;
   griddep_wait();
   griddep_launch_dependents();
-  const int at = threadIdx.x % a.team;
-  const int64_t t = int64_t(blockIdx.x) * (R_THREADS / a.team) + threadIdx.x / a.team;
+  int at;
+  const int64_t t = team_token(a, at);
   if (t >= a.tokens) {
-    clear_padding<T, W>(a, t - a.tokens, at);
+    clear_padding<T, VEC>(a, t - a.tokens, at);
     return;
   }
-  const T* row = static_cast<const T*>(a.x) + t * a.cols;
+  const T* x = static_cast<const T*>(a.x) + t * a.cols;
+  T* out = static_cast<T*>(a.out);
   for (int j0 = 0; j0 < a.topk; j0 += R_GROUP) {
-    int64_t to[R_GROUP];
-    float w[R_GROUP];
-#pragma unroll
-    for (int j = 0; j < R_GROUP; ++j) {
-      to[j] = j0 + j < a.topk ? row_at(a, t, j0 + j) : -1;
-      w[j] = a.weights && to[j] >= 0 ? a.weights[t * a.topk + j0 + j] : 1.0f;
-    }
-    for (int64_t c = int64_t(at) * W; c < a.cols; c += int64_t(a.team) * W) {
-      Piece<T, W> v;
-      v.load(row + c);
+    Choices k;
+    k.load(a, t, j0, true);
+    for (int64_t c = int64_t(at) * P::REACH; c < a.cols; c += int64_t(a.team) * P::N) {
+      P v;
+      v.load(x + c, a.team, a.cols - c);
+      float f[P::N];
+      v.get(f);
 #pragma unroll
       for (int j = 0; j < R_GROUP; ++j) {
-        if (to[j] < 0) continue;
-        Piece<T, W> s;
+        if (k.row[j] < 0) continue;
+        P s = v;
+        if (a.weights) {
+          float g[P::N];
 #pragma unroll
-        for (int i = 0; i < W; ++i) s.f[i] = v.f[i] * w[j];
-        s.store(static_cast<T*>(a.out) + to[j] * a.cols + c);
+          for (int i = 0; i < P::N; ++i) g[i] = f[i] * k.w[j];
+          s.set(g);
+        }
+        s.store(out + k.row[j] * a.cols + c, a.team, a.cols - c);
       }
     }
   }
 }
 
-// out[t] = sum_j w[t][j] y[row of (t, j)], in the order of j, in fp32.
-template <typename T, int W>
+// out[t] = sum_j w[t][j] y[row of (t, j)], in the order of j, in fp32.  The loads of all
+// choices are in flight together.
+template <typename T, bool VEC>
 __global__ void __launch_bounds__(R_THREADS) expert_combine(const RowsArgs a) {
+  using P = Piece<T, VEC>;
   griddep_wait();
   griddep_launch_dependents();
-  const int at = threadIdx.x % a.team;
-  const int64_t t = int64_t(blockIdx.x) * (R_THREADS / a.team) + threadIdx.x / a.team;
+  int at;
+  const int64_t t = team_token(a, at);
   if (t >= a.tokens) return;
   const T* y = static_cast<const T*>(a.y);
-  for (int64_t c = int64_t(at) * W; c < a.cols; c += int64_t(a.team) * W) {
-    Piece<T, W> sum;
+  Choices k;
+  k.load(a, t, 0, true);
+  for (int64_t c = int64_t(at) * P::REACH; c < a.cols; c += int64_t(a.team) * P::N) {
+    float sum[P::N];
 #pragma unroll
-    for (int i = 0; i < W; ++i) sum.f[i] = 0.0f;
+    for (int i = 0; i < P::N; ++i) sum[i] = 0.0f;
     for (int j0 = 0; j0 < a.topk; j0 += R_GROUP) {
-      Piece<T, W> v[R_GROUP];
-      float w[R_GROUP];
+      if (a.topk > R_GROUP) k.load(a, t, j0, true);
+      P v[R_GROUP];
 #pragma unroll
       for (int j = 0; j < R_GROUP; ++j) {
-        const int64_t r = j0 + j < a.topk ? row_at(a, t, j0 + j) : -1;
-        w[j] = 0.0f;
-#pragma unroll
-        for (int i = 0; i < W; ++i) v[j].f[i] = 0.0f;
-        if (r < 0) continue;
-        w[j] = a.weights ? a.weights[t * a.topk + j0 + j] : 1.0f;
-        v[j].load(y + r * a.cols + c);
+        v[j].clear();
+        if (k.row[j] >= 0) v[j].load(y + k.row[j] * a.cols + c, a.team, a.cols - c);
       }
 #pragma unroll
-      for (int j = 0; j < R_GROUP; ++j)
+      for (int j = 0; j < R_GROUP; ++j) {
+        float f[P::N];
+        v[j].get(f);
 #pragma unroll
-        for (int i = 0; i < W; ++i) sum.f[i] = fmaf(w[j], v[j].f[i], sum.f[i]);
+        for (int i = 0; i < P::N; ++i) sum[i] = fmaf(k.w[j], f[i], sum[i]);
+      }
     }
-    sum.store(static_cast<T*>(a.out) + t * a.cols + c);
+    P s;
+    s.set(sum);
+    s.store(static_cast<T*>(a.out) + t * a.cols + c, a.team, a.cols - c);
   }
 }
 
-// out[row of (t, j)] = w[t][j] x[t],  dweights[t][j] = <x[t], y[row of (t, j)]>.
-template <typename T, int W>
+// out[row of (t, j)] = w[t][j] x[t],  dweights[t][j] = <x[t], y[row of (t, j)]>.  out may
+// be y: a thread reads a piece of all its rows before it writes any.
+template <typename T, bool VEC>
 __global__ void __launch_bounds__(R_THREADS) expert_combine_backward(const RowsArgs a) {
+  using P = Piece<T, VEC>;
   __shared__ float part[R_THREADS / 32][R_GROUP];
   griddep_wait();
   griddep_launch_dependents();
-  const int at = threadIdx.x % a.team;
-  const int64_t t = int64_t(blockIdx.x) * (R_THREADS / a.team) + threadIdx.x / a.team;
-  if (t >= a.tokens) clear_padding<T, W>(a, t - a.tokens, at);
+  int at;
+  const int64_t t = team_token(a, at);
+  if (t >= a.tokens) clear_padding<T, VEC>(a, t - a.tokens, at);
   const bool live = t < a.tokens;
-  const T* row = static_cast<const T*>(a.x) + t * a.cols;
+  const T* x = static_cast<const T*>(a.x) + t * a.cols;
+  const T* y = static_cast<const T*>(a.y);
+  T* out = static_cast<T*>(a.out);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   for (int j0 = 0; j0 < a.topk; j0 += R_GROUP) {
-    int64_t to[R_GROUP];
-    float w[R_GROUP], dot[R_GROUP];
+    Choices k;
+    k.load(a, t, j0, live);
+    float dot[R_GROUP];
 #pragma unroll
-    for (int j = 0; j < R_GROUP; ++j) {
-      to[j] = live && j0 + j < a.topk ? row_at(a, t, j0 + j) : -1;
-      w[j] = a.weights && to[j] >= 0 ? a.weights[t * a.topk + j0 + j] : 1.0f;
-      dot[j] = 0.0f;
-    }
-    if (live)
-      for (int64_t c = int64_t(at) * W; c < a.cols; c += int64_t(a.team) * W) {
-        Piece<T, W> d;
-        d.load(row + c);
+    for (int j = 0; j < R_GROUP; ++j) dot[j] = 0.0f;
+    for (int64_t c = int64_t(at) * P::REACH; live && c < a.cols; c += int64_t(a.team) * P::N) {
+      P d, v[R_GROUP];
+      d.load(x + c, a.team, a.cols - c);
 #pragma unroll
-        for (int j = 0; j < R_GROUP; ++j) {
-          if (to[j] < 0) continue;
-          Piece<T, W> v, s;
-          v.load(static_cast<const T*>(a.y) + to[j] * a.cols + c);
-#pragma unroll
-          for (int i = 0; i < W; ++i) {
-            dot[j] = fmaf(d.f[i], v.f[i], dot[j]);
-            s.f[i] = d.f[i] * w[j];
-          }
-          s.store(static_cast<T*>(a.out) + to[j] * a.cols + c);
-        }
+      for (int j = 0; j < R_GROUP; ++j) {
+        v[j].clear();
+        if (k.row[j] >= 0) v[j].load(y + k.row[j] * a.cols + c, a.team, a.cols - c);
       }
+      float f[P::N];
+      d.get(f);
+#pragma unroll
+      for (int j = 0; j < R_GROUP; ++j) {
+        float g[P::N];
+        v[j].get(g);
+#pragma unroll
+        for (int i = 0; i < P::N; ++i) {
+          dot[j] = fmaf(f[i], g[i], dot[j]);
+          g[i] = f[i] * k.w[j];
+        }
+        v[j].set(g);
+      }
+#pragma unroll
+      for (int j = 0; j < R_GROUP; ++j)
+        if (k.row[j] >= 0) v[j].store(out + k.row[j] * a.cols + c, a.team, a.cols - c);
+    }
     __syncthreads();   // the last group's sums have been read
 #pragma unroll
     for (int j = 0; j < R_GROUP; ++j) {
-      float s = dot[j];
+      float s = k.row[j] >= 0 ? dot[j] : 0.0f;
 #pragma unroll
       for (int d = 16; d; d >>= 1) s += __shfl_xor_sync(~0u, s, d);
       if (lane == 0) part[warp][j] = s;
@@ -329,12 +406,12 @@ __global__ void __launch_bounds__(R_THREADS) expert_combine_backward(const RowsA
 
 enum RowsOp { GATHER, COMBINE, BACKWARD };
 
-template <typename T, int W>
+template <typename T, bool VEC>
 bool rows_launch(RowsOp op, unsigned grid, cudaStream_t st, const RowsArgs& a) {
   switch (op) {
-    case GATHER: return launch_early(expert_gather<T, W>, grid, R_THREADS, 0, st, a);
-    case COMBINE: return launch_early(expert_combine<T, W>, grid, R_THREADS, 0, st, a);
-    default: return launch_early(expert_combine_backward<T, W>, grid, R_THREADS, 0, st, a);
+    case GATHER: return launch_early(expert_gather<T, VEC>, grid, R_THREADS, 0, st, a);
+    case COMBINE: return launch_early(expert_combine<T, VEC>, grid, R_THREADS, 0, st, a);
+    default: return launch_early(expert_combine_backward<T, VEC>, grid, R_THREADS, 0, st, a);
   }
 }
 
@@ -374,19 +451,20 @@ mxq_status rows_run(RowsOp op, const mxq_expert_rows_args* q, void* stream) {
   a.topk = q->topk;
   a.experts = pads ? q->experts : 0;
   const bool bf16 = q->dtype == MXQ_OUT_BF16;
-  const int width = bf16 ? 8 : 4;
-  const bool vec = q->cols % width == 0;
-  const int64_t pieces = vec ? q->cols / width : q->cols;
+  const bool vec = q->cols % (bf16 ? 8 : 4) == 0;
+  // as many threads as a row has pieces, at most a CTA
+  const int64_t pieces = vec ? q->cols / (bf16 ? 8 : 4) : (q->cols + 3) / 4;
   a.team = 32;
   while (a.team < R_THREADS && a.team * 2 <= pieces) a.team *= 2;
   const int per = R_THREADS / a.team;
   const int64_t teams = a.tokens + a.experts;
   const unsigned grid = static_cast<unsigned>((teams + per - 1) / per);
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  const bool ok = bf16 ? (vec ? rows_launch<__nv_bfloat16, 8>(op, grid, st, a)
-                              : rows_launch<__nv_bfloat16, 1>(op, grid, st, a))
-                       : (vec ? rows_launch<float, 4>(op, grid, st, a)
-                              : rows_launch<float, 1>(op, grid, st, a));
+  using B = __nv_bfloat16;
+  const bool ok = bf16 ? (vec ? rows_launch<B, true>(op, grid, st, a)
+                              : rows_launch<B, false>(op, grid, st, a))
+                       : (vec ? rows_launch<float, true>(op, grid, st, a)
+                              : rows_launch<float, false>(op, grid, st, a));
   return ok ? launch_status() : MXQ_ERR_CUDA;
 }
 
