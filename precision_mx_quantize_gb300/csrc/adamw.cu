@@ -22,6 +22,7 @@ namespace {
 
 constexpr int A_THREADS = 256;
 constexpr int A_CHUNK = 8192;      // elements of a CTA, a multiple of A_THREADS * 4 and F_BLOCK
+constexpr float A_LEAST = 0.001953125f;   // 2^-9, the smallest code above zero
 constexpr int A_MAX = 384;         // tensors of a launch (their table is a kernel argument)
 
 struct AdamTensor {
@@ -69,29 +70,28 @@ struct AdamStep {
       skip = !(fabsf(scale) <= 3.402823466e38f);   // NaN or infinity: leave all as it is
     }
   }
-  // One element: m and v become the new moments, r = sqrt(v); returns the new p.
+  // One element: m and v become the new moments, r = sqrt(v); returns the new p.  Root
+  // and quotient are the hardware's, within 2^-23 and 2^-22: the correctly rounded ones
+  // cost a third of the 8-bit step's instructions.  A divisor above zero is at least the
+  // root of the smallest fp32 value, 2^-75, so the quotient's range is not left.
   MXQ_DEV float update(float p, float g, float decay, float& m, float& v, float& r) const {
     g *= scale;
     m = fmaf(b1, m, c1 * g);
     v = fmaf(b2, v, c2 * g * g);
-    r = sqrtf(v);
+    asm("sqrt.approx.f32 %0, %1;" : "=f"(r) : "f"(v));
     const float kept = fmaf(-lr * decay, p, p);
-    return fmaf(-step_size, m / fmaf(r, inv_r, eps), kept);
+    return fmaf(-step_size, __fdividef(m, fmaf(r, inv_r, eps)), kept);
   }
 };
 
-// N consecutive elements; vec: at an address for one load or two.
-template <int N>
-MXQ_DEV void load_n(const float* p, bool vec, int n, float (&f)[N]) {
+// Four consecutive elements, the first n where they are fewer; vec: one access.
+MXQ_DEV void load_n(const float* p, bool vec, int n, float (&f)[4]) {
   if (vec) {
-#pragma unroll
-    for (int i = 0; i < N; i += 4) {
-      const float4 v = *reinterpret_cast<const float4*>(p + i);
-      f[i] = v.x; f[i + 1] = v.y; f[i + 2] = v.z; f[i + 3] = v.w;
-    }
+    const float4 v = *reinterpret_cast<const float4*>(p);
+    f[0] = v.x; f[1] = v.y; f[2] = v.z; f[3] = v.w;
   } else {
 #pragma unroll
-    for (int i = 0; i < N; ++i) f[i] = i < n ? p[i] : 0.0f;
+    for (int i = 0; i < 4; ++i) f[i] = i < n ? p[i] : 0.0f;
   }
 }
 
@@ -158,23 +158,106 @@ MXQ_DEV void decode4(uint32_t w, float (&f)[4]) {
   f[0] = a.x; f[1] = a.y; f[2] = b.x; f[3] = b.y;
 }
 
-// Codes of a block of 128, four values per lane; `least` is the smallest code's value
-// that a value above zero keeps (0: none).
-MXQ_DEV uint32_t encode_block(const float (&x)[4], float least, float& scale) {
-  uint32_t top = 0;
+// A chunk [first, end) of a tensor with moments in 8 bits: a warp has four blocks of 128
+// at a time, each lane four elements of every block.
+constexpr int A_BLOCKS = 4;
+
+template <typename G>
+MXQ_DEV void update_codes(const AdamTensor& t, const G* g, const AdamStep& step, int64_t first,
+                          int64_t end, bool aligned) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  uint8_t *mc = static_cast<uint8_t*>(t.m), *rc = static_cast<uint8_t*>(t.v);
+  constexpr int SPAN = A_BLOCKS * F_BLOCK;
+  for (int64_t base = first + warp * SPAN; base < end; base += A_THREADS / 32 * SPAN) {
+    float p[A_BLOCKS][4], d[A_BLOCKS][4];
+    uint32_t mw[A_BLOCKS], rw[A_BLOCKS];
+    int n[A_BLOCKS];
+    // scales: lanes 0 to 3 hold m's of the four blocks, lanes 4 to 7 r's
+    const int64_t block = base / F_BLOCK + (lane & 3);
+    const bool scaled = lane < 2 * A_BLOCKS && block * F_BLOCK < end;
+    float* const scale_at = (lane < A_BLOCKS ? t.m_scale : t.r_scale) + block;
+    float scale = scaled ? *scale_at : 0.0f;
 #pragma unroll
-  for (int i = 0; i < 4; ++i) top = max(top, __float_as_uint(x[i]) & 0x7FFFFFFFu);
-  top = __reduce_max_sync(~0u, top);   // magnitudes order as their bits, NaN above infinity
-  float mul;
-  fp8_scale<MXQ_E4M3>(__uint_as_float(top), scale, mul);
-  if (mul == 0.0f) return 0u;
-  float q[4];
+    for (int q = 0; q < A_BLOCKS; ++q) {
+      const int64_t i = base + q * F_BLOCK + lane * 4;
+      n[q] = static_cast<int>(max(min(end - i, int64_t(4)), int64_t(0)));
+      const bool vec = aligned && n[q] == 4;
+      load_n(t.p + i, vec, n[q], p[q]);
+      load_n(g + i, vec, n[q], d[q]);
+      mw[q] = load_codes(mc + i, vec, n[q]);
+      rw[q] = load_codes(rc + i, vec, n[q]);
+    }
+    float m[A_BLOCKS][4], r[A_BLOCKS][4], top = 0.0f;
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    q[i] = __fmul_rn(x[i], mul);
-    if (x[i] > 0.0f) q[i] = fmaxf(q[i], least);
+    for (int q = 0; q < A_BLOCKS; ++q) {
+      const int64_t i = base + q * F_BLOCK + lane * 4;
+      const bool vec = aligned && n[q] == 4;
+      const float ms = __shfl_sync(~0u, scale, q), rs = __shfl_sync(~0u, scale, A_BLOCKS + q);
+      float v[4];
+      decode4(mw[q], m[q]);
+      decode4(rw[q], v);
+      uint32_t m_top = 0, r_top = 0;   // magnitudes order as their bits, NaN above infinity
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        m[q][j] *= ms;
+        v[j] *= rs;
+        v[j] *= v[j];
+        p[q][j] = step.update(p[q][j], d[q][j], t.decay, m[q][j], v[j], r[q][j]);
+        if (j >= n[q]) m[q][j] = r[q][j] = 0.0f;
+        m_top = max(m_top, __float_as_uint(m[q][j]) & 0x7FFFFFFFu);
+        r_top = max(r_top, __float_as_uint(r[q][j]) & 0x7FFFFFFFu);
+      }
+      store_n(t.p + i, vec, n[q], p[q]);
+      if (t.copy) store_n(t.copy + i, vec, n[q], p[q]);
+      m_top = __reduce_max_sync(~0u, m_top);
+      r_top = __reduce_max_sync(~0u, r_top);
+      if (lane == q) top = __uint_as_float(m_top);
+      if (lane == A_BLOCKS + q) top = __uint_as_float(r_top);
+    }
+    // the eight scales and their reciprocals at once, one per lane
+    float mul;
+    fp8_scale<MXQ_E4M3>(top, scale, mul);
+    if (scaled) *scale_at = scale;
+#pragma unroll
+    for (int q = 0; q < A_BLOCKS; ++q) {
+      const int64_t i = base + q * F_BLOCK + lane * 4;
+      const bool vec = aligned && n[q] == 4;
+      const float km = __shfl_sync(~0u, mul, q), kr = __shfl_sync(~0u, mul, A_BLOCKS + q);
+      float a[4], b[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        a[j] = __fmul_rn(m[q][j], km);
+        b[j] = __fmul_rn(r[q][j], kr);
+        if (r[q][j] > 0.0f) b[j] = fmaxf(b[j], A_LEAST);
+      }
+      const uint32_t ca = km == 0.0f ? 0u : cvt_e4m3x4(a[0], a[1], a[2], a[3]);
+      const uint32_t cb = kr == 0.0f ? 0u : cvt_e4m3x4(b[0], b[1], b[2], b[3]);
+      store_codes(mc + i, vec, n[q], ca);
+      store_codes(rc + i, vec, n[q], cb);
+    }
   }
-  return cvt_e4m3x4(q[0], q[1], q[2], q[3]);
+}
+
+template <typename G>
+MXQ_DEV void update_floats(const AdamTensor& t, const G* g, const AdamStep& step, int64_t first,
+                           int64_t end, bool aligned) {
+  float *tm = static_cast<float*>(t.m), *tv = static_cast<float*>(t.v);
+#pragma unroll 2
+  for (int64_t i = first + threadIdx.x * 4; i < end; i += A_THREADS * 4) {
+    const int n = static_cast<int>(min(end - i, int64_t(4)));
+    const bool vec = aligned && n == 4;
+    float p[4], d[4], m[4], v[4], r;
+    load_n(t.p + i, vec, n, p);
+    load_n(g + i, vec, n, d);
+    load_n(tm + i, vec, n, m);
+    load_n(tv + i, vec, n, v);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) p[j] = step.update(p[j], d[j], t.decay, m[j], v[j], r);
+    store_n(t.p + i, vec, n, p);
+    if (t.copy) store_n(t.copy + i, vec, n, p);
+    store_n(tm + i, vec, n, m);
+    store_n(tv + i, vec, n, v);
+  }
 }
 
 template <int MAX, typename G, bool CODES>
@@ -199,50 +282,8 @@ __global__ void __launch_bounds__(A_THREADS) adamw_kernel(const __grid_constant_
                          reinterpret_cast<uintptr_t>(t.m) | reinterpret_cast<uintptr_t>(t.v) |
                          reinterpret_cast<uintptr_t>(t.copy);
   const bool aligned = (bits & 15u) == 0;
-  const int lane = threadIdx.x & 31;
-#pragma unroll 2
-  for (int64_t i = first + threadIdx.x * 4; i - lane * 4 < end; i += A_THREADS * 4) {
-    const int n = static_cast<int>(max(min(end - i, int64_t(4)), int64_t(0)));
-    const bool vec = aligned && n == 4;
-    float p[4], d[4], m[4], v[4], r[4];
-    load_n(t.p + i, vec, n, p);
-    load_n(g + i, vec, n, d);
-    if constexpr (CODES) {
-      const float ms = t.m_scale[i / F_BLOCK], rs = t.r_scale[i / F_BLOCK];   // the warp's block
-      decode4(load_codes(static_cast<const uint8_t*>(t.m) + i, vec, n), m);
-      decode4(load_codes(static_cast<const uint8_t*>(t.v) + i, vec, n), v);
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        m[j] *= ms;
-        v[j] *= rs;
-        v[j] *= v[j];
-      }
-    } else {
-      load_n(static_cast<const float*>(t.m) + i, vec, n, m);
-      load_n(static_cast<const float*>(t.v) + i, vec, n, v);
-    }
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      p[j] = step.update(p[j], d[j], t.decay, m[j], v[j], r[j]);
-      if (j >= n) m[j] = r[j] = 0.0f;
-    }
-    store_n(t.p + i, vec, n, p);
-    if (t.copy) store_n(t.copy + i, vec, n, p);
-    if constexpr (CODES) {
-      float ms, rs;
-      const uint32_t mc = encode_block(m, 0.0f, ms);
-      const uint32_t rc = encode_block(r, 0.001953125f, rs);
-      store_codes(static_cast<uint8_t*>(t.m) + i, vec, n, mc);
-      store_codes(static_cast<uint8_t*>(t.v) + i, vec, n, rc);
-      if (lane == 0) {
-        t.m_scale[i / F_BLOCK] = ms;
-        t.r_scale[i / F_BLOCK] = rs;
-      }
-    } else {
-      store_n(static_cast<float*>(t.m) + i, vec, n, m);
-      store_n(static_cast<float*>(t.v) + i, vec, n, v);
-    }
-  }
+  if constexpr (CODES) update_codes(t, g, step, first, end, aligned);
+  else update_floats(t, g, step, first, end, aligned);
 }
 
 template <int MAX>
