@@ -36,8 +36,8 @@ struct GGroup {
 // Work of such a launch.
 struct DenseWork {
   using Params = GGroup;
-  static constexpr int TABLE = 0;
-  static constexpr bool PARTIAL = false, QUANTIZES = true;
+  static constexpr int STAGES = G_STAGES, TABLE = 0;
+  static constexpr bool PARTIAL = false, QUANTIZES = true, STAGED = false;
   const GGroup& g;
   int p = 0;   // problem of the last item asked for
 

@@ -36,11 +36,15 @@ struct ExpertParams {
   int32_t stores;        // 32-byte stores per row of a tile
 };
 
+#ifndef STAGED_ROWS
+#define STAGED_ROWS false
+#endif
 template <bool WGRAD>
 struct ExpertWork {
   using Params = ExpertParams;
-  static constexpr int TABLE = X_TABLE * 4;
+  static constexpr int STAGES = STAGED_ROWS || WGRAD ? 5 : 6, TABLE = (X_TABLE * 4 + 15) / 16 * 16;
   static constexpr bool PARTIAL = WGRAD, QUANTIZES = false;
+  static constexpr bool STAGED = STAGED_ROWS || WGRAD;
   const ExpertParams& g;
   const int32_t *off, *tile0, *sf0;
   int e = 0;   // expert of the last item asked for

@@ -44,7 +44,7 @@ constexpr int G_BM = 128;                    // rows of A per CTA (pair tile: 25
 constexpr int G_BN = 256;                    // columns of the tile (rows of B)
 constexpr int G_BN_CTA = G_BN / G_CLUSTER;   // rows of B each CTA holds
 constexpr int G_BKB = 128;                   // bytes of K per stage (one 128 B swizzle row)
-constexpr int G_STAGES = 6;
+constexpr int G_STAGES = 6;                  // stages of the operand ring, at most
 constexpr int G_THREADS = 384;               // 12 warps
 constexpr int G_A_BYTES = G_BM * G_BKB;      // 16 KB
 constexpr int G_B_BYTES = G_BN_CTA * G_BKB;  // 16 KB
@@ -53,7 +53,8 @@ constexpr int G_SFB_BYTES = 2048;            // all 256 rows: up to 4 chunks of 
 constexpr int G_STAGE_BYTES = G_A_BYTES + G_B_BYTES + G_SFA_BYTES + G_SFB_BYTES;
 constexpr int G_BAR_BYTES = 512;
 constexpr uint32_t kNotYet = 0xFFFFFFFFu;   // peer's stage count not yet reported
-constexpr int G_SMEM = G_STAGES * G_STAGE_BYTES + G_BAR_BYTES + 1024;
+constexpr int G_PITCH = 144;                 // staged epilogue: 128 bytes of a row and its padding
+constexpr int G_STAGED_BYTES = 8 * 32 * G_PITCH;
 constexpr uint32_t G_TMEM_COLS = 512;
 constexpr uint32_t G_SFA_COL0 = 256;                 // 8 columns per stage
 constexpr uint32_t G_SFB_COL0 = 256 + 8 * G_STAGES;  // 16 columns per stage
@@ -217,6 +218,64 @@ MXQ_DEV void store_row_codes(const uint32_t (&v)[128], const GArgs& a, int64_t r
   }
 }
 
+// Staged epilogue: a warp's 32 rows of up to 128 columns of C through its piece of shared
+// memory, 128 bytes of every row at a time, so that a store writes whole 128-byte lines
+// (four rows at a time).  A store straight from the accumulators has a row per lane and
+// touches 32 lines for 1 KB, one line a cycle: with few K stages to a tile that alone
+// takes longer than the products.  The pitch of 144 bytes keeps eight lanes' 16-byte
+// accesses on different banks both ways.
+MXQ_DEV void store_staged(const uint32_t (&v)[128], const GArgs& a, uint8_t* buf, int64_t row0,
+                          int rows, int64_t col0, int ncols) {
+  const int lane = threadIdx.x & 31, sub = lane >> 3, at = lane & 7;
+  const int per = a.out_bf16 ? 64 : 32;   // columns of 128 bytes
+  const int size = a.out_bf16 ? 2 : 4;
+  uint8_t* const mine = buf + lane * G_PITCH;
+  uint8_t* const c = static_cast<uint8_t*>(a.C) + ((row0 + sub) * a.N + col0) * size + at * 16;
+  const int64_t step = int64_t(4) * a.N * size;
+  auto out = [&](int first) {
+    __syncwarp();
+    const bool in = first + (at + 1) * (16 / size) <= ncols;
+#pragma unroll
+    for (int q = 0; q < 8; ++q) {
+      const int r = 4 * q + sub;
+      if (in && r < rows)
+        *reinterpret_cast<uint4*>(c + q * step + first * size) =
+            *reinterpret_cast<const uint4*>(buf + r * G_PITCH + at * 16);
+    }
+    __syncwarp();
+  };
+  if (a.out_bf16) {
+#pragma unroll
+    for (int s = 0; s < 2; ++s) {
+      if (s * per >= ncols) break;
+#pragma unroll
+      for (int q = 0; q < 8; ++q) {
+        uint32_t w[4];
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+          const __nv_bfloat162 b =
+              __floats2bfloat162_rn(__uint_as_float(v[64 * s + 8 * q + 2 * u]),
+                                    __uint_as_float(v[64 * s + 8 * q + 2 * u + 1]));
+          w[u] = *reinterpret_cast<const uint32_t*>(&b);
+        }
+        *reinterpret_cast<uint4*>(mine + q * 16) = make_uint4(w[0], w[1], w[2], w[3]);
+      }
+      out(s * per);
+    }
+  } else {
+#pragma unroll
+    for (int s = 0; s < 4; ++s) {
+      if (s * per >= ncols) break;
+#pragma unroll
+      for (int q = 0; q < 8; ++q)
+        *reinterpret_cast<uint4*>(mine + q * 16) =
+            make_uint4(v[32 * s + 4 * q], v[32 * s + 4 * q + 1], v[32 * s + 4 * q + 2],
+                       v[32 * s + 4 * q + 3]);
+      out(s * per);
+    }
+  }
+}
+
 // One work item (a 256x256 tile) as the roles of the kernel see it.
 struct Item {
   const GArgs* a;                            // what its problem's items have in common
@@ -233,7 +292,9 @@ struct Item {
 };
 
 // Work says which items a launch has and where they lie:
-//   Params, the launch's __grid_constant__ argument; TABLE, bytes of shared memory;
+//   Params, the launch's __grid_constant__ argument; STAGES of the operand ring;
+//   TABLE, bytes of shared memory; STAGED, whether the epilogue goes through shared
+//   memory (G_STAGED_BYTES of it);
 //   first(g), the arguments that all items share; prefetch(g), of its tensor maps;
 //   load(g, table), by all threads, once the previous grid is complete;
 //   an object per role, whose tiles() counts the items and at(t) describes item t
@@ -244,10 +305,10 @@ __global__ void __launch_bounds__(G_THREADS, 1)
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~static_cast<uintptr_t>(1023));
-  uint64_t* full = reinterpret_cast<uint64_t*>(smem + G_STAGES * G_STAGE_BYTES);
-  uint64_t* empty = full + G_STAGES;
-  uint64_t* sf_ready = empty + G_STAGES;
-  uint64_t* tmem_full = sf_ready + G_STAGES;
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + Work::STAGES * G_STAGE_BYTES);
+  uint64_t* empty = full + Work::STAGES;
+  uint64_t* sf_ready = empty + Work::STAGES;
+  uint64_t* tmem_full = sf_ready + Work::STAGES;
   uint64_t* tmem_empty = tmem_full + 1;      // leader: both CTAs drained the accumulator
   uint64_t* drain = tmem_empty + 1;
   uint32_t* tmem_base_slot = reinterpret_cast<uint32_t*>(drain + 1);
@@ -260,10 +321,10 @@ __global__ void __launch_bounds__(G_THREADS, 1)
   const uint32_t rank = cluster_rank();
   const bool leader = rank == 0;
   const GArgs& a0 = Work::first(g);   // format, epilogue kind and wait limit of the launch
-  void* table = smem + G_STAGES * G_STAGE_BYTES + G_BAR_BYTES;
+  void* table = smem + Work::STAGES * G_STAGE_BYTES + G_BAR_BYTES;
   if (threadIdx.x == 0) {
     Work::prefetch(g);
-    for (int s = 0; s < G_STAGES; ++s) {
+    for (int s = 0; s < Work::STAGES; ++s) {
       mbar_init(smem_u32(&full[s]), 1);    // leader: one arrival, bytes of both CTAs
       mbar_init(smem_u32(&empty[s]), 1);
       mbar_init(smem_u32(&sf_ready[s]), 2);  // two scale-copy warps
@@ -334,7 +395,7 @@ __global__ void __launch_bounds__(G_THREADS, 1)
           tma_load_2d_pair(st + G_A_BYTES + G_B_BYTES + G_SFA_BYTES + sf_bytes_a, it.tsb, bar,
                            0, srow_b1 + kc);
           ++issued;
-          if (++s == G_STAGES) { s = 0; phase ^= 1; }
+          if (++s == Work::STAGES) { s = 0; phase ^= 1; }
         }
       }
       if (!leader) {
@@ -351,9 +412,9 @@ __global__ void __launch_bounds__(G_THREADS, 1)
         }
         uint32_t last = issued;
         if (*peer_issued != kNotYet && *peer_issued > last) last = *peer_issued;
-        for (uint32_t k = last > G_STAGES ? last - G_STAGES : 0; k < last; ++k) {
-          if (k >= issued) mbar_arrive_expect_tx(smem_u32(&full[k % G_STAGES]), cta_tx);
-          if (!mbar_wait(smem_u32(&full[k % G_STAGES]), (k / G_STAGES) & 1, tmo)) {
+        for (uint32_t k = last > Work::STAGES ? last - Work::STAGES : 0; k < last; ++k) {
+          if (k >= issued) mbar_arrive_expect_tx(smem_u32(&full[k % Work::STAGES]), cta_tx);
+          if (!mbar_wait(smem_u32(&full[k % Work::STAGES]), (k / Work::STAGES) & 1, tmo)) {
             // a stage one CTA never issued: later stages were not issued either
             record_error(&g_err_gemm, MXQ_ERR_TIMEOUT, SITE_GEMM_FULL);
             break;
@@ -420,7 +481,7 @@ __global__ void __launch_bounds__(G_THREADS, 1)
             if (n > 3) mma_mxf8_pair(tmem, ad + 6, bd + 6, idesc[3], sfa_t, sfb_t, 1u);
           }
           tc_commit_pair_mc(smem_u32(&empty[s]), 0x3);   // stage free in both CTAs
-          if (++s == G_STAGES) { s = 0; phase ^= 1; }
+          if (++s == Work::STAGES) { s = 0; phase ^= 1; }
         }
         if (!ok) break;
         tc_commit_pair_mc(smem_u32(tmem_full), 0x3);     // accumulators ready in both CTAs
@@ -482,7 +543,7 @@ __global__ void __launch_bounds__(G_THREADS, 1)
           tc_cp_sf_pair(sfb_t + 4, sfb_smem + sf_bytes_a);
         }
         tc_commit_pair_mc(smem_u32(&sf_ready[s]), 0x1);
-        if (++s == G_STAGES) { s = 0; phase ^= 1; }
+        if (++s == Work::STAGES) { s = 0; phase ^= 1; }
       }
     }
   } else {
@@ -515,7 +576,8 @@ __global__ void __launch_bounds__(G_THREADS, 1)
 #pragma unroll
         for (int i = 0; i < 128; ++i) v[i] = 0u;
       }
-      const uint32_t pn = t + ncl < n_tiles ? it.pace_ns : 0u;   // last tile: no pacing
+      [[maybe_unused]] const uint32_t pn =
+          t + ncl < n_tiles ? it.pace_ns : 0u;   // last tile: no pacing
       const int64_t row = (int64_t(it.mp) * G_CLUSTER + rank) * G_BM + quad * 32 + lane;
       const int64_t col0 = int64_t(it.nt) * G_BN + colh * 128;
       if (Work::QUANTIZES && a.q_scale_tc && row >= a.M &&
@@ -525,7 +587,16 @@ __global__ void __launch_bounds__(G_THREADS, 1)
         uint8_t* chunk = a.q_scales + ((row >> 7) * (int64_t(a.N) >> 7) + (col0 >> 7)) * 512;
         *reinterpret_cast<uint32_t*>(chunk + (row & 31) * 16 + ((row & 127) >> 5) * 4) = 0u;
       }
-      if (row < it.rows && col0 < a.N &&
+      if constexpr (Work::STAGED) {
+        uint8_t* const buf = smem + Work::STAGES * G_STAGE_BYTES + G_BAR_BYTES + Work::TABLE +
+                             (warp - 2) * (32 * G_PITCH);
+        const int rows = static_cast<int>(min(int64_t(it.rows) - (row - lane), int64_t(32)));
+        if (rows > 0 && col0 < a.N &&
+            MXQ_IN_BOUNDS(Work::inside(it) && row - lane + rows <= it.rows, &g_err_gemm,
+                          SITE_B_GEMM_STORE))
+          store_staged(v, a, buf, it.c0 + row - lane, rows, col0,
+                       static_cast<int>(min(a.N - col0, int64_t(128))));
+      } else if (row < it.rows && col0 < a.N &&
           MXQ_IN_BOUNDS(Work::inside(it) && row >= 0 && col0 >= 0 && (col0 & 31) == 0,
                         &g_err_gemm, SITE_B_GEMM_STORE)) {
         const int64_t ncols = (a.N - col0) < 128 ? (a.N - col0) : 128;
@@ -613,7 +684,9 @@ int max_gemm_clusters(cudaLaunchConfig_t cfg) {
 // Launches the kernel on as many clusters as the device holds, at most `items`.
 template <typename Work>
 mxq_status gemm_kernel_run(const typename Work::Params& g, int64_t items, void* stream) {
-  constexpr int smem = G_SMEM + Work::TABLE;
+  constexpr int smem = Work::STAGES * G_STAGE_BYTES + G_BAR_BYTES + Work::TABLE +
+                       (Work::STAGED ? G_STAGED_BYTES : 0) + 1024;
+  static_assert(Work::STAGES <= G_STAGES && Work::TABLE % 16 == 0, "shared memory layout");
   static_assert(smem <= 232448, "shared memory of a CTA");
   if (!ensure_dynamic_smem(reinterpret_cast<const void*>(mx_gemm_kernel<Work>), smem))
     return MXQ_ERR_CUDA;
