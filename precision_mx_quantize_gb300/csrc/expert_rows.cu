@@ -10,6 +10,8 @@
 //
 // Gather, combine and their gradients move rows: a team of 32 to 256 threads holds a
 // token and all rows of its choices, so that a token's row is read (or written) once.
+#include <mutex>
+
 #include "fp8_common.cuh"
 #include "mxq_host.h"
 
@@ -145,24 +147,26 @@ struct RowsArgs {
 };
 
 constexpr int R_THREADS = 256;
-constexpr int R_GROUP = 8;   // choices handled together
 
-// Rows of up to R_GROUP choices of a token from j0 on and their weights; -1 and weight 0
-// where a choice has no row, so that what follows needs no branches.  A row outside the
-// buffer is reported and left out.
+// Rows of up to G choices of a token from j0 on and their weights.  ready() puts -1 and
+// weight 0 where a choice has no row, so that what follows needs no branches; a row
+// outside the buffer is reported and left out.
+template <int G>
 struct Choices {
-  int32_t row[R_GROUP];
-  float w[R_GROUP];
-  MXQ_DEV void load(const RowsArgs& a, int64_t t, int j0, bool live) {
+  int32_t row[G];
+  float w[G];
+  MXQ_DEV void load(const RowsArgs& a, int64_t t, int j0) {
 #pragma unroll
-    for (int j = 0; j < R_GROUP; ++j) {
-      const bool is = live && j0 + j < a.topk;
+    for (int j = 0; j < G; ++j) {
+      const bool is = t < a.tokens && j0 + j < a.topk;
       row[j] = is ? a.row_of[t * a.topk + j0 + j] : -1;
       w[j] = is && a.weights ? a.weights[t * a.topk + j0 + j] : 1.0f;
     }
+  }
+  MXQ_DEV void ready(const RowsArgs& a) {
     bool bad = false;
 #pragma unroll
-    for (int j = 0; j < R_GROUP; ++j) {
+    for (int j = 0; j < G; ++j) {
       if (row[j] >= a.rows) {
         bad = true;
         row[j] = -1;
@@ -257,162 +261,240 @@ MXQ_DEV void clear_padding(const RowsArgs& a, int64_t e, int at) {
       zero.store(static_cast<T*>(a.out) + r * a.cols + c, a.team, a.cols - c);
 }
 
-// The token (or, past them, the expert whose padding is cleared) of a thread's team and
-// the thread's place in it.
-MXQ_DEV int64_t team_token(const RowsArgs& a, int& at) {
-  at = threadIdx.x & (a.team - 1);
-  return int64_t(blockIdx.x) * (R_THREADS / a.team) + threadIdx.x / a.team;
+// Teams walk the tokens (and, past them, the experts whose padding they clear) a grid
+// apart, and load a token's choices while the one before is on its way.
+struct Team {
+  int at, threads;   // place in the team, its size
+  int64_t t, step;   // first token, tokens from one to the next
+  MXQ_DEV explicit Team(const RowsArgs& a) : threads(a.team) {
+    const int per = R_THREADS / a.team;
+    at = threadIdx.x & (a.team - 1);
+    t = int64_t(blockIdx.x) * per + threadIdx.x / a.team;
+    step = int64_t(gridDim.x) * per;
+  }
+};
+
+// The pieces of all choices' rows at column c.  VEC: a choice without a row reads the
+// first one, which is there and not used, because a branch around a load makes the next
+// one wait (combine, 8192x8 tokens x 4096 bf16: 141 us with branches, 117 us without).
+// Unaligned rows have a load per element and more of them in flight; leaving out those
+// of no use is worth more there (backward, 4099x3 x 1001 fp32: 25.5 us, else 33.2 us).
+template <typename T, bool VEC, int G>
+MXQ_DEV void load_rows(Piece<T, VEC> (&v)[G], const Choices<G>& k, const T* y, const RowsArgs& a,
+                       const Team& team, int64_t c) {
+#pragma unroll
+  for (int j = 0; j < G; ++j) {
+    if constexpr (VEC) {
+      v[j].load(y + max(k.row[j], 0) * a.cols, team.threads, a.cols - c);
+    } else {
+      v[j].clear();
+      if (k.row[j] >= 0) v[j].load(y + k.row[j] * a.cols, team.threads, a.cols - c);
+    }
+  }
 }
 
-template <typename T, bool VEC>
+template <typename T, bool VEC, int G>
 __global__ void __launch_bounds__(R_THREADS) expert_gather(const RowsArgs a) {
   using P = Piece<T, VEC>;
   griddep_wait();
   griddep_launch_dependents();
-  int at;
-  const int64_t t = team_token(a, at);
-  if (t >= a.tokens) {
-    clear_padding<T, VEC>(a, t - a.tokens, at);
-    return;
-  }
-  const T* x = static_cast<const T*>(a.x) + t * a.cols;
+  const Team team(a);
   T* out = static_cast<T*>(a.out);
-  for (int j0 = 0; j0 < a.topk; j0 += R_GROUP) {
-    Choices k;
-    k.load(a, t, j0, true);
-    for (int64_t c = int64_t(at) * P::REACH; c < a.cols; c += int64_t(a.team) * P::N) {
-      P v;
-      v.load(x + c, a.team, a.cols - c);
-      float f[P::N];
-      v.get(f);
+  Choices<G> next;
+  next.load(a, team.t, 0);
+  int64_t t = team.t;
+  for (; t < a.tokens; t += team.step) {
+    Choices<G> k = next;
+    next.load(a, t + team.step, 0);
+    const T* x = static_cast<const T*>(a.x) + t * a.cols;
+    for (int j0 = 0; j0 < a.topk; j0 += G) {
+      if (j0) k.load(a, t, j0);
+      k.ready(a);
+      for (int64_t c = int64_t(team.at) * P::REACH; c < a.cols; c += int64_t(team.threads) * P::N) {
+        P v;
+        v.load(x + c, team.threads, a.cols - c);
+        float f[P::N];
+        v.get(f);
 #pragma unroll
-      for (int j = 0; j < R_GROUP; ++j) {
-        if (k.row[j] < 0) continue;
-        P s = v;
-        if (a.weights) {
-          float g[P::N];
+        for (int j = 0; j < G; ++j) {
+          if (k.row[j] < 0) continue;
+          P s = v;
+          if (a.weights) {
+            float g[P::N];
 #pragma unroll
-          for (int i = 0; i < P::N; ++i) g[i] = f[i] * k.w[j];
-          s.set(g);
+            for (int i = 0; i < P::N; ++i) g[i] = f[i] * k.w[j];
+            s.set(g);
+          }
+          s.store(out + k.row[j] * a.cols + c, team.threads, a.cols - c);
         }
-        s.store(out + k.row[j] * a.cols + c, a.team, a.cols - c);
       }
     }
   }
+  for (; t < a.tokens + a.experts; t += team.step) clear_padding<T, VEC>(a, t - a.tokens, team.at);
 }
 
 // out[t] = sum_j w[t][j] y[row of (t, j)], in the order of j, in fp32.  The loads of all
 // choices are in flight together.
-template <typename T, bool VEC>
+template <typename T, bool VEC, int G>
 __global__ void __launch_bounds__(R_THREADS) expert_combine(const RowsArgs a) {
   using P = Piece<T, VEC>;
   griddep_wait();
   griddep_launch_dependents();
-  int at;
-  const int64_t t = team_token(a, at);
-  if (t >= a.tokens) return;
+  const Team team(a);
   const T* y = static_cast<const T*>(a.y);
-  Choices k;
-  k.load(a, t, 0, true);
-  for (int64_t c = int64_t(at) * P::REACH; c < a.cols; c += int64_t(a.team) * P::N) {
-    float sum[P::N];
+  Choices<G> next;
+  next.load(a, team.t, 0);
+  for (int64_t t = team.t; t < a.tokens; t += team.step) {
+    Choices<G> k = next;
+    next.load(a, t + team.step, 0);
+    k.ready(a);
+    for (int64_t c = int64_t(team.at) * P::REACH; c < a.cols; c += int64_t(team.threads) * P::N) {
+      float sum[P::N];
 #pragma unroll
-    for (int i = 0; i < P::N; ++i) sum[i] = 0.0f;
-    for (int j0 = 0; j0 < a.topk; j0 += R_GROUP) {
-      if (a.topk > R_GROUP) k.load(a, t, j0, true);
-      P v[R_GROUP];
+      for (int i = 0; i < P::N; ++i) sum[i] = 0.0f;
+      for (int j0 = 0; j0 < a.topk; j0 += G) {
+        if (a.topk > G) {
+          k.load(a, t, j0);
+          k.ready(a);
+        }
+        P v[G];
+        load_rows(v, k, y + c, a, team, c);
 #pragma unroll
-      for (int j = 0; j < R_GROUP; ++j) {
-        v[j].clear();
-        if (k.row[j] >= 0) v[j].load(y + k.row[j] * a.cols + c, a.team, a.cols - c);
+        for (int j = 0; j < G; ++j) {
+          float f[P::N];
+          v[j].get(f);
+#pragma unroll
+          for (int i = 0; i < P::N; ++i)
+            sum[i] = k.row[j] < 0 ? sum[i] : fmaf(k.w[j], f[i], sum[i]);
+        }
       }
-#pragma unroll
-      for (int j = 0; j < R_GROUP; ++j) {
-        float f[P::N];
-        v[j].get(f);
-#pragma unroll
-        for (int i = 0; i < P::N; ++i) sum[i] = fmaf(k.w[j], f[i], sum[i]);
-      }
+      P s;
+      s.set(sum);
+      s.store(static_cast<T*>(a.out) + t * a.cols + c, team.threads, a.cols - c);
     }
-    P s;
-    s.set(sum);
-    s.store(static_cast<T*>(a.out) + t * a.cols + c, a.team, a.cols - c);
   }
 }
 
 // out[row of (t, j)] = w[t][j] x[t],  dweights[t][j] = <x[t], y[row of (t, j)]>.  out may
 // be y: a thread reads a piece of all its rows before it writes any.
-template <typename T, bool VEC>
+template <typename T, bool VEC, int G>
 __global__ void __launch_bounds__(R_THREADS) expert_combine_backward(const RowsArgs a) {
   using P = Piece<T, VEC>;
-  __shared__ float part[R_THREADS / 32][R_GROUP];
+  __shared__ float part[2][R_THREADS / 32][G];
   griddep_wait();
   griddep_launch_dependents();
-  int at;
-  const int64_t t = team_token(a, at);
-  if (t >= a.tokens) clear_padding<T, VEC>(a, t - a.tokens, at);
-  const bool live = t < a.tokens;
-  const T* x = static_cast<const T*>(a.x) + t * a.cols;
+  const Team team(a);
   const T* y = static_cast<const T*>(a.y);
   T* out = static_cast<T*>(a.out);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  for (int j0 = 0; j0 < a.topk; j0 += R_GROUP) {
-    Choices k;
-    k.load(a, t, j0, live);
-    float dot[R_GROUP];
+  Choices<G> next;
+  next.load(a, team.t, 0);
+  int64_t t = team.t;
+  int turn = 0;
+  // a CTA's teams make the same number of turns: the sums between its warps need all
+  const int64_t first = int64_t(blockIdx.x) * (R_THREADS / a.team);
+  for (int64_t block = first; block < a.tokens; block += team.step, t += team.step) {
+    Choices<G> k = next;
+    next.load(a, t + team.step, 0);
+    const bool live = t < a.tokens;
+    if (!live) clear_padding<T, VEC>(a, t - a.tokens, team.at);
+    const T* x = static_cast<const T*>(a.x) + t * a.cols;
+    for (int j0 = 0; j0 < a.topk; j0 += G, turn ^= 1) {
+      if (j0) k.load(a, t, j0);
+      k.ready(a);
+      float dot[G];
 #pragma unroll
-    for (int j = 0; j < R_GROUP; ++j) dot[j] = 0.0f;
-    for (int64_t c = int64_t(at) * P::REACH; live && c < a.cols; c += int64_t(a.team) * P::N) {
-      P d, v[R_GROUP];
-      d.load(x + c, a.team, a.cols - c);
+      for (int j = 0; j < G; ++j) dot[j] = 0.0f;
+      for (int64_t c = int64_t(team.at) * P::REACH; live && c < a.cols;
+           c += int64_t(team.threads) * P::N) {
+        P d, v[G];
+        d.load(x + c, team.threads, a.cols - c);
+        load_rows(v, k, y + c, a, team, c);
+        float f[P::N];
+        d.get(f);
 #pragma unroll
-      for (int j = 0; j < R_GROUP; ++j) {
-        v[j].clear();
-        if (k.row[j] >= 0) v[j].load(y + k.row[j] * a.cols + c, a.team, a.cols - c);
-      }
-      float f[P::N];
-      d.get(f);
+        for (int j = 0; j < G; ++j) {
+          float g[P::N];
+          v[j].get(g);
 #pragma unroll
-      for (int j = 0; j < R_GROUP; ++j) {
-        float g[P::N];
-        v[j].get(g);
-#pragma unroll
-        for (int i = 0; i < P::N; ++i) {
-          dot[j] = fmaf(f[i], g[i], dot[j]);
-          g[i] = f[i] * k.w[j];
+          for (int i = 0; i < P::N; ++i) {
+            dot[j] = fmaf(f[i], g[i], dot[j]);
+            g[i] = f[i] * k.w[j];
+          }
+          v[j].set(g);
         }
-        v[j].set(g);
+#pragma unroll
+        for (int j = 0; j < G; ++j)
+          if (k.row[j] >= 0) v[j].store(out + k.row[j] * a.cols + c, team.threads, a.cols - c);
       }
 #pragma unroll
-      for (int j = 0; j < R_GROUP; ++j)
-        if (k.row[j] >= 0) v[j].store(out + k.row[j] * a.cols + c, a.team, a.cols - c);
-    }
-    __syncthreads();   // the last group's sums have been read
+      for (int j = 0; j < G; ++j) {
+        float s = k.row[j] >= 0 ? dot[j] : 0.0f;
 #pragma unroll
-    for (int j = 0; j < R_GROUP; ++j) {
-      float s = k.row[j] >= 0 ? dot[j] : 0.0f;
-#pragma unroll
-      for (int d = 16; d; d >>= 1) s += __shfl_xor_sync(~0u, s, d);
-      if (lane == 0) part[warp][j] = s;
-    }
-    __syncthreads();
-    if (live && at < R_GROUP && j0 + at < a.topk) {
-      float s = 0.0f;
-      for (int v = 0; v < a.team / 32; ++v) s += part[warp + v][at];
-      a.dweights[t * a.topk + j0 + at] = s;
+        for (int d = 16; d; d >>= 1) s += __shfl_xor_sync(~0u, s, d);
+        if (lane == 0) part[turn][warp][j] = s;
+      }
+      // two buffers in turn: whoever writes one again has passed the barrier of the
+      // other, behind this one's readers
+      __syncthreads();
+      if (live && team.at < G && j0 + team.at < a.topk) {
+        float s = 0.0f;
+        for (int v = 0; v < team.threads / 32; ++v) s += part[turn][warp + v][team.at];
+        a.dweights[t * a.topk + j0 + team.at] = s;
+      }
     }
   }
+  for (; t < a.tokens + a.experts; t += team.step) clear_padding<T, VEC>(a, t - a.tokens, team.at);
 }
 
 enum RowsOp { GATHER, COMBINE, BACKWARD };
 
-template <typename T, bool VEC>
-bool rows_launch(RowsOp op, unsigned grid, cudaStream_t st, const RowsArgs& a) {
-  switch (op) {
-    case GATHER: return launch_early(expert_gather<T, VEC>, grid, R_THREADS, 0, st, a);
-    case COMBINE: return launch_early(expert_combine<T, VEC>, grid, R_THREADS, 0, st, a);
-    default: return launch_early(expert_combine_backward<T, VEC>, grid, R_THREADS, 0, st, a);
+// Teams that the device holds at once, or as many as there are.
+template <void (*KERNEL)(RowsArgs)>
+bool rows_launch_resident(int64_t ctas, cudaStream_t st, const RowsArgs& a) {
+  static std::mutex mu;
+  static int resident[64] = {0};   // CTAs of an SM, per device
+  int dev = 0, n = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return false;
+  {
+    std::lock_guard<std::mutex> lock(mu);
+    n = resident[dev];
   }
+  if (n == 0) {
+    if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, KERNEL, R_THREADS, 0) != cudaSuccess ||
+        n <= 0) {
+      cudaGetLastError();
+      n = 1;
+    }
+    std::lock_guard<std::mutex> lock(mu);
+    resident[dev] = n;
+  }
+  const int64_t grid = std::min<int64_t>(ctas, int64_t(n) * sm_count());
+  return launch_early(KERNEL, static_cast<unsigned>(grid), R_THREADS, 0, st, a);
+}
+
+template <typename T, bool VEC, int G>
+bool rows_launch_group(RowsOp op, int64_t ctas, cudaStream_t st, const RowsArgs& a) {
+  switch (op) {
+    // one token a team: its stores wait for nothing (8192x8 x 4096 bf16 with the order:
+    // 107 us; 118 us where teams walk the tokens)
+    case GATHER:
+      return launch_early(expert_gather<T, VEC, G>, static_cast<unsigned>(ctas), R_THREADS, 0, st,
+                          a);
+    case COMBINE: return rows_launch_resident<expert_combine<T, VEC, G>>(ctas, st, a);
+    default: return rows_launch_resident<expert_combine_backward<T, VEC, G>>(ctas, st, a);
+  }
+}
+
+// As many choices at a time as there are, rounded up to two, at most eight: the others'
+// loads, registers and instructions (combine, 20000x6 x 512 fp32: 59 us with eight, 48 us
+// with six).
+template <typename T, bool VEC>
+bool rows_launch(RowsOp op, int64_t ctas, cudaStream_t st, const RowsArgs& a) {
+  if (a.topk <= 2) return rows_launch_group<T, VEC, 2>(op, ctas, st, a);
+  if (a.topk <= 4) return rows_launch_group<T, VEC, 4>(op, ctas, st, a);
+  if (a.topk <= 6) return rows_launch_group<T, VEC, 6>(op, ctas, st, a);
+  return rows_launch_group<T, VEC, 8>(op, ctas, st, a);
 }
 
 mxq_status rows_run(RowsOp op, const mxq_expert_rows_args* q, void* stream) {
@@ -430,6 +512,13 @@ mxq_status rows_run(RowsOp op, const mxq_expert_rows_args* q, void* stream) {
       ((op == COMBINE || q->rows) && !q->out) || (pads && (!q->offsets || !q->counts)) ||
       (op == BACKWARD && !q->dweights))
     return MXQ_ERR_ARG;
+  if (q->rows == 0 && op != GATHER) {   // no choice has a row
+    const size_t bytes = op == COMBINE ? size_t(q->tokens) * q->cols *
+                                             (q->dtype == MXQ_OUT_BF16 ? 2 : 4)
+                                       : size_t(q->tokens) * q->topk * 4;
+    return cudaMemsetAsync(op == COMBINE ? q->out : q->dweights, 0, bytes,
+                           static_cast<cudaStream_t>(stream)) == cudaSuccess ? MXQ_OK : MXQ_ERR_CUDA;
+  }
   const void* words[] = {q->row_of, q->offsets, q->counts, q->weights, q->dweights};
   for (const void* p : words)
     if (!aligned4(p)) return MXQ_ERR_ALIGN;
@@ -458,7 +547,7 @@ mxq_status rows_run(RowsOp op, const mxq_expert_rows_args* q, void* stream) {
   while (a.team < R_THREADS && a.team * 2 <= pieces) a.team *= 2;
   const int per = R_THREADS / a.team;
   const int64_t teams = a.tokens + a.experts;
-  const unsigned grid = static_cast<unsigned>((teams + per - 1) / per);
+  const int64_t grid = (teams + per - 1) / per;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   using B = __nv_bfloat16;
   const bool ok = bf16 ? (vec ? rows_launch<B, true>(op, grid, st, a)

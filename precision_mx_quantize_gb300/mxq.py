@@ -975,15 +975,18 @@ def expert_order(ids: torch.Tensor, experts: int, align: int = 1):
     experts, align = int(experts), int(align)
     if not 1 <= experts <= 1024:
         raise ValueError(f"experts must be 1 to 1024, got {experts}")
-    n, dev = ids.numel(), ids.get_device()
-    meta = torch.empty(n + 2 * experts + 1 + (_order_workspace(n, experts) + 3) // 4,
-                       dtype=torch.int32, device=ids.device)
-    row_of, offsets, counts, ws = meta.split_with_sizes(
-        [n, experts + 1, experts, meta.numel() - n - 2 * experts - 1])
+    tokens, topk = ids.shape
+    n, dev = tokens * topk, ids.get_device()
+    where = ids.device
+    row_of = torch.empty((tokens, topk), dtype=torch.int32, device=where)
+    offsets = torch.empty(experts + 1, dtype=torch.int32, device=where)
+    counts = torch.empty(experts, dtype=torch.int32, device=where)
+    ws_bytes = _order_workspace(n, experts)
+    ws = torch.empty(ws_bytes, dtype=torch.uint8, device=where) if ws_bytes else None
     _ok(mxq_expert_order(ids.data_ptr(), ids.element_size(), n, experts, align, row_of.data_ptr(),
-                         offsets.data_ptr(), counts.data_ptr(), ws.data_ptr(), 4 * ws.numel(),
+                         offsets.data_ptr(), counts.data_ptr(), _ptr(ws), ws_bytes,
                          _stream(dev)), "mxq_expert_order")
-    return row_of.view(ids.shape), offsets, counts
+    return row_of, offsets, counts
 
 
 def _need_tokens(t, name):
@@ -1109,23 +1112,43 @@ def gemm_experts_wgrad_workspace(rows, M, N, experts, fmt, device):
     return torch.empty(max(n, 256), dtype=torch.uint8, device=device)
 
 
-def _need_experts(A, offsets):
-    """Returns (A's device index, the number of experts)."""
-    _need(A, "A", torch.uint8, 0)
-    dev = A.get_device()
-    _need(offsets, "offsets", torch.int32, 2, dev)
-    return dev, offsets.numel() - 1
+def _count_experts(offsets):
+    if not isinstance(offsets, torch.Tensor) or offsets.dim() != 1:
+        raise ValueError("offsets must be a 1-D torch.Tensor [experts + 1]")
+    return offsets.numel() - 1
 
 
 @functools.lru_cache(maxsize=4096)
-def _expert_scale_bytes(experts, N, K, fmt, b_scale_layout):
-    """Bytes of the scales of B [experts, N, K]."""
-    if b_scale_layout == SCALES_ROWMAJOR:
-        return experts * N * (K // 32)
-    n = int(mxq_scales_tc_bytes(N, K))
-    if n == 0 or (fmt == E2M1 and K % 256 != 0):
-        raise ValueError(f"no tensor-core scale layout for {N} lines x {K}")
-    return experts * n
+def _experts_sizes(rows, N, K, experts, fmt, b_scale_layout):
+    """Bytes of mx_gemm_experts' A, sA, B, sB and workspace, and the library's codes of
+    the format and the layout."""
+    f, layout = FMTS[fmt], SCALE_LAYOUTS[b_scale_layout]
+    kb = K // 2 if f == E2M1 else K
+    sb = N * (K // 32)
+    if layout == SCALES_TC:
+        sb = int(mxq_scales_tc_bytes(N, K))
+        if sb == 0 or (f == E2M1 and K % 256 != 0):
+            raise ValueError(f"no tensor-core scale layout for {N} lines x {K}")
+    return (rows * kb, rows * (K // 32), experts * N * kb, experts * sb,
+            max(_experts_workspace(rows, N, K, experts, f, layout), 256), f, layout)
+
+
+@functools.lru_cache(maxsize=4096)
+def _experts_wgrad_sizes(rows, M, N, experts, fmt):
+    """The same of mx_gemm_experts_wgrad."""
+    f = FMTS[fmt]
+    rb = rows // 2 if f == E2M1 else rows
+    return (M * rb, M * (rows // 32), N * rb, N * (rows // 32),
+            max(_experts_wgrad_workspace(rows, M, N, experts, f), 256), f)
+
+
+def _need_product(A, sA, B, sB, offsets, sizes, dev):
+    """The operands of a product grouped by expert."""
+    _need(A, "codes_A", torch.uint8, sizes[0], dev)
+    _need(sA, "scales_A", torch.uint8, sizes[1], dev)
+    _need(B, "codes_B", torch.uint8, sizes[2], dev)
+    _need(sB, "scales_B", torch.uint8, sizes[3], dev)
+    _need(offsets, "offsets", torch.int32, 2, dev)
 
 
 def mx_gemm_experts(A, sA, B, sB, offsets, fmt, rows, N, K, out_dtype=torch.float32, out=None,
@@ -1139,26 +1162,24 @@ def mx_gemm_experts(A, sA, B, sB, offsets, fmt, rows, N, K, out_dtype=torch.floa
     another.  offsets: int32 [experts + 1] on the device (expert_order).  Rows that no
     expert holds are not written.  workspace: as gemm_experts_workspace returns it, for
     callers that keep one."""
-    od, f, layout = _out_code(out_dtype), FMTS[fmt], SCALE_LAYOUTS[b_scale_layout]
-    dev, experts = _need_experts(A, offsets)
+    od = _out_code(out_dtype)
+    experts = _count_experts(offsets)
     rows, N, K = int(rows), int(N), int(K)
-    kb = K // 2 if f == E2M1 else K
-    _need(A, "codes_A", torch.uint8, rows * kb, dev)
-    _need(sA, "scales_A", torch.uint8, rows * (K // 32), dev)
-    _need(B, "codes_B", torch.uint8, experts * N * kb, dev)
-    _need(sB, "scales_B", torch.uint8, _expert_scale_bytes(experts, N, K, f, layout), dev)
+    sizes = _experts_sizes(rows, N, K, experts, fmt, b_scale_layout)
+    _need(A, "codes_A", torch.uint8, 0)
+    dev = A.get_device()
+    _need_product(A, sA, B, sB, offsets, sizes, dev)
     if out is None:
         out = torch.empty((rows, N), dtype=out_dtype, device=A.device)
     else:
         _need_rows(out, "out", out_dtype, (rows, N), dev)
     if workspace is None:
-        workspace = torch.empty(max(_experts_workspace(rows, N, K, experts, f, layout), 256),
-                                dtype=torch.uint8, device=A.device)
+        workspace = torch.empty(sizes[4], dtype=torch.uint8, device=A.device)
     else:
         _need(workspace, "workspace", torch.uint8, 0, dev)   # its size is checked by the library
     a = _EXPERTS_ARGS.pack(A.data_ptr(), sA.data_ptr(), B.data_ptr(), sB.data_ptr(),
                            offsets.data_ptr(), out.data_ptr(), workspace.data_ptr(),
-                           workspace.numel(), rows, 0, N, K, experts, f, od, layout)
+                           workspace.numel(), rows, 0, N, K, experts, sizes[5], od, sizes[6])
     _ok(mxq_gemm_experts(a, _stream(dev)), "mxq_gemm_experts")
     return out
 
@@ -1172,14 +1193,13 @@ def mx_gemm_experts_wgrad(A, sA, B, sB, offsets, fmt, M, N, rows, out_dtype=torc
     mx_quantize(..., "col") writes them.  offsets: multiples of 32 (E2M1: 64), as
     expert_order(..., align=32) gives them.  workspace: as
     gemm_experts_wgrad_workspace returns it, for callers that keep one."""
-    od, f = _out_code(out_dtype), FMTS[fmt]
-    dev, experts = _need_experts(A, offsets)
+    od = _out_code(out_dtype)
+    experts = _count_experts(offsets)
     rows, M, N = int(rows), int(M), int(N)
-    rb = rows // 2 if f == E2M1 else rows
-    _need(A, "codes_A", torch.uint8, M * rb, dev)
-    _need(sA, "scales_A", torch.uint8, M * (rows // 32), dev)
-    _need(B, "codes_B", torch.uint8, N * rb, dev)
-    _need(sB, "scales_B", torch.uint8, N * (rows // 32), dev)
+    sizes = _experts_wgrad_sizes(rows, M, N, experts, fmt)
+    _need(A, "codes_A", torch.uint8, 0)
+    dev = A.get_device()
+    _need_product(A, sA, B, sB, offsets, sizes, dev)
     if out is None:
         out = torch.empty((experts, M, N), dtype=out_dtype, device=A.device)
     else:
@@ -1187,13 +1207,13 @@ def mx_gemm_experts_wgrad(A, sA, B, sB, offsets, fmt, M, N, rows, out_dtype=torc
         if out.dim() > 1 and out.size(-1) != N:
             raise ValueError(f"out has rows of {out.size(-1)} elements; they must hold {N}")
     if workspace is None:
-        workspace = torch.empty(max(_experts_wgrad_workspace(rows, M, N, experts, f), 256),
-                                dtype=torch.uint8, device=A.device)
+        workspace = torch.empty(sizes[4], dtype=torch.uint8, device=A.device)
     else:
         _need(workspace, "workspace", torch.uint8, 0, dev)   # its size is checked by the library
     a = _EXPERTS_ARGS.pack(A.data_ptr(), sA.data_ptr(), B.data_ptr(), sB.data_ptr(),
                            offsets.data_ptr(), out.data_ptr(), workspace.data_ptr(),
-                           workspace.numel(), rows, M, N, 0, experts, f, od, SCALES_ROWMAJOR)
+                           workspace.numel(), rows, M, N, 0, experts, sizes[5], od,
+                           SCALES_ROWMAJOR)
     _ok(mxq_gemm_experts_wgrad(a, _stream(dev)), "mxq_gemm_experts_wgrad")
     return out
 
@@ -1225,8 +1245,9 @@ def _overlap(buffers):
 
 
 class AdamWPlan:
-    """The tensors that adamw_step updates, checked once.  It keeps the tensors; one whose
-    storage has moved since is looked up anew at the next step."""
+    """The tensors that adamw_step updates, checked once.  It keeps them, and its own
+    reference to their memory; a parameter or weight that has moved since is looked up
+    anew at the next step (the moments stay where they are)."""
 
     def __init__(self, params, states, weights=None, weight_decay=0.0):
         self.params, self.states = list(params), list(states)
@@ -1275,16 +1296,44 @@ class AdamWPlan:
             raise ValueError(f"{twice[0]} and {twice[1]} share memory")
         self.bits, self.device = bits or 32, dev
         self.numels = [p.numel() for p in self.params]
-        self._tensors = [t for _, t in buffers]
-        self._places = list(map(torch.Tensor.data_ptr, self._tensors))
+        self._movable = self.params + [w for w in self.weights if w is not None]
+        self._places = list(map(torch.Tensor.data_ptr, self._movable))
+        self._memory = [t.detach() for _, t in buffers]
         self._table = b"".join(table)
-        self._written = set(self._places)
+        self._written = {t.data_ptr() for _, t in buffers if t.numel()}
+        self._grads = struct.Struct(f"@{len(table)}P")
 
     def table(self):
-        """The tensors' part of a launch; taken anew where a tensor has moved."""
-        if list(map(torch.Tensor.data_ptr, self._tensors)) != self._places:
+        """The tensors' part of a launch; taken anew where one has moved."""
+        if list(map(torch.Tensor.data_ptr, self._movable)) != self._places:
             self._check()
         return self._table
+
+    def grads(self, grads):
+        """(the gradients' part of a launch, the code of their dtype)."""
+        grads = list(grads)
+        if len(grads) != len(self.params):
+            raise ValueError(f"{len(grads)} grads for {len(self.params)} params")
+        try:
+            dtypes = {g.dtype for g in grads}
+            ok = (len(dtypes) == 1 and list(map(torch.Tensor.numel, grads)) == self.numels
+                  and all(map(torch.Tensor.is_contiguous, grads)) and all(map(_on_gpu, grads))
+                  and set(map(torch.Tensor.get_device, grads)) == {self.device})
+        except (AttributeError, TypeError):
+            ok = False
+        dtype = grads[0].dtype if isinstance(grads[0], torch.Tensor) else None
+        code = _FLOAT_CODES.get(dtype)
+        if code is None:
+            raise ValueError(f"grads must be torch.float32 or torch.bfloat16, got {dtype}")
+        if not ok:   # word the error
+            for i, (g, n) in enumerate(zip(grads, self.numels)):
+                _need(g, f"grads[{i}]", dtype, n, self.device)
+                if g.numel() != n:
+                    raise ValueError(f"grads[{i}] holds {g.numel()} elements, its parameter {n}")
+        places = list(map(torch.Tensor.data_ptr, grads))
+        if not self._written.isdisjoint(places):
+            raise ValueError("a gradient shares memory with a parameter or its state")
+        return self._grads.pack(*places), code
 
 
 def adamw_plan(params, states, weights=None, weight_decay=0.0):
@@ -1308,28 +1357,10 @@ def adamw_step(plan: AdamWPlan, grads, step, lr, betas=(0.9, 0.999), eps=1e-8, g
     parameter, all fp32 or all bf16; step: 1 at the first step.  step (int64), lr (fp32)
     and grad_scale (fp32; a factor of the gradients, NaN or infinity to leave everything
     as it is) may be 1-element CUDA tensors, which a captured launch reads anew."""
-    grads = list(grads)
-    if len(grads) != len(plan.params):
-        raise ValueError(f"{len(grads)} grads for {len(plan.params)} params")
-    if not grads:
+    if not plan.params:
         return
     table, dev = plan.table(), plan.device
-    dtype = grads[0].dtype if isinstance(grads[0], torch.Tensor) else None
-    code = _FLOAT_CODES.get(dtype)
-    if code is None:
-        raise ValueError(f"grads must be torch.float32 or torch.bfloat16, got {dtype}")
-    places = []
-    for i, (g, n) in enumerate(zip(grads, plan.numels)):
-        try:
-            if not (g.dtype is dtype and g.numel() == n and g.is_contiguous()
-                    and g.get_device() == dev):
-                raise AttributeError
-        except AttributeError:
-            _need(g, f"grads[{i}]", dtype, n, dev)
-            raise ValueError(f"grads[{i}] holds {g.numel()} elements, its parameter {n}") from None
-        places.append(g.data_ptr())
-    if not plan._written.isdisjoint(p for p in places if p):
-        raise ValueError("a gradient shares memory with a parameter or its state")
+    places, code = plan.grads(grads)
     t, t_at = _scalar(step, "step", torch.int64, dev)
     rate, rate_at = _scalar(lr, "lr", torch.float32, dev)
     scale_at = 0
@@ -1337,5 +1368,4 @@ def adamw_step(plan: AdamWPlan, grads, step, lr, betas=(0.9, 0.999), eps=1e-8, g
         _need(grad_scale, "grad_scale", torch.float32, 1, dev)
         scale_at = grad_scale.data_ptr()
     a = _ADAMW_ARGS.pack(rate, betas[0], betas[1], eps, t, rate_at, t_at, scale_at, code, plan.bits)
-    _ok(mxq_adamw(table, struct.pack(f"@{len(places)}P", *places), len(places), a, _stream(dev)),
-        "mxq_adamw")
+    _ok(mxq_adamw(table, places, len(plan.params), a, _stream(dev)), "mxq_adamw")

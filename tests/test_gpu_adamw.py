@@ -183,11 +183,11 @@ def test_grad_scale(bits):
     states = [mxq.adamw_state(params[0], bits)]
     grads = _grads([700], 9)
     plan = _step_and_check(params, grads, states, 1, scale=0.125)
-    before = [params[0].clone()] + [t.clone() for t in plan._tensors]
+    before = [params[0].clone()] + [t.clone() for t in plan._memory]
     for bad in (float("nan"), float("inf"), -float("inf")):
         mxq.adamw_step(plan, grads, 2, 1e-3, grad_scale=torch.tensor([bad], device="cuda"))
     mxq.check()
-    for a, b in zip(before, [params[0]] + plan._tensors):
+    for a, b in zip(before, [params[0]] + plan._memory):
         assert torch.equal(a, b)
 
 
