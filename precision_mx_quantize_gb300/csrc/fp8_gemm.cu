@@ -125,33 +125,6 @@ MXQ_DEV void mma_f8(uint32_t d_tmem, uint64_t a, uint64_t b, uint32_t idesc, uin
       : "memory");
 }
 
-MXQ_DEV void tc_commit(uint32_t bar) {
-  asm volatile(
-      "tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar)
-      : "memory");
-}
-
-MXQ_DEV void tmem_alloc(uint32_t dst_smem, uint32_t cols) {
-  asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(dst_smem),
-               "r"(cols)
-               : "memory");
-  asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
-}
-
-MXQ_DEV void tmem_dealloc(uint32_t taddr, uint32_t cols) {
-  asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(taddr), "r"(cols)
-               : "memory");
-}
-
-#define MXQ_TMEM_LD16(taddr, r)                                                                  \
-  asm volatile(                                                                                  \
-      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, "    \
-      "%11, %12, %13, %14, %15}, [%16];"                                                         \
-      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),     \
-        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), \
-        "=r"(r[14]), "=r"(r[15])                                                                 \
-      : "r"(taddr))
-
 // The wait of a role that runs on to its end whatever happens: when the limit
 // runs out it records the error, and every later wait of the CTA passes at
 // once.  Its warps then need no vote on a result before each warp-wide
@@ -181,16 +154,6 @@ MXQ_DEV void arrive_remote_if(bool p, uint32_t cluster_bar) {
       "r"(static_cast<uint32_t>(p))
       : "memory");
 }
-
-// Waits for this thread's tensor-memory loads; the registers pass through, so
-// that no use of them can move above the wait.
-#define MXQ_TMEM_WAIT16(r)                                                                       \
-  asm volatile("tcgen05.wait::ld.sync.aligned;"                                                  \
-               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]),         \
-                 "+r"(r[6]), "+r"(r[7]), "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]),       \
-                 "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15])                              \
-               :                                                                                 \
-               : "memory")
 
 // ---- 128 lines of B x T lines of A per CTA --------------------------------------
 constexpr int L_THREADS = 192;

@@ -12,11 +12,12 @@
 // walks the tiles of all experts as one persistent grid.
 //
 // rows: rows of a tile past the expert's end are the next expert's; they are computed
-// and not stored.  wgrad: offsets are multiples of an MMA's K (32 elements, E2M1 64),
+// and not stored.  Experts with few rows have tiles of their own (gemm_few.cuh).  wgrad: offsets are multiples of an MMA's K (32 elements, E2M1 64),
 // so the last stage of an expert issues one to four MMAs and none reads the next
 // expert's codes; an expert without rows gets zeros.
 #include <string.h>
 
+#include "gemm_few.cuh"
 #include "gemm_kernel.cuh"
 
 namespace mxq {
@@ -36,15 +37,24 @@ struct ExpertParams {
   int32_t stores;        // 32-byte stores per row of a tile
 };
 
-#ifndef STAGED_ROWS
-#define STAGED_ROWS false
-#endif
-template <bool WGRAD>
+// How a launch's tiles lie: 256 rows of an expert by 256 of its columns, stored straight
+// from the accumulators or through shared memory; a weight gradient's 256x256; or T
+// rows by 128 columns (gemm_few.cuh).
+enum Form { ROWS, ROWS_STAGED, WGRAD, FEW16, FEW64 };
+
+constexpr bool is_few(Form f) { return f == FEW16 || f == FEW64; }
+constexpr int tile_rows(Form f) { return f == FEW16 ? 16 : f == FEW64 ? 64 : G_CLUSTER * G_BM; }
+constexpr int tile_cols(Form f) { return is_few(f) ? W_LINES : G_BN; }
+constexpr int chunk_rows(Form f) { return is_few(f) ? tile_rows(f) : G_BM; }   // of a scale chunk
+
+template <Form FORM>
 struct ExpertWork {
   using Params = ExpertParams;
-  static constexpr int STAGES = STAGED_ROWS || WGRAD ? 5 : 6, TABLE = (X_TABLE * 4 + 15) / 16 * 16;
-  static constexpr bool PARTIAL = WGRAD, QUANTIZES = false;
-  static constexpr bool STAGED = STAGED_ROWS || WGRAD;
+  [[maybe_unused]] static constexpr bool PARTIAL = FORM == WGRAD, QUANTIZES = false;
+  [[maybe_unused]] static constexpr bool STAGED = FORM == WGRAD || FORM == ROWS_STAGED;
+  [[maybe_unused]] static constexpr int STAGES = STAGED ? 5 : 6;   // a stage less makes room to go through
+  static constexpr int TABLE = (X_TABLE * 4 + 15) / 16 * 16;
+  static constexpr int TR = tile_rows(FORM), TC = tile_cols(FORM);
   const ExpertParams& g;
   const int32_t *off, *tile0, *sf0;
   int e = 0;   // expert of the last item asked for
@@ -62,7 +72,7 @@ struct ExpertWork {
     prefetch_tmap(&g.tsb);
   }
   MXQ_DEV static void load(const ExpertParams& g, void* table) {
-    for (int i = threadIdx.x; i < 3 * (g.experts + 1); i += G_THREADS)
+    for (int i = threadIdx.x; i < 3 * (g.experts + 1); i += blockDim.x)
       static_cast<int32_t*>(table)[i] = g.table[i];
   }
   MXQ_DEV int tiles() const { return tile0[g.experts]; }
@@ -75,14 +85,14 @@ struct ExpertWork {
     it.tb = &g.tb;
     it.tsa = &g.tsa;
     it.tsb = &g.tsb;
-    if constexpr (WGRAD) {
+    if constexpr (FORM == WGRAD) {
       const int bytes = g.a.fp4 ? len >> 1 : len;
       it.nk = (bytes + G_BKB - 1) / G_BKB;
       it.last = ((bytes - 1) % G_BKB) / 32 + 1;
       tile_coords(t - tile0[e], g.a, it.mp, it.nt);
       it.kx = g.a.fp4 ? lo >> 1 : lo;
-      it.ay = it.mp * (G_CLUSTER * G_BM);
-      it.by = it.nt * G_BN;
+      it.ay = it.mp * TR;
+      it.by = it.nt * TC;
       it.sa = G_CLUSTER * it.mp * g.a.kc_per_row + sf0[e];
       it.sb = 2 * it.nt * g.a.kc_per_row + sf0[e];
       it.c0 = int64_t(e) * g.a.M;
@@ -91,13 +101,14 @@ struct ExpertWork {
     } else {
       it.nk = g.a.nk;
       it.last = 4;
-      const Grid grid{(len + G_CLUSTER * G_BM - 1) / (G_CLUSTER * G_BM), g.a.n_nt, g.a.group, 0};
+      const int n_mp = (len + TR - 1) / TR;
+      const Grid grid{n_mp, g.a.n_nt, is_few(FORM) ? n_mp : g.a.group, 0};
       tile_coords(t - tile0[e], grid, it.mp, it.nt);
       it.kx = 0;
-      it.ay = lo + it.mp * (G_CLUSTER * G_BM);
-      it.by = e * g.a.N + it.nt * G_BN;
-      it.sa = (sf0[e] + G_CLUSTER * it.mp) * g.a.kc_per_row;
-      it.sb = (e * g.b_tiles + 2 * it.nt) * g.a.kc_per_row;
+      it.ay = lo + it.mp * TR;
+      it.by = e * g.a.N + it.nt * TC;
+      it.sa = (sf0[e] + it.mp * (TR / chunk_rows(FORM))) * g.a.kc_per_row;
+      it.sb = (e * g.b_tiles + it.nt * (TC / G_BM)) * g.a.kc_per_row;
       it.c0 = lo;
       it.rows = len;
       it.pace_ns = g.a.pace_ns;
@@ -105,8 +116,7 @@ struct ExpertWork {
     return it;
   }
   [[maybe_unused]] MXQ_DEV static bool inside(const Item& it) {
-    return it.mp >= 0 && it.mp * (G_CLUSTER * G_BM) < it.rows && it.nt >= 0 &&
-           it.nt < it.a->n_nt;
+    return it.mp >= 0 && it.mp * TR < it.rows && it.nt >= 0 && it.nt < it.a->n_nt;
   }
 
  private:
@@ -122,6 +132,7 @@ struct PrepareArgs {
   int32_t rows, experts;
   int32_t unit;            // offsets are multiples of it
   int32_t n_nt;            // rows: tiles along N
+  int32_t tile_rows, chunk_rows;   // rows: of a tile, of a scale chunk of A
   int32_t tiles;           // wgrad: tiles of an expert
   int32_t stage_rows;      // wgrad: elements of K per stage
   int32_t stage_chunks;    // wgrad: chunks per stage
@@ -168,7 +179,7 @@ MXQ_DEV void write_chunk(uint8_t* chunk, const uint8_t* s, int64_t line, int64_t
   *reinterpret_cast<uint4*>(chunk + lane * 16) = make_uint4(w[0], w[1], w[2], w[3]);
 }
 
-template <bool WGRAD>
+template <bool ALONG_K>
 __global__ void __launch_bounds__(256) experts_prepare(const PrepareArgs p) {
   __shared__ int32_t table[X_TABLE];
   int32_t *off = table, *tile0 = off + p.experts + 1, *sf0 = tile0 + p.experts + 1;
@@ -205,12 +216,12 @@ __global__ void __launch_bounds__(256) experts_prepare(const PrepareArgs p) {
       if (lane == 0) before = end;
       const int len = v - before;
       int nt, ns;
-      if (WGRAD) {
+      if (ALONG_K) {
         nt = live ? p.tiles : 0;
         ns = (len + p.stage_rows - 1) / p.stage_rows * p.stage_chunks;
       } else {
-        nt = (len + G_CLUSTER * G_BM - 1) / (G_CLUSTER * G_BM) * p.n_nt;
-        ns = (len + G_BM - 1) / G_BM;
+        nt = (len + p.tile_rows - 1) / p.tile_rows * p.n_nt;
+        ns = (len + p.chunk_rows - 1) / p.chunk_rows;
       }
 #pragma unroll
       for (int d = 1; d < 32; d <<= 1) {
@@ -238,7 +249,7 @@ __global__ void __launch_bounds__(256) experts_prepare(const PrepareArgs p) {
   const int64_t warp = (int64_t(blockIdx.x) * blockDim.x + threadIdx.x) >> 5;
   const int64_t warps = (int64_t(gridDim.x) * blockDim.x) >> 5;
   const int sf = sf0[p.experts];
-  if (WGRAD) {
+  if (ALONG_K) {
     const int64_t tiles_a = (p.lines_a + 127) / 128, tiles_b = (p.lines_b + 127) / 128;
     for (int64_t u = warp; u < (tiles_a + tiles_b) * sf; u += warps) {
       const int64_t tile = u / sf;
@@ -263,8 +274,8 @@ __global__ void __launch_bounds__(256) experts_prepare(const PrepareArgs p) {
       int64_t line, lines;
       if (is_a) {
         const int e = holder(sf0, p.experts, static_cast<int>(tile));
-        line = off[e] + (tile - sf0[e]) * 128;
-        lines = off[e + 1];
+        line = off[e] + (tile - sf0[e]) * p.chunk_rows;
+        lines = min(int64_t(off[e + 1]), line + p.chunk_rows);
       } else {
         const int64_t e = tile / tiles_b;
         line = e * p.lines_b + (tile % tiles_b) * 128;
@@ -282,6 +293,7 @@ __global__ void __launch_bounds__(256) experts_prepare(const PrepareArgs p) {
 // ---- sizes ----------------------------------------------------------------------
 
 struct ExpertPlan {
+  Form form;
   int64_t kbytes;              // bytes of a line of codes
   int64_t stage_rows;          // elements of a K stage
   int64_t stage_chunks;
@@ -293,6 +305,22 @@ struct ExpertPlan {
 
 constexpr int64_t X_LIM = int64_t(1) << 31;
 
+// The form of a rows product from its sizes; the device alone knows the experts' rows, so
+// it goes by their average over the experts that can have any.  Measured, 64 experts of
+// 4096x4096 E2M1 (2048x2048 E4M3), us at an average of 1 (of 8 experts), 8, 16, 32, 64:
+//   FEW16  20.5 (14.0)  92.7 (50.8)  115 (61.6)   186 (97.9)
+//   FEW64  25.1 (15.3)  91.2 (52.3)  96.2 (53.2)  102 (57.6)  128 (71.4)
+//   ROWS   27.2 (16.4)  97.3 (56.4)  102 (56.9)   105 (58.3)  108 (60.3)
+// Through shared memory, the stores of a tile take less of the SM's memory path, and a
+// stage of the ring less: 9 stages to a tile, 1237 rows of 7 experts, 13.0 against 15.2
+// us; 16 stages, 62 against 58 us at an average of 32.
+Form rows_form(const mxq_experts_args& q, int64_t kbytes) {
+  const int64_t average = q.rows / std::max<int64_t>(1, std::min<int64_t>(q.experts, q.rows));
+  if (average <= 8) return FEW16;
+  if (average <= 32) return FEW64;
+  return kbytes <= 12 * G_BKB ? ROWS_STAGED : ROWS;
+}
+
 bool expert_plan(const mxq_experts_args& q, bool wgrad, ExpertPlan& p) {
   if (q.rows < 0 || q.N < 1 || q.experts < 1 || q.experts > X_MAX || q.rows >= X_LIM ||
       q.N >= X_LIM)
@@ -301,10 +329,11 @@ bool expert_plan(const mxq_experts_args& q, bool wgrad, ExpertPlan& p) {
   const bool fp4 = q.fmt == MXQ_E2M1;
   p.stage_rows = fp4 ? 256 : 128;
   p.stage_chunks = fp4 ? 2 : 1;
-  p.n_nt = (q.N + G_BN - 1) / G_BN;
   p.table = (3 * (int64_t(q.experts) + 1) * 4 + 255) / 256 * 256;
   if (wgrad) {
     if (q.M < 1 || q.M >= X_LIM || q.rows % 32 != 0) return false;
+    p.form = WGRAD;
+    p.n_nt = (q.N + G_BN - 1) / G_BN;
     const int64_t unit = fp4 ? 64 : 32;
     const int64_t stages =
         q.rows / p.stage_rows + std::min<int64_t>(q.experts, q.rows / unit) + 1;
@@ -319,11 +348,13 @@ bool expert_plan(const mxq_experts_args& q, bool wgrad, ExpertPlan& p) {
     if (q.K < 32 || q.K >= X_LIM || q.K % 32 != 0 || q.experts * q.N >= X_LIM) return false;
     if (q.b_scale_layout != MXQ_SCALES_ROWMAJOR && q.b_scale_layout != MXQ_SCALES_TC) return false;
     p.kbytes = fp4 ? q.K / 2 : q.K;
+    p.form = rows_form(q, p.kbytes);
+    p.n_nt = (q.N + tile_cols(p.form) - 1) / tile_cols(p.form);
     p.kcs = (q.K + p.stage_rows - 1) / p.stage_rows * p.stage_chunks;
-    p.tiles_a = q.rows / 128 + std::min<int64_t>(q.experts, q.rows);
+    p.tiles_a = q.rows / chunk_rows(p.form) + std::min<int64_t>(q.experts, q.rows);
     p.tiles_b = q.experts * ((q.N + 127) / 128);
     p.n_mp = 0;
-    p.items = (q.rows / (G_CLUSTER * G_BM) + std::min<int64_t>(q.experts, q.rows)) * p.n_nt;
+    p.items = (q.rows / tile_rows(p.form) + std::min<int64_t>(q.experts, q.rows)) * p.n_nt;
     p.ws_b = q.b_scale_layout == MXQ_SCALES_TC ? 0 : p.tiles_b * p.kcs * 512;
   }
   p.ws_a = p.tiles_a * p.kcs * 512;
@@ -331,18 +362,18 @@ bool expert_plan(const mxq_experts_args& q, bool wgrad, ExpertPlan& p) {
   return p.items < X_LIM && (p.tiles_a + 2) * p.kcs < X_LIM && (p.tiles_b + 2) * p.kcs < X_LIM;
 }
 
-template <bool WGRAD>
+template <bool ALONG_K>
 mxq_status experts_launch(const mxq_experts_args& q, void* stream) {
   ExpertPlan p;
   if (q.out_dtype != MXQ_OUT_F32 && q.out_dtype != MXQ_OUT_BF16) return MXQ_ERR_ARG;
-  if (!expert_plan(q, WGRAD, p)) return MXQ_ERR_ARG;
+  if (!expert_plan(q, ALONG_K, p)) return MXQ_ERR_ARG;
   const bool fp4 = q.fmt == MXQ_E2M1, bf16 = q.out_dtype == MXQ_OUT_BF16;
-  const bool tc = !WGRAD && q.b_scale_layout == MXQ_SCALES_TC;
+  const bool tc = !ALONG_K && q.b_scale_layout == MXQ_SCALES_TC;
   if (tc && q.K % p.stage_rows != 0) return MXQ_ERR_ARG;
   if (q.N % (bf16 ? 8 : 4) != 0) return MXQ_ERR_ALIGN;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   if (q.rows == 0) {
-    if (!WGRAD) return MXQ_OK;
+    if (!ALONG_K) return MXQ_OK;
     if (!q.C) return MXQ_ERR_ARG;
     const size_t bytes = size_t(q.experts) * q.M * q.N * (bf16 ? 2 : 4);
     return cudaMemsetAsync(q.C, 0, bytes, st) == cudaSuccess ? MXQ_OK : MXQ_ERR_CUDA;
@@ -358,8 +389,10 @@ mxq_status experts_launch(const mxq_experts_args& q, void* stream) {
   r.offsets = q.offsets;
   r.rows = static_cast<int32_t>(q.rows);
   r.experts = q.experts;
-  r.unit = WGRAD ? (fp4 ? 64 : 32) : 1;
+  r.unit = ALONG_K ? (fp4 ? 64 : 32) : 1;
   r.n_nt = static_cast<int32_t>(p.n_nt);
+  r.tile_rows = tile_rows(p.form);
+  r.chunk_rows = chunk_rows(p.form);
   r.tiles = static_cast<int32_t>(p.n_mp * p.n_nt);
   r.stage_rows = static_cast<int32_t>(p.stage_rows);
   r.stage_chunks = static_cast<int32_t>(p.stage_chunks);
@@ -368,19 +401,19 @@ mxq_status experts_launch(const mxq_experts_args& q, void* stream) {
   r.sb = tc ? nullptr : q.sB;
   r.ca = ws + p.table;
   r.cb = r.ca + p.ws_a;
-  r.lines_a = WGRAD ? static_cast<int32_t>(q.M) : 0;
+  r.lines_a = ALONG_K ? static_cast<int32_t>(q.M) : 0;
   r.lines_b = static_cast<int32_t>(q.N);
-  r.kb = static_cast<int32_t>((WGRAD ? q.rows : q.K) / 32);
+  r.kb = static_cast<int32_t>((ALONG_K ? q.rows : q.K) / 32);
   r.kcs = static_cast<int32_t>(p.kcs);
 
   ExpertParams g;
   memset(&g, 0, sizeof(g));
   const uint64_t kbytes = static_cast<uint64_t>(p.kbytes);
-  const uint64_t lines_a = static_cast<uint64_t>(WGRAD ? q.M : q.rows);
-  const uint64_t lines_b = static_cast<uint64_t>(WGRAD ? q.N : q.experts * q.N);
-  const auto codes = [&](CUtensorMap* m, const void* base, uint64_t lines) {
+  const uint64_t lines_a = static_cast<uint64_t>(ALONG_K ? q.M : q.rows);
+  const uint64_t lines_b = static_cast<uint64_t>(ALONG_K ? q.N : q.experts * q.N);
+  const auto codes = [&](CUtensorMap* m, const void* base, uint64_t lines, int box) {
     return tensor_map_2d(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, base, kbytes, lines, kbytes, G_BKB,
-                         G_BM, CU_TENSOR_MAP_SWIZZLE_128B,
+                         static_cast<uint32_t>(box), CU_TENSOR_MAP_SWIZZLE_128B,
                          CU_TENSOR_MAP_L2_PROMOTION_L2_256B) == CUDA_SUCCESS;
   };
   const auto chunks = [&](CUtensorMap* m, const void* base, int64_t tiles) {
@@ -389,18 +422,18 @@ mxq_status experts_launch(const mxq_experts_args& q, void* stream) {
                          static_cast<uint32_t>(p.stage_chunks), CU_TENSOR_MAP_SWIZZLE_NONE,
                          CU_TENSOR_MAP_L2_PROMOTION_L2_256B) == CUDA_SUCCESS;
   };
-  if (!codes(&g.ta, q.A, lines_a) || !codes(&g.tb, q.B, lines_b) ||
+  if (!codes(&g.ta, q.A, lines_a, chunk_rows(p.form)) || !codes(&g.tb, q.B, lines_b, G_BM) ||
       !chunks(&g.tsa, r.ca, p.tiles_a) ||
       !chunks(&g.tsb, tc ? static_cast<const void*>(q.sB) : r.cb, p.tiles_b))
     return MXQ_ERR_CUDA;
   GArgs& a = g.a;
-  a.M = static_cast<int32_t>(WGRAD ? q.M : 0);
+  a.M = static_cast<int32_t>(ALONG_K ? q.M : 0);
   a.N = static_cast<int32_t>(q.N);
   a.n_mp = static_cast<int32_t>(p.n_mp);
   a.n_nt = static_cast<int32_t>(p.n_nt);
   a.nk = static_cast<int32_t>((p.kbytes + G_BKB - 1) / G_BKB);
   a.kc_per_row = static_cast<int32_t>(p.kcs);
-  if (WGRAD) {   // an expert of average length
+  if (ALONG_K) {   // an expert of average length
     const double k = std::max(1.0, double(p.kbytes) / q.experts);
     choose_raster(a.n_mp, a.n_nt, q.M * k, q.N * k, 2 * G_BM * k, a.group, a.group_n);
   } else {
@@ -422,8 +455,17 @@ mxq_status experts_launch(const mxq_experts_args& q, void* stream) {
 
   const int64_t units = (p.tiles_a + (tc ? 0 : p.tiles_b)) * p.kcs;
   const unsigned grid = static_cast<unsigned>(std::min<int64_t>((units + 7) / 8, 4 * sm_count()));
-  if (!launch_early(experts_prepare<WGRAD>, grid, 256, 0, st, r)) return MXQ_ERR_CUDA;
-  return gemm_kernel_run<ExpertWork<WGRAD>>(g, p.items, stream);
+  if (!launch_early(experts_prepare<ALONG_K>, grid, 256, 0, st, r)) return MXQ_ERR_CUDA;
+  if constexpr (ALONG_K) {
+    return gemm_kernel_run<ExpertWork<WGRAD>>(g, p.items, stream);
+  } else {
+    switch (p.form) {
+      case FEW16: return gemm_few_run<ExpertWork<FEW16>, 16>(g, p.items, stream);
+      case FEW64: return gemm_few_run<ExpertWork<FEW64>, 64>(g, p.items, stream);
+      case ROWS_STAGED: return gemm_kernel_run<ExpertWork<ROWS_STAGED>>(g, p.items, stream);
+      default: return gemm_kernel_run<ExpertWork<ROWS>>(g, p.items, stream);
+    }
+  }
 }
 
 }  // namespace

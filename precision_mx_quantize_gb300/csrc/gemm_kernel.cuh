@@ -116,16 +116,17 @@ MXQ_DEV void mma_mxf4_pair(uint32_t d_tmem, uint64_t a, uint64_t b, uint32_t ide
       : "memory");
 }
 
-// Instruction descriptor of a block-scaled pair MMA: K-major A and B,
-// M = 256 (128 per CTA), N = 256, E8M0 scales, scale-factor byte ids.
-MXQ_DEV uint32_t idesc_block_scaled(uint32_t fmt_code, uint32_t a_sf, uint32_t b_sf) {
+// Instruction descriptor of a block-scaled m x n MMA: K-major A and B, E8M0 scales,
+// scale-factor byte ids.
+MXQ_DEV uint32_t idesc_block_scaled(uint32_t fmt_code, uint32_t m, uint32_t n, uint32_t a_sf,
+                                    uint32_t b_sf) {
   uint32_t d = 0;
   d |= (b_sf & 3u) << 4;
   d |= (fmt_code & 7u) << 7;    // A format
   d |= (fmt_code & 7u) << 10;   // B format
-  d |= static_cast<uint32_t>(G_BN >> 3) << 17;
+  d |= (n >> 3) << 17;
   d |= 1u << 23;                // scale type: UE8M0
-  d |= static_cast<uint32_t>((G_CLUSTER * G_BM) >> 4) << 24;
+  d |= (m >> 4) << 24;
   d |= (a_sf & 3u) << 29;
   return d;
 }
@@ -433,7 +434,7 @@ __global__ void __launch_bounds__(G_THREADS, 1)
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         const uint32_t sf_id = a0.fp4 ? ((2 * j) & 3) : j;
-        idesc[j] = idesc_block_scaled(fmt_code, sf_id, sf_id);
+        idesc[j] = idesc_block_scaled(fmt_code, G_CLUSTER * G_BM, G_BN, sf_id, sf_id);
       }
       const uint32_t st0 = smem_u32(smem);
       const uint64_t adesc_s0 = smem_desc(st0, 0, 1024, 2);
