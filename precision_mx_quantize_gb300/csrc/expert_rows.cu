@@ -505,26 +505,27 @@ mxq_status rows_run(RowsOp op, const mxq_expert_rows_args* q, void* stream) {
   if (q->dtype != MXQ_OUT_F32 && q->dtype != MXQ_OUT_BF16) return MXQ_ERR_ARG;
   const bool pads = op != COMBINE;
   if (pads && (q->experts < 1 || q->experts > O_MAX_EXPERTS)) return MXQ_ERR_ARG;
-  if (q->cols == 0 && op != BACKWARD) return MXQ_OK;
-  if (q->tokens == 0 && (!pads || q->rows == 0)) return MXQ_OK;
-  // an empty buffer of rows has no address
-  if (!q->row_of || (op != COMBINE && !q->x) || (op != GATHER && q->rows && !q->y) ||
-      ((op == COMBINE || q->rows) && !q->out) || (pads && (!q->offsets || !q->counts)) ||
-      (op == BACKWARD && !q->dweights))
+  if (q->tokens == 0 || (q->cols == 0 && op != BACKWARD)) return MXQ_OK;
+  // an empty buffer has no address
+  const bool x = op != COMBINE && q->cols, y = op != GATHER && q->rows && q->cols;
+  const bool out = op == COMBINE || (q->rows && q->cols);
+  if (!q->row_of || (x && !q->x) || (y && !q->y) || (out && !q->out) ||
+      (pads && (!q->offsets || !q->counts)) || (op == BACKWARD && !q->dweights))
     return MXQ_ERR_ARG;
-  if (q->rows == 0 && op != GATHER) {   // no choice has a row
-    const size_t bytes = op == COMBINE ? size_t(q->tokens) * q->cols *
-                                             (q->dtype == MXQ_OUT_BF16 ? 2 : 4)
-                                       : size_t(q->tokens) * q->topk * 4;
-    return cudaMemsetAsync(op == COMBINE ? q->out : q->dweights, 0, bytes,
-                           static_cast<cudaStream_t>(stream)) == cudaSuccess ? MXQ_OK : MXQ_ERR_CUDA;
-  }
   const void* words[] = {q->row_of, q->offsets, q->counts, q->weights, q->dweights};
   for (const void* p : words)
     if (!aligned4(p)) return MXQ_ERR_ALIGN;
   const void* data[] = {q->x, q->y, q->out};
   for (const void* p : data)
     if (!aligned16(p)) return MXQ_ERR_ALIGN;
+  if (op != GATHER && (q->rows == 0 || q->cols == 0)) {   // no choice has a row: sums of nothing
+    const size_t size = q->dtype == MXQ_OUT_BF16 ? 2 : 4;
+    const size_t bytes = op == COMBINE ? size_t(q->tokens) * q->cols * size
+                                       : size_t(q->tokens) * q->topk * 4;
+    void* const sums = op == COMBINE ? q->out : q->dweights;
+    return cudaMemsetAsync(sums, 0, bytes, static_cast<cudaStream_t>(stream)) == cudaSuccess
+               ? MXQ_OK : MXQ_ERR_CUDA;
+  }
   RowsArgs a = {};
   a.x = q->x;
   a.y = q->y;

@@ -155,6 +155,23 @@ def test_gradients_against_differences():
         assert abs(d - (dw.double() * v.double()).sum().item()) < 1e-4
 
 
+def test_empty_buffers():
+    ids = torch.full((3, 2), -1, device="cuda")
+    row_of, offsets, counts = mxq.expert_order(ids, 4)
+    x, none = torch.ones(3, 8, device="cuda"), torch.empty(0, 8, device="cuda")
+    assert mxq.expert_gather(x, row_of, offsets, counts, 0).shape == (0, 8)
+    assert mxq.expert_combine(none, row_of).eq(0).all()
+    dy, dw = mxq.expert_combine_backward(x, none, row_of, offsets, counts)
+    assert dy.shape == (0, 8) and dw.eq(0).all()
+    for rows, cols, tokens in ((4, 0, 3), (4, 8, 0)):
+        x, y = torch.ones(tokens, cols, device="cuda"), torch.ones(rows, cols, device="cuda")
+        choice = torch.zeros(tokens, 2, dtype=torch.int32, device="cuda")
+        assert mxq.expert_gather(x, choice, offsets, counts, rows).shape == (rows, cols)
+        assert mxq.expert_combine(y, choice).shape == (tokens, cols)
+        assert mxq.expert_combine_backward(x, y, choice, offsets, counts)[1].eq(0).all()
+    mxq.check()
+
+
 def test_rows_outside_the_buffer_are_left_out_and_reported():
     row_of = torch.tensor([[0, 5], [9, -3]], dtype=torch.int32, device="cuda")
     x = torch.ones(2, 16, device="cuda")
