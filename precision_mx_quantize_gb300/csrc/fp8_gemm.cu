@@ -705,13 +705,6 @@ MXQ_DEV bool sync_any(int id, int threads, bool v) {
   return any != 0;
 }
 
-MXQ_DEV void tma_store_2d(const CUtensorMap* map, uint32_t src, int32_t x, int32_t y) {
-  asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.tile.bulk_group [%0, {%2, %3}], [%1];" ::"l"(
-                   reinterpret_cast<uint64_t>(map)),
-               "r"(src), "r"(x), "r"(y)
-               : "memory");
-}
-
 // How the sums of a tile leave: by TMA where the rows of C are 16-byte multiples,
 // else copied; or shared, by p.split pairs of a cluster that take a part of the
 // K blocks each and join their sums in order through distributed shared memory.

@@ -37,7 +37,8 @@ struct GGroup {
 struct DenseWork {
   using Params = GGroup;
   static constexpr int STAGES = G_STAGES, TABLE = 0;
-  static constexpr bool PARTIAL = false, QUANTIZES = true, STAGED = false;
+  static constexpr bool PARTIAL = false, QUANTIZES = true;
+  static constexpr StoreBy OUT = STORE_DIRECT;
   const GGroup& g;
   int p = 0;   // problem of the last item asked for
 
@@ -72,6 +73,7 @@ struct DenseWork {
     it.sb = 2 * it.nt * a.kc_per_row;
     it.c0 = 0;
     it.rows = a.M;
+    it.z = 0;
     it.pace_ns = a.pace_ns;
     return it;
   }

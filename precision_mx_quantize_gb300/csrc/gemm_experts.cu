@@ -30,6 +30,7 @@ constexpr int X_TABLE = 3 * (X_MAX + 1);    // words of the table
 // the form rows, 128-row tiles of A's scale chunks; in wgrad, chunks along K.
 struct ExpertParams {
   CUtensorMap ta, tb, tsa, tsb;
+  CUtensorMap tc;        // wgrad: C
   GArgs a;
   const int32_t* table;
   int32_t experts;
@@ -51,8 +52,10 @@ template <Form FORM>
 struct ExpertWork {
   using Params = ExpertParams;
   [[maybe_unused]] static constexpr bool PARTIAL = FORM == WGRAD, QUANTIZES = false;
-  [[maybe_unused]] static constexpr bool STAGED = FORM == WGRAD || FORM == ROWS_STAGED;
-  [[maybe_unused]] static constexpr int STAGES = STAGED ? 5 : 6;   // a stage less makes room to go through
+  [[maybe_unused]] static constexpr StoreBy OUT =
+      FORM == WGRAD ? STORE_TMA : FORM == ROWS_STAGED ? STORE_STAGED : STORE_DIRECT;
+  // a stage less makes room for staged tiles
+  [[maybe_unused]] static constexpr int STAGES = OUT == STORE_DIRECT ? 6 : 5;
   static constexpr int TABLE = (X_TABLE * 4 + 15) / 16 * 16;
   static constexpr int TR = tile_rows(FORM), TC = tile_cols(FORM);
   const ExpertParams& g;
@@ -70,11 +73,13 @@ struct ExpertWork {
     prefetch_tmap(&g.tb);
     prefetch_tmap(&g.tsa);
     prefetch_tmap(&g.tsb);
+    if (FORM == WGRAD) prefetch_tmap(&g.tc);
   }
   MXQ_DEV static void load(const ExpertParams& g, void* table) {
     for (int i = threadIdx.x; i < 3 * (g.experts + 1); i += blockDim.x)
       static_cast<int32_t*>(table)[i] = g.table[i];
   }
+  MXQ_DEV static const CUtensorMap* store_map(const ExpertParams& g) { return &g.tc; }
   MXQ_DEV int tiles() const { return tile0[g.experts]; }
   MXQ_DEV Item at(int t) {
     while (e + 1 < g.experts && t >= tile0[e + 1]) ++e;
@@ -85,6 +90,7 @@ struct ExpertWork {
     it.tb = &g.tb;
     it.tsa = &g.tsa;
     it.tsb = &g.tsb;
+    it.z = e;
     if constexpr (FORM == WGRAD) {
       const int bytes = g.a.fp4 ? len >> 1 : len;
       it.nk = (bytes + G_BKB - 1) / G_BKB;
@@ -426,6 +432,15 @@ mxq_status experts_launch(const mxq_experts_args& q, void* stream) {
       !chunks(&g.tsa, r.ca, p.tiles_a) ||
       !chunks(&g.tsb, tc ? static_cast<const void*>(q.sB) : r.cb, p.tiles_b))
     return MXQ_ERR_CUDA;
+  if (ALONG_K) {
+    const uint64_t size = bf16 ? 2 : 4;
+    if (tensor_map_3d(&g.tc, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32,
+                      q.C, static_cast<uint64_t>(q.N), static_cast<uint64_t>(q.M),
+                      static_cast<uint64_t>(q.experts), q.N * size, q.M * q.N * size,
+                      static_cast<uint32_t>(128 / size), 32, 1, CU_TENSOR_MAP_SWIZZLE_128B,
+                      CU_TENSOR_MAP_L2_PROMOTION_NONE) != CUDA_SUCCESS)
+      return MXQ_ERR_CUDA;
+  }
   GArgs& a = g.a;
   a.M = static_cast<int32_t>(ALONG_K ? q.M : 0);
   a.N = static_cast<int32_t>(q.N);

@@ -54,7 +54,13 @@ constexpr int G_STAGE_BYTES = G_A_BYTES + G_B_BYTES + G_SFA_BYTES + G_SFB_BYTES;
 constexpr int G_BAR_BYTES = 512;
 constexpr uint32_t kNotYet = 0xFFFFFFFFu;   // peer's stage count not yet reported
 constexpr int G_PITCH = 144;                 // staged epilogue: 128 bytes of a row and its padding
-constexpr int G_STAGED_BYTES = 8 * 32 * G_PITCH;
+
+// How a tile leaves: straight from the accumulators, through shared memory and copied out
+// by its threads, or through shared memory and by TMA (32 rows of every warp either way).
+enum StoreBy { STORE_DIRECT, STORE_STAGED, STORE_TMA };
+constexpr int out_bytes(StoreBy by) {   // of shared memory, one piece per warp
+  return by == STORE_STAGED ? 8 * 32 * G_PITCH : by == STORE_TMA ? 8 * 32 * 128 : 0;
+}
 constexpr uint32_t G_TMEM_COLS = 512;
 constexpr uint32_t G_SFA_COL0 = 256;                 // 8 columns per stage
 constexpr uint32_t G_SFB_COL0 = 256 + 8 * G_STAGES;  // 16 columns per stage
@@ -277,6 +283,64 @@ MXQ_DEV void store_staged(const uint32_t (&v)[128], const GArgs& a, uint8_t* buf
   }
 }
 
+// The same by TMA: the copy engine reads the lines from shared memory itself, which
+// spares the pass that a thread's loads make, and leaves out what lies past the map's
+// ends.  128-byte swizzle: the 16-byte piece q of row r lies at q ^ (r & 7), so that eight
+// lanes' stores meet different banks.  `z`, `y` and `x`: matrix, row and column of C.
+template <typename Work>
+MXQ_DEV void store_tma(const uint32_t (&v)[128], const typename Work::Params& g, bool bf16,
+                       uint8_t* buf, int z, int y, int x, int ncols) {
+  const int lane = threadIdx.x & 31;
+  const int per = bf16 ? 64 : 32;   // columns of 128 bytes
+  uint8_t* const mine = buf + lane * 128;
+  auto ready = [&] {   // the copy of the lines before has been read
+    if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+    __syncwarp();
+  };
+  auto put = [&](int q, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+    *reinterpret_cast<uint4*>(mine + (q ^ (lane & 7)) * 16) = make_uint4(a, b, c, d);
+  };
+  auto out = [&](int first) {
+    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+    __syncwarp();
+    if (lane == 0) {
+      tma_store_3d(Work::store_map(g), smem_u32(buf), x + first, y, z);
+      asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+    }
+  };
+  if (bf16) {
+#pragma unroll
+    for (int s = 0; s < 2; ++s) {
+      if (s * per >= ncols) break;
+      ready();
+#pragma unroll
+      for (int q = 0; q < 8; ++q) {
+        uint32_t w[4];
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+          const __nv_bfloat162 b =
+              __floats2bfloat162_rn(__uint_as_float(v[64 * s + 8 * q + 2 * u]),
+                                    __uint_as_float(v[64 * s + 8 * q + 2 * u + 1]));
+          w[u] = *reinterpret_cast<const uint32_t*>(&b);
+        }
+        put(q, w[0], w[1], w[2], w[3]);
+      }
+      out(s * per);
+    }
+  } else {
+#pragma unroll
+    for (int s = 0; s < 4; ++s) {
+      if (s * per >= ncols) break;
+      ready();
+#pragma unroll
+      for (int q = 0; q < 8; ++q)
+        put(q, v[32 * s + 4 * q], v[32 * s + 4 * q + 1], v[32 * s + 4 * q + 2],
+            v[32 * s + 4 * q + 3]);
+      out(s * per);
+    }
+  }
+}
+
 // One work item (a 256x256 tile) as the roles of the kernel see it.
 struct Item {
   const GArgs* a;                            // what its problem's items have in common
@@ -289,13 +353,13 @@ struct Item {
   int sa, sb;                                // first scale chunks of A's pair tile and B's tile
   int64_t c0;                                // row of C that row 0 of the problem goes to
   int rows;                                  // rows of the problem
+  int z;                                     // its number among the matrices of C
   uint32_t pace_ns;
 };
 
 // Work says which items a launch has and where they lie:
 //   Params, the launch's __grid_constant__ argument; STAGES of the operand ring;
-//   TABLE, bytes of shared memory; STAGED, whether the epilogue goes through shared
-//   memory (G_STAGED_BYTES of it);
+//   TABLE, bytes of shared memory; OUT, how tiles leave (by TMA: store_map(g));
 //   first(g), the arguments that all items share; prefetch(g), of its tensor maps;
 //   load(g, table), by all threads, once the previous grid is complete;
 //   an object per role, whose tiles() counts the items and at(t) describes item t
@@ -306,7 +370,8 @@ __global__ void __launch_bounds__(G_THREADS, 1)
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~static_cast<uintptr_t>(1023));
-  uint64_t* full = reinterpret_cast<uint64_t*>(smem + Work::STAGES * G_STAGE_BYTES);
+  uint8_t* out = smem + Work::STAGES * G_STAGE_BYTES;   // staged tiles
+  uint64_t* full = reinterpret_cast<uint64_t*>(out + out_bytes(Work::OUT));
   uint64_t* empty = full + Work::STAGES;
   uint64_t* sf_ready = empty + Work::STAGES;
   uint64_t* tmem_full = sf_ready + Work::STAGES;
@@ -322,7 +387,7 @@ __global__ void __launch_bounds__(G_THREADS, 1)
   const uint32_t rank = cluster_rank();
   const bool leader = rank == 0;
   const GArgs& a0 = Work::first(g);   // format, epilogue kind and wait limit of the launch
-  void* table = smem + Work::STAGES * G_STAGE_BYTES + G_BAR_BYTES;
+  void* table = out + out_bytes(Work::OUT) + G_BAR_BYTES;
   if (threadIdx.x == 0) {
     Work::prefetch(g);
     for (int s = 0; s < Work::STAGES; ++s) {
@@ -588,15 +653,18 @@ __global__ void __launch_bounds__(G_THREADS, 1)
         uint8_t* chunk = a.q_scales + ((row >> 7) * (int64_t(a.N) >> 7) + (col0 >> 7)) * 512;
         *reinterpret_cast<uint32_t*>(chunk + (row & 31) * 16 + ((row & 127) >> 5) * 4) = 0u;
       }
-      if constexpr (Work::STAGED) {
-        uint8_t* const buf = smem + Work::STAGES * G_STAGE_BYTES + G_BAR_BYTES + Work::TABLE +
-                             (warp - 2) * (32 * G_PITCH);
+      if constexpr (Work::OUT != STORE_DIRECT) {
+        uint8_t* const buf = out + (warp - 2) * (out_bytes(Work::OUT) / 8);
         const int rows = static_cast<int>(min(int64_t(it.rows) - (row - lane), int64_t(32)));
         if (rows > 0 && col0 < a.N &&
             MXQ_IN_BOUNDS(Work::inside(it) && row - lane + rows <= it.rows, &g_err_gemm,
-                          SITE_B_GEMM_STORE))
-          store_staged(v, a, buf, it.c0 + row - lane, rows, col0,
-                       static_cast<int>(min(a.N - col0, int64_t(128))));
+                          SITE_B_GEMM_STORE)) {
+          const int ncols = static_cast<int>(min(a.N - col0, int64_t(128)));
+          if constexpr (Work::OUT == STORE_TMA)
+            store_tma<Work>(v, g, a.out_bf16 != 0, buf, it.z, static_cast<int>(row - lane),
+                            static_cast<int>(col0), ncols);
+          else store_staged(v, a, buf, it.c0 + row - lane, rows, col0, ncols);
+        }
       } else if (row < it.rows && col0 < a.N &&
           MXQ_IN_BOUNDS(Work::inside(it) && row >= 0 && col0 >= 0 && (col0 & 31) == 0,
                         &g_err_gemm, SITE_B_GEMM_STORE)) {
@@ -655,6 +723,9 @@ __global__ void __launch_bounds__(G_THREADS, 1)
     }
   }
 
+  // the copies out of shared memory are complete (only epilogue lanes have any)
+  if (Work::OUT == STORE_TMA && lane == 0)
+    asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
   tc_fence_before();
   cluster_sync();  // no CTA leaves while its peer may still signal it
   tc_fence_after();
@@ -686,7 +757,7 @@ int max_gemm_clusters(cudaLaunchConfig_t cfg) {
 template <typename Work>
 mxq_status gemm_kernel_run(const typename Work::Params& g, int64_t items, void* stream) {
   constexpr int smem = Work::STAGES * G_STAGE_BYTES + G_BAR_BYTES + Work::TABLE +
-                       (Work::STAGED ? G_STAGED_BYTES : 0) + 1024;
+                       out_bytes(Work::OUT) + 1024;
   static_assert(Work::STAGES <= G_STAGES && Work::TABLE % 16 == 0, "shared memory layout");
   static_assert(smem <= 232448, "shared memory of a CTA");
   if (!ensure_dynamic_smem(reinterpret_cast<const void*>(mx_gemm_kernel<Work>), smem))
