@@ -1013,6 +1013,13 @@ def _need_choices(row_of, weights, dev, tokens=None):
     return row_of.shape
 
 
+def _need_apart(out, t, name):
+    """out and t share no memory: a call reads rows of t after it has written rows of out."""
+    a, b = out.data_ptr(), t.data_ptr()
+    if a < b + t.numel() * t.element_size() and b < a + out.numel() * out.element_size():
+        raise ValueError(f"out and {name} share memory")
+
+
 def _need_offsets(offsets, counts, dev):
     """Returns the number of experts."""
     _need(counts, "counts", torch.int32, 1, dev)
@@ -1038,6 +1045,7 @@ def expert_gather(x: torch.Tensor, row_of, offsets, counts, rows, weights=None, 
         out = torch.empty((rows, cols), dtype=x.dtype, device=x.device)
     else:
         _need_rows(out, "out", x.dtype, (rows, cols), dev)
+        _need_apart(out, x, "x")
     a = _EXPERT_ROWS_ARGS.pack(x.data_ptr(), 0, out.data_ptr(), row_of.data_ptr(),
                                offsets.data_ptr(), counts.data_ptr(),
                                0 if weights is None else weights.data_ptr(), 0, tokens, rows, cols,
@@ -1056,6 +1064,7 @@ def expert_combine(y: torch.Tensor, row_of, weights=None, out=None):
         out = torch.empty((tokens, cols), dtype=y.dtype, device=y.device)
     else:
         _need_rows(out, "out", y.dtype, (tokens, cols), dev)
+        _need_apart(out, y, "y")
     a = _EXPERT_ROWS_ARGS.pack(0, y.data_ptr(), out.data_ptr(), row_of.data_ptr(), 0, 0,
                                0 if weights is None else weights.data_ptr(), 0, tokens, rows, cols,
                                topk, 0, code)
@@ -1080,6 +1089,9 @@ def expert_combine_backward(dout: torch.Tensor, y, row_of, offsets, counts, weig
         out = torch.empty_like(y)
     else:
         _need_rows(out, "out", y.dtype, (rows, cols), dev)
+        _need_apart(out, dout, "dout")
+        if out.data_ptr() != y.data_ptr():
+            _need_apart(out, y, "y")
     dweights = torch.empty((tokens, topk), dtype=torch.float32, device=y.device)
     a = _EXPERT_ROWS_ARGS.pack(dout.data_ptr(), y.data_ptr(), out.data_ptr(), row_of.data_ptr(),
                                offsets.data_ptr(), counts.data_ptr(),
@@ -1161,7 +1173,7 @@ def mx_gemm_experts(A, sA, B, sB, offsets, fmt, rows, N, K, out_dtype=torch.floa
     chunk layout, one buffer of mx_quantize(..., scale_layout="tc") per expert, one after
     another.  offsets: int32 [experts + 1] on the device (expert_order).  Rows that no
     expert holds are not written.  workspace: as gemm_experts_workspace returns it, for
-    callers that keep one."""
+    callers that keep one; two calls that may run at the same time need one each."""
     od = _out_code(out_dtype)
     experts = _count_experts(offsets)
     rows, N, K = int(rows), int(N), int(K)
@@ -1192,7 +1204,8 @@ def mx_gemm_experts_wgrad(A, sA, B, sB, offsets, fmt, M, N, rows, out_dtype=torc
     A: codes [M, rows] and row-major scales, B: [N, rows], both as
     mx_quantize(..., "col") writes them.  offsets: multiples of 32 (E2M1: 64), as
     expert_order(..., align=32) gives them.  workspace: as
-    gemm_experts_wgrad_workspace returns it, for callers that keep one."""
+    gemm_experts_wgrad_workspace returns it, for callers that keep one; two calls that
+    may run at the same time need one each."""
     od = _out_code(out_dtype)
     experts = _count_experts(offsets)
     rows, M, N = int(rows), int(M), int(N)

@@ -257,6 +257,17 @@ def test_rows_bindings(fake):
         lambda: mxq.expert_combine_backward(x.float(), y, row_of, offsets, counts),
         lambda: mxq.expert_combine_backward(x, y[:, :32].contiguous(), row_of, offsets, counts),
         lambda: mxq.expert_combine_backward(x, y, row_of, offsets, counts, out=y[:3])])
+    # reads and writes of one memory
+    big = torch.zeros(400, 33, dtype=BF)
+    _refused([
+        lambda: mxq.expert_gather(big[:5], row_of, offsets, counts, 160, out=big[:160]),
+        lambda: mxq.expert_gather(big[159:164], row_of, offsets, counts, 160, out=big[:160]),
+        lambda: mxq.expert_combine(big[:160], row_of, out=big[:5]),
+        lambda: mxq.expert_combine_backward(big[:5], y, row_of, offsets, counts, out=big[:160]),
+        lambda: mxq.expert_combine_backward(x, big[:160], row_of, offsets, counts,
+                                            out=big[1:161])])
+    mxq.expert_gather(big[160:165], row_of, offsets, counts, 160, out=big[:160])
+    fake.clear()
     assert not fake
 
 

@@ -157,6 +157,25 @@ def test_requantize_follows_the_weights():
     assert torch.equal(layer.infer(rows, offsets), before * 2.0)
 
 
+def test_no_tokens_and_one_expert_with_all():
+    layer = _layer(4, 64, 96)
+    rows, (row_of, offsets, counts) = layer.dispatch(
+        torch.empty(0, 96, dtype=torch.bfloat16, device="cuda"),
+        torch.empty(0, 2, dtype=torch.int64, device="cuda"))
+    y, saved = layer.forward(rows, offsets)
+    drows, dw = layer.backward(y, saved, offsets)
+    assert rows.shape == drows.shape == (0, 96) and dw.eq(0).all()
+    assert mxq.expert_combine(y, row_of).shape == (0, 64)
+    x = synth.normal((50, 96), 1).cuda()
+    ids = torch.full((50, 1), 2, device="cuda")
+    rows, (row_of, offsets, counts) = layer.dispatch(x, ids)
+    y, saved = layer.forward(rows, offsets)
+    _, dw = layer.backward(y, saved, offsets)
+    mxq.check()
+    assert offsets.tolist() == [0, 0, 0, 64, 64] and torch.equal(rows[:50], x)
+    assert dw[[0, 1, 3]].eq(0).all() and dw[2].ne(0).any()
+
+
 def test_refusals():
     w = torch.zeros(2, 64, 48, dtype=torch.bfloat16, device="cuda")
     with pytest.raises(ValueError):
@@ -173,10 +192,9 @@ def test_example_runs(bits):
     assert len(losses) == 3 and np.isfinite(losses).all() and np.isfinite(gap)
 
 
-def test_example_gradients_are_its_loss_differences():
-    # combine, product and gather are linear in the weights' codes: along a direction the
-    # loss of float64 products of the dequantized operands changes as dweight says, up to
-    # the rounding of the gradient's operands to E4M3 (2^-4 each) and of dout to bf16
+def test_weight_gradient_of_a_sum_of_experts():
+    # the gradient of sum_t <dout_t, sum_j gate W x_t> in float64, without any rounding, and the
+    # layer's, whose operands are rounded to E4M3 (2^-4 each) and dy to bf16
     tokens, experts, topk, out_f, in_f = 60, 3, 2, 64, 128
     layer = _layer(experts, out_f, in_f)
     x = synth.normal((tokens, in_f), 1).cuda()
