@@ -375,6 +375,80 @@ __global__ void __launch_bounds__(R_THREADS) expert_combine(const RowsArgs a) {
   }
 }
 
+// The same for aligned rows, with the rows' pieces on their way into shared memory while
+// those of the two units before are summed (a unit: a thread's piece of all rows of a
+// token).  Every thread copies and reads its own 16 bytes of a row, so no barrier is
+// needed, and no registers hold what is in flight.
+constexpr int C_AHEAD = 2;
+
+template <typename T, int G>
+__global__ void __launch_bounds__(R_THREADS) expert_combine_ring(const RowsArgs a) {
+  using P = Piece<T, true>;
+  extern __shared__ uint4 ring[];   // [C_AHEAD + 1][G][R_THREADS]
+  griddep_wait();
+  griddep_launch_dependents();
+  const Team team(a);
+  const T* const y = static_cast<const T*>(a.y);
+  T* const out = static_cast<T*>(a.out);
+  const int64_t c0 = int64_t(team.at) * P::REACH, step = int64_t(team.threads) * P::N;
+  if (team.t >= a.tokens || c0 >= a.cols) return;
+  uint4* const mine = ring + threadIdx.x;
+  // the unit that is fetched next; its token's choices, loaded when the last one's were used
+  int64_t ft = team.t, fc = c0;
+  Choices<G> k;
+  k.load(a, ft, 0);
+  int put = 0;
+  auto fetch = [&] {
+    if (ft < a.tokens) {
+      if (fc == c0) k.ready(a);
+#pragma unroll
+      for (int j = 0; j < G; ++j) {
+        const int bytes = k.row[j] < 0 ? 0 : 16;   // none: zeros are written
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(
+                         smem_u32(mine + (put * G + j) * R_THREADS)),
+                     "l"(y + max(k.row[j], 0) * a.cols + fc), "r"(bytes)
+                     : "memory");
+      }
+      fc += step;
+      if (fc >= a.cols) {
+        fc = c0;
+        ft += team.step;
+        k.load(a, ft, 0);
+      }
+      put = put == C_AHEAD ? 0 : put + 1;
+    }
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  };
+#pragma unroll
+  for (int i = 0; i < C_AHEAD; ++i) fetch();
+  int get = 0;
+  for (int64_t t = team.t; t < a.tokens; t += team.step) {
+    Choices<G> now;   // read anew: they are in the first-level cache
+    now.load(a, t, 0);
+    for (int64_t c = c0; c < a.cols; c += step) {
+      fetch();
+      asm volatile("cp.async.wait_group %0;" ::"n"(C_AHEAD) : "memory");
+      if (c == c0) now.ready(a);
+      float sum[P::N];
+#pragma unroll
+      for (int i = 0; i < P::N; ++i) sum[i] = 0.0f;
+#pragma unroll
+      for (int j = 0; j < G; ++j) {
+        P v;
+        v.v = mine[(get * G + j) * R_THREADS];
+        float f[P::N];
+        v.get(f);
+#pragma unroll
+        for (int i = 0; i < P::N; ++i) sum[i] = now.row[j] < 0 ? sum[i] : fmaf(now.w[j], f[i], sum[i]);
+      }
+      get = get == C_AHEAD ? 0 : get + 1;
+      P r;
+      r.set(sum);
+      r.store(out + t * a.cols + c, team.threads, a.cols - c);
+    }
+  }
+}
+
 // out[row of (t, j)] = w[t][j] x[t],  dweights[t][j] = <x[t], y[row of (t, j)]>.  out may
 // be y: a thread reads a piece of all its rows before it writes any.
 template <typename T, bool VEC, int G>
@@ -450,8 +524,9 @@ __global__ void __launch_bounds__(R_THREADS) expert_combine_backward(const RowsA
 enum RowsOp { GATHER, COMBINE, BACKWARD };
 
 // Teams that the device holds at once, or as many as there are.
-template <void (*KERNEL)(RowsArgs)>
+template <void (*KERNEL)(RowsArgs), int SMEM = 0>
 bool rows_launch_resident(int64_t ctas, cudaStream_t st, const RowsArgs& a) {
+  if (SMEM && !ensure_dynamic_smem(reinterpret_cast<const void*>(KERNEL), SMEM)) return false;
   static std::mutex mu;
   static int resident[64] = {0};   // CTAs of an SM, per device
   int dev = 0, n = 0;
@@ -461,7 +536,7 @@ bool rows_launch_resident(int64_t ctas, cudaStream_t st, const RowsArgs& a) {
     n = resident[dev];
   }
   if (n == 0) {
-    if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, KERNEL, R_THREADS, 0) != cudaSuccess ||
+    if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, KERNEL, R_THREADS, SMEM) != cudaSuccess ||
         n <= 0) {
       cudaGetLastError();
       n = 1;
@@ -470,7 +545,7 @@ bool rows_launch_resident(int64_t ctas, cudaStream_t st, const RowsArgs& a) {
     resident[dev] = n;
   }
   const int64_t grid = std::min<int64_t>(ctas, int64_t(n) * sm_count());
-  return launch_early(KERNEL, static_cast<unsigned>(grid), R_THREADS, 0, st, a);
+  return launch_early(KERNEL, static_cast<unsigned>(grid), R_THREADS, SMEM, st, a);
 }
 
 template <typename T, bool VEC, int G>
@@ -481,7 +556,13 @@ bool rows_launch_group(RowsOp op, int64_t ctas, cudaStream_t st, const RowsArgs&
     case GATHER:
       return launch_early(expert_gather<T, VEC, G>, static_cast<unsigned>(ctas), R_THREADS, 0, st,
                           a);
-    case COMBINE: return rows_launch_resident<expert_combine<T, VEC, G>>(ctas, st, a);
+    case COMBINE:
+      if constexpr (VEC) {
+        if (a.topk <= G)
+          return rows_launch_resident<expert_combine_ring<T, G>, (C_AHEAD + 1) * G * R_THREADS * 16>(
+              ctas, st, a);
+      }
+      return rows_launch_resident<expert_combine<T, VEC, G>>(ctas, st, a);
     default: return rows_launch_resident<expert_combine_backward<T, VEC, G>>(ctas, st, a);
   }
 }
