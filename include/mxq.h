@@ -605,11 +605,13 @@ size_t mxq_gemm_experts_wgrad_workspace_size(int64_t rows, int64_t M, int64_t N,
  *   m = beta1 m + (1 - beta1) g,   v = beta2 v + (1 - beta2) g^2
  *   p = p - lr weight_decay p
  *         - lr / (1 - beta1^t) * m / (sqrt(v / (1 - beta2^t)) + eps)
- * in fp32.  state_bits 32: m and v in fp32.  state_bits 8: m and r = sqrt(v) as E4M3
- * codes with one fp32 scale per 128 elements by the rule of the block-128 format
- * (the last block of a tensor shorter); an r above zero keeps at least the smallest
- * code, 2^-9 of its scale.  p's step uses m and v before that rounding.  A block
- * with a NaN or an infinity has scale NaN from then on.
+ * in fp32, one rounding per operation of m and v.  state_bits 32: m and v in fp32.
+ * state_bits 8: m and r = sqrt(v) as E4M3 codes with one fp32 scale per 128 elements
+ * (the last block of a tensor shorter):
+ *   scale = max(amax * RN(1 / 448), 2^-126),   code = RN_sat(value * (1 / scale))
+ * where an r above zero keeps at least the smallest code, 2^-9 of its scale.  p's step
+ * uses m and v before that rounding.  A block with a NaN or an infinity has scale NaN
+ * and zero codes, and stays so.
  */
 typedef struct {
   float* param;             /* [n]                                              */

@@ -70,19 +70,29 @@ struct AdamStep {
       skip = !(fabsf(scale) <= 3.402823466e38f);   // NaN or infinity: leave all as it is
     }
   }
-  // One element: m and v become the new moments, r = sqrt(v); returns the new p.  Root
-  // and quotient are the hardware's, within 2^-23 and 2^-22: the correctly rounded ones
-  // cost a third of the 8-bit step's instructions.  A divisor above zero is at least the
-  // root of the smallest fp32 value, 2^-75, so the quotient's range is not left.
+  // One element: m and v become the new moments, r = sqrt(v); returns the new p.
+  // The moments take one rounding per operation, the root's included: an 8-bit state
+  // amplifies a last bit into a whole code where a value lies next to a border, and so
+  // the same state comes from any fp32 program that follows the formula step by step.
+  // The quotient only enters p: it is the hardware's, within 2^-22.  A divisor above zero
+  // is at least the root of the smallest fp32 value, 2^-75, so its range is not left.
   MXQ_DEV float update(float p, float g, float decay, float& m, float& v, float& r) const {
-    g *= scale;
-    m = fmaf(b1, m, c1 * g);
-    v = fmaf(b2, v, c2 * g * g);
-    asm("sqrt.approx.f32 %0, %1;" : "=f"(r) : "f"(v));
+    g = __fmul_rn(g, scale);
+    m = __fadd_rn(__fmul_rn(m, b1), __fmul_rn(g, c1));
+    v = __fadd_rn(__fmul_rn(v, b2), __fmul_rn(__fmul_rn(g, g), c2));
+    r = __fsqrt_rn(v);
     const float kept = fmaf(-lr * decay, p, p);
     return fmaf(-step_size, __fdividef(m, fmaf(r, inv_r, eps)), kept);
   }
 };
+
+// Scale and multiplier of a block of a moment from its amax: the block-128 format's rule
+// with a product by 1 / 448 in place of the division.
+MXQ_DEV void moment_scale(float amax, float& scale, float& mul) {
+  const bool finite = amax <= 3.402823466e38f;
+  scale = finite ? fmaxf(__fmul_rn(amax, 1.0f / 448.0f), F_TINY) : __uint_as_float(0x7FFFFFFFu);
+  mul = finite ? __fdiv_rn(1.0f, scale) : 0.0f;
+}
 
 // Four consecutive elements, the first n where they are fewer; vec: one access.
 MXQ_DEV void load_n(const float* p, bool vec, int n, float (&f)[4]) {
@@ -219,7 +229,7 @@ MXQ_DEV void update_blocks(const AdamTensor& t, const G* g, const AdamStep& step
   }
   // all scales and their reciprocals at once, one per lane
   float mul;
-  fp8_scale<MXQ_E4M3>(top, scale, mul);
+  moment_scale(top, scale, mul);
   if (scaled) *scale_at = scale;
 #pragma unroll
   for (int q = 0; q < A_BLOCKS; ++q) {

@@ -521,6 +521,106 @@ __global__ void __launch_bounds__(R_THREADS) expert_combine_backward(const RowsA
   for (; t < a.tokens + a.experts; t += team.step) clear_padding<T, VEC>(a, t - a.tokens, team.at);
 }
 
+// The same for aligned rows and more than four choices, with the pieces two units ahead as
+// in expert_combine_ring (8192x8 x 4096 bf16: 210 us in registers, 188 us).  With fewer
+// choices the registers hold as much (4096x4 x 2048 fp32: 51.6 us, 53.8 us), and unaligned
+// rows copied element by element lose (4099x3 x 1001 fp32: 25.5 us, 27.8 us).
+template <typename T, int G>
+__global__ void __launch_bounds__(R_THREADS) expert_combine_backward_ring(const RowsArgs a) {
+  using P = Piece<T, true>;
+  static_assert(sizeof(P) == 16, "a slot of the ring");
+  extern __shared__ uint4 ring[];   // [C_AHEAD + 1][G + 1][R_THREADS], x's piece first
+  __shared__ float part[2][R_THREADS / 32][G];
+  griddep_wait();
+  griddep_launch_dependents();
+  const Team team(a);
+  const T* const x = static_cast<const T*>(a.x);
+  const T* const y = static_cast<const T*>(a.y);
+  T* const out = static_cast<T*>(a.out);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int64_t c0 = int64_t(team.at) * P::REACH, step = int64_t(team.threads) * P::N;
+  uint4* const mine = ring + threadIdx.x;
+  int64_t ft = c0 < a.cols ? team.t : a.tokens, fc = c0;
+  Choices<G> k;
+  k.load(a, ft, 0);
+  int put = 0;
+  auto copy = [&](int slot, const T* from, int bytes) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(
+                     smem_u32(mine + (put * (G + 1) + slot) * R_THREADS)),
+                 "l"(from), "r"(bytes)
+                 : "memory");
+  };
+  auto fetch = [&] {
+    if (ft < a.tokens) {
+      if (fc == c0) k.ready(a);
+      copy(0, x + ft * a.cols + fc, 16);
+#pragma unroll
+      for (int j = 0; j < G; ++j)
+        copy(1 + j, y + max(k.row[j], 0) * a.cols + fc, k.row[j] < 0 ? 0 : 16);
+      fc += step;
+      if (fc >= a.cols) {
+        fc = c0;
+        ft += team.step;
+        k.load(a, ft, 0);
+      }
+      put = put == C_AHEAD ? 0 : put + 1;
+    }
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  };
+#pragma unroll
+  for (int i = 0; i < C_AHEAD; ++i) fetch();
+  int get = 0, turn = 0;
+  int64_t t = team.t;
+  // a CTA's teams make the same number of turns: the sums between its warps need all
+  const int64_t first = int64_t(blockIdx.x) * (R_THREADS / a.team);
+  for (int64_t block = first; block < a.tokens; block += team.step, t += team.step, turn ^= 1) {
+    const bool live = t < a.tokens;
+    if (!live) clear_padding<T, true>(a, t - a.tokens, team.at);
+    Choices<G> now;   // read anew: they are in the first-level cache
+    now.load(a, t, 0);
+    now.ready(a);
+    float dot[G];
+#pragma unroll
+    for (int j = 0; j < G; ++j) dot[j] = 0.0f;
+    for (int64_t c = c0; live && c < a.cols; c += step) {
+      fetch();
+      asm volatile("cp.async.wait_group %0;" ::"n"(C_AHEAD) : "memory");
+      const uint4* const unit = mine + get * (G + 1) * R_THREADS;
+      float f[P::N];
+      reinterpret_cast<const P*>(unit)->get(f);
+#pragma unroll
+      for (int j = 0; j < G; ++j) {
+        if (now.row[j] < 0) continue;
+        float g[P::N];
+        reinterpret_cast<const P*>(unit + (1 + j) * R_THREADS)->get(g);
+#pragma unroll
+        for (int i = 0; i < P::N; ++i) {
+          dot[j] = fmaf(f[i], g[i], dot[j]);
+          g[i] = f[i] * now.w[j];
+        }
+        P s;
+        s.set(g);
+        s.store(out + now.row[j] * a.cols + c, team.threads, a.cols - c);
+      }
+      get = get == C_AHEAD ? 0 : get + 1;
+    }
+#pragma unroll
+    for (int j = 0; j < G; ++j) {
+      float s = dot[j];
+#pragma unroll
+      for (int d = 16; d; d >>= 1) s += __shfl_xor_sync(~0u, s, d);
+      if (lane == 0) part[turn][warp][j] = s;
+    }
+    __syncthreads();   // two buffers in turn, as above
+    if (live && team.at < a.topk) {
+      float s = 0.0f;
+      for (int v = 0; v < team.threads / 32; ++v) s += part[turn][warp + v][team.at];
+      a.dweights[t * a.topk + team.at] = s;
+    }
+  }
+  for (; t < a.tokens + a.experts; t += team.step) clear_padding<T, true>(a, t - a.tokens, team.at);
+}
+
 enum RowsOp { GATHER, COMBINE, BACKWARD };
 
 // Teams that the device holds at once, or as many as there are.
@@ -563,7 +663,13 @@ bool rows_launch_group(RowsOp op, int64_t ctas, cudaStream_t st, const RowsArgs&
               ctas, st, a);
       }
       return rows_launch_resident<expert_combine<T, VEC, G>>(ctas, st, a);
-    default: return rows_launch_resident<expert_combine_backward<T, VEC, G>>(ctas, st, a);
+    default:
+      if constexpr (VEC && G > 4) {
+        if (a.topk <= G)
+          return rows_launch_resident<expert_combine_backward_ring<T, G>,
+                                      (C_AHEAD + 1) * (G + 1) * R_THREADS * 16>(ctas, st, a);
+      }
+      return rows_launch_resident<expert_combine_backward<T, VEC, G>>(ctas, st, a);
   }
 }
 

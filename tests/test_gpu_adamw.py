@@ -1,11 +1,11 @@
 """The AdamW step on the GPU against the definition in float64.
 
 Tolerances, e = 2^-24 (half a step of fp32).  m and v: two rounded coefficients, products
-and one addition, 5 e of the terms' magnitudes (v one more for g^2).  The hardware's root
-is within 2^-23, 2 e, its quotient within two steps, 4 e.  p: one rounding of p, and the
-step: m's 6 e of its terms, half of v's 7 e, the root's 2, the factor's 2, one for eps,
-the quotient's 4, and 3 for the rate, whose expm1 form is within that: 22 e of the step
-that m's terms would give (U), and the product lr decay, 3 e of it.  8 bits: the state is what its codes stand for, rounded to fp32 once (e more, 2 e in
+and one addition, 5 e of the terms' magnitudes (v one more for g^2).  The hardware's
+quotient is within two steps, 4 e.  p: one rounding of p, and the step: m's 6 e of its
+terms, half of v's 7 e, one each for the root and its factor, two for the factor itself, one
+for eps, the quotient's 4, and 3 for the rate, whose expm1 form is within that: 22 e of the
+step that m's terms would give (U), and the product lr decay, 3 e of it.  8 bits: the state is what its codes stand for, rounded to fp32 once (e more, 2 e in
 v); the new code is half a step of four bits, 2^-4 of the value, or 2^-10 of the scale
 among the subnormal codes, and r's smallest code is 2^-9 of the scale; the scale is
 amax / 448 within its value's error and two more roundings.  Below 2^-126 a rounding is
@@ -120,6 +120,36 @@ def test_steps(bits, dtype, offset):
     for step in (1, 2, 3, 50):
         plan = _step_and_check(params, _grads(SIZES, step, dtype, offset), states, step, copies,
                                plan=plan)
+
+
+def test_codes_of_the_formula_step_by_step():
+    # each operation rounded once: the same formula in numpy's fp32 gives the same codes,
+    # scales and moments, bit for bit
+    n, f = 5000, np.float32
+    p, g = _params([n], 1), _grads([n], 2)
+    other = p[0].clone()
+    state, plain = mxq.adamw_state(p[0], 8), mxq.adamw_state(other, 32)
+    plans = [mxq.adamw_plan(p, [state]), mxq.adamw_plan([other], [plain])]
+    from oracle import mx_oracle as O
+    table = O.decode_table("e4m3").astype(f)
+    decode = lambda c, s: table[to_np(c)] * np.repeat(to_np(s), 128)[:n]
+    b1, c1, b2, c2 = f(0.9), f(1 - 0.9), f(0.95), f(1 - 0.95)
+    for step in (1, 2, 3):
+        d = to_np(g[0])
+        old = [decode(*state[0]), decode(*state[1]) ** 2, to_np(plain[0]), to_np(plain[1])]
+        for plan in plans:
+            mxq.adamw_step(plan, g, step, 1e-3, betas=BETAS)
+        mxq.check()
+        m, v = old[0] * b1 + d * c1, old[1] * b2 + d * d * c2
+        for (codes, scales), x, least in ((state[0], m, f(0)), (state[1], np.sqrt(v), f(2.0 ** -9))):
+            t = np.pad(x, (0, -n % 128)).reshape(-1, 128)
+            s = np.maximum(np.abs(t).max(1) * (f(1) / f(448)), f(2.0 ** -126))
+            q = t * (f(1) / s)[:, None]
+            q = np.where(t > 0, np.maximum(q, least), q).reshape(-1)[:n]
+            want = O.encode_element(O.round_to_element(q.astype(np.float64), "e4m3"), "e4m3")
+            assert np.array_equal(to_np(scales), s) and np.array_equal(to_np(codes), want)
+        assert np.array_equal(to_np(plain[0]), old[2] * b1 + d * c1)
+        assert np.array_equal(to_np(plain[1]), old[3] * b2 + d * d * c2)
 
 
 def test_matrices_decays_and_no_copies():
