@@ -79,6 +79,7 @@ struct ExpertWork {
     for (int i = threadIdx.x; i < 3 * (g.experts + 1); i += blockDim.x)
       static_cast<int32_t*>(table)[i] = g.table[i];
   }
+  static int table_bytes(const ExpertParams& g) { return 3 * (g.experts + 1) * 4; }
   MXQ_DEV static const CUtensorMap* store_map(const ExpertParams& g) { return &g.tc; }
   MXQ_DEV int tiles() const { return tile0[g.experts]; }
   MXQ_DEV Item at(int t) {

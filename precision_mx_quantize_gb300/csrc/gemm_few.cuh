@@ -3,9 +3,11 @@
 // lines of the weight are the tensor cores' M and T tokens their N, and a K stage costs
 // an MMA of T columns, where a 256x256 tile computes 256 columns for a handful of rows.
 //   out[t][n] = sum_k w[n][k] x[t][k]
-// One CTA per SM walks the tiles (expert, 128 lines, T tokens), the tokens fastest, so
-// that CTAs that share a weight's lines run together.  A ring of 160 KB and more in
-// flight per SM hides the memory's latency.
+// Two CTAs per SM walk the tiles (expert, 128 lines, T tokens), the tokens fastest, so
+// that CTAs that share a weight's lines run together.  Two, because a tensor-core
+// instruction costs the lane that issues it about 100 cycles, however few its columns:
+// one CTA with a ring as long issues five of them for 16 KB of weight
+// (FEW_NOTE).
 //   warp 0   TMA: 128 bytes of K of the lines and of the tokens, their scale chunks
 //   warp 1   tensor memory; one lane issues the MMAs into two accumulators in turn
 //   warps 2-5  epilogue: a line per lane, so that a token's 32 outputs are side by side
@@ -25,11 +27,13 @@ template <int T>
 struct Few {
   // scales: up to two chunks of each operand
   static constexpr int STAGE = W_OPERAND + T * G_BKB + 2048;
-  static constexpr int STAGES = T == 16 ? 10 : 8;
+  static constexpr int STAGES = T == 16 ? 5 : 4;          // two CTAs fit in an SM
   static constexpr uint32_t SF_COL0 = 2 * T;              // two accumulators before them
-  static constexpr uint32_t TMEM = 256;
+  static constexpr uint32_t TMEM = T == 16 ? 128 : 256;
+  static constexpr int FIXED = STAGES * STAGE + G_BAR_BYTES + 1024;   // and the table
   static_assert(T % 16 == 0 && SF_COL0 + 16 * STAGES <= TMEM, "tensor memory");
   static_assert(STAGE % 1024 == 0, "swizzle atoms");
+  static_assert(2 * (FIXED + 3 * 257 * 4 + 1024) <= 228 * 1024, "two CTAs with 256 experts");
 };
 
 MXQ_DEV void tc_cp_sf(uint32_t taddr, uint32_t smem_addr) {
@@ -60,7 +64,7 @@ MXQ_DEV void mma_mxf4(uint32_t d_tmem, uint64_t a, uint64_t b, uint32_t idesc, u
 // Work is the expert table's walker with tiles of 128 lines by T tokens: at(t) gives an
 // Item whose mp counts token tiles and nt tiles of lines.
 template <typename Work, int T>
-__global__ void __launch_bounds__(W_THREADS, 1)
+__global__ void __launch_bounds__(W_THREADS, 2)
     mx_gemm_few(const __grid_constant__ typename Work::Params g) {
   using F = Few<T>;
   constexpr int S = F::STAGES;
@@ -264,14 +268,14 @@ __global__ void __launch_bounds__(W_THREADS, 1)
   if (warp == 1) tmem_dealloc(tmem, F::TMEM);
 }
 
-// Launches the kernel on as many CTAs as there are SMs, at most `items`.
+// Launches the kernel on two CTAs per SM, at most `items`.
 template <typename Work, int T>
 mxq_status gemm_few_run(const typename Work::Params& g, int64_t items, void* stream) {
-  constexpr int smem = Few<T>::STAGES * Few<T>::STAGE + G_BAR_BYTES + Work::TABLE + 1024;
-  static_assert(smem <= 232448, "shared memory of a CTA");
+  // the table takes what this launch's experts need
+  const int smem = Few<T>::FIXED + (Work::table_bytes(g) + 15) / 16 * 16;
   if (!ensure_dynamic_smem(reinterpret_cast<const void*>(mx_gemm_few<Work, T>), smem))
     return MXQ_ERR_CUDA;
-  const unsigned grid = static_cast<unsigned>(std::min<int64_t>(items, sm_count()));
+  const unsigned grid = static_cast<unsigned>(std::min<int64_t>(items, 2 * sm_count()));
   if (!launch_early(mx_gemm_few<Work, T>, grid, W_THREADS, smem, static_cast<cudaStream_t>(stream),
                     g))
     return MXQ_ERR_CUDA;
