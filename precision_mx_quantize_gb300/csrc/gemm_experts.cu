@@ -9,7 +9,8 @@
 // A first kernel turns the offsets into a table (first row, first tile and first scale
 // chunk of every expert) and rewrites row-major scales into the tensor cores' chunks,
 // for every expert from a chunk of its own.  The product's kernel (gemm_kernel.cuh) then
-// walks the tiles of all experts as one persistent grid.
+// walks the tiles of all experts as one persistent grid.  With few rows to an expert
+// there is no first kernel: the product's makes the table and A's chunks itself.
 //
 // rows: rows of a tile past the expert's end are the next expert's; they are computed
 // and not stored.  Experts with few rows have tiles of their own (gemm_few.cuh).  wgrad: offsets are multiples of an MMA's K (32 elements, E2M1 64),
@@ -26,6 +27,23 @@ namespace {
 constexpr int X_MAX = 1024;                 // experts
 constexpr int X_TABLE = 3 * (X_MAX + 1);    // words of the table
 
+// What the table and the scale chunks are made from.
+struct PrepareArgs {
+  const int32_t* offsets;
+  int32_t rows, experts;
+  int32_t unit;            // offsets are multiples of it
+  int32_t n_nt;            // rows: tiles along N
+  int32_t tile_rows, chunk_rows;   // rows: of a tile, of a scale chunk of A
+  int32_t tiles;           // wgrad: tiles of an expert
+  int32_t stage_rows;      // wgrad: elements of K per stage
+  int32_t stage_chunks;    // wgrad: chunks per stage
+  int32_t* table;
+  const uint8_t *sa, *sb;  // row-major scales; sb NULL: B's are in chunks already
+  uint8_t *ca, *cb;
+  int32_t lines_a, lines_b;   // wgrad: lines of A and of B; rows: lines of one expert's B
+  int32_t kb, kcs;            // blocks in a line of scales, chunks per 128-line tile
+};
+
 // The table: off[experts + 1], tile0[experts + 1], sf0[experts + 1].  sf0 counts, in
 // the form rows, 128-row tiles of A's scale chunks; in wgrad, chunks along K.
 struct ExpertParams {
@@ -36,7 +54,69 @@ struct ExpertParams {
   int32_t experts;
   int32_t b_tiles;       // rows: 128-line scale tiles of one expert's B
   int32_t stores;        // 32-byte stores per row of a tile
+  PrepareArgs prep;      // few rows: the kernel makes its table itself
 };
+
+// The table from the offsets, by one warp.  Offsets that fall, lie outside the rows or
+// split an MMA's K are moved to the nearest that do not, so that no tile leaves the
+// buffers, and reported.
+template <bool ALONG_K>
+MXQ_DEV void make_table(const PrepareArgs& p, int32_t* table, bool report) {
+  int32_t *off = table, *tile0 = off + p.experts + 1, *sf0 = tile0 + p.experts + 1;
+  const int lane = threadIdx.x & 31;
+  bool bad = false;
+  auto placed = [&](int i) {
+    const int raw = p.offsets[i];
+    const int v = min(max(raw, 0), p.rows) / p.unit * p.unit;
+    bad |= v != raw;
+    return v;
+  };
+  int end = placed(0), tiles = 0, sfs = 0;
+  if (lane == 0) {
+    off[0] = end;
+    tile0[0] = sf0[0] = 0;
+  }
+  for (int i = lane; i - lane < p.experts; i += 32) {
+    const bool live = i < p.experts;
+    int v = live ? placed(i + 1) : 0;
+    const int own = v;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+      const int o = __shfl_up_sync(~0u, v, d);
+      if (lane >= d) v = max(v, o);
+    }
+    v = max(v, end);
+    bad |= live && v != own;
+    int before = __shfl_up_sync(~0u, v, 1);
+    if (lane == 0) before = end;
+    const int len = v - before;
+    int nt, ns;
+    if (ALONG_K) {
+      nt = live ? p.tiles : 0;
+      ns = (len + p.stage_rows - 1) / p.stage_rows * p.stage_chunks;
+    } else {
+      nt = (len + p.tile_rows - 1) / p.tile_rows * p.n_nt;
+      ns = (len + p.chunk_rows - 1) / p.chunk_rows;
+    }
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+      const int a = __shfl_up_sync(~0u, nt, d), b = __shfl_up_sync(~0u, ns, d);
+      if (lane >= d) {
+        nt += a;
+        ns += b;
+      }
+    }
+    if (live) {
+      off[i + 1] = v;
+      tile0[i + 1] = tiles + nt;
+      sf0[i + 1] = sfs + ns;
+    }
+    end = __shfl_sync(~0u, v, 31);
+    tiles += __shfl_sync(~0u, nt, 31);
+    sfs += __shfl_sync(~0u, ns, 31);
+  }
+  if (bad && report) record_error(&g_err_gemm, MXQ_ERR_ARG, SITE_EXPERT_OFFSETS);
+}
 
 // How a launch's tiles lie: 256 rows of an expert by 256 of its columns, stored straight
 // from the accumulators or through shared memory; a weight gradient's 256x256; or T
@@ -71,13 +151,17 @@ struct ExpertWork {
   MXQ_DEV static void prefetch(const ExpertParams& g) {
     prefetch_tmap(&g.ta);
     prefetch_tmap(&g.tb);
-    prefetch_tmap(&g.tsa);
+    if (!is_few(FORM)) prefetch_tmap(&g.tsa);
     prefetch_tmap(&g.tsb);
     if (FORM == WGRAD) prefetch_tmap(&g.tc);
   }
   MXQ_DEV static void load(const ExpertParams& g, void* table) {
-    for (int i = threadIdx.x; i < 3 * (g.experts + 1); i += blockDim.x)
-      static_cast<int32_t*>(table)[i] = g.table[i];
+    if constexpr (is_few(FORM)) {
+      if (threadIdx.x < 32) make_table<false>(g.prep, static_cast<int32_t*>(table), blockIdx.x == 0);
+    } else {
+      for (int i = threadIdx.x; i < 3 * (g.experts + 1); i += blockDim.x)
+        static_cast<int32_t*>(table)[i] = g.table[i];
+    }
   }
   static int table_bytes(const ExpertParams& g) { return 3 * (g.experts + 1) * 4; }
   MXQ_DEV static const CUtensorMap* store_map(const ExpertParams& g) { return &g.tc; }
@@ -134,22 +218,6 @@ struct ExpertWork {
 
 // ---- the table and the scale chunks -------------------------------------------
 
-struct PrepareArgs {
-  const int32_t* offsets;
-  int32_t rows, experts;
-  int32_t unit;            // offsets are multiples of it
-  int32_t n_nt;            // rows: tiles along N
-  int32_t tile_rows, chunk_rows;   // rows: of a tile, of a scale chunk of A
-  int32_t tiles;           // wgrad: tiles of an expert
-  int32_t stage_rows;      // wgrad: elements of K per stage
-  int32_t stage_chunks;    // wgrad: chunks per stage
-  int32_t* table;
-  const uint8_t *sa, *sb;  // row-major scales; sb NULL: B's are in chunks already
-  uint8_t *ca, *cb;
-  int32_t lines_a, lines_b;   // wgrad: lines of A and of B; rows: lines of one expert's B
-  int32_t kb, kcs;            // blocks in a line of scales, chunks per 128-line tile
-};
-
 // Largest i with first[i] <= at (first[0] == 0, first[n] > at).
 MXQ_DEV int holder(const int32_t* first, int n, int at) {
   int lo = 0, hi = n;
@@ -172,16 +240,7 @@ MXQ_DEV void write_chunk(uint8_t* chunk, const uint8_t* s, int64_t line, int64_t
   for (int q = 0; q < 4; ++q) {
     w[q] = 0u;
     const int64_t r = line + lane + 32 * q;
-    if (r < lines) {
-      const uint8_t* p = s + r * kb + block;
-      if (n >= 4 && (reinterpret_cast<uintptr_t>(p) & 3u) == 0) {
-        w[q] = *reinterpret_cast<const uint32_t*>(p);
-      } else {
-#pragma unroll
-        for (int u = 0; u < 4; ++u)
-          if (u < n) w[q] |= static_cast<uint32_t>(p[u]) << (8 * u);
-      }
-    }
+    if (r < lines) w[q] = scale_word(s + r * kb + block, n);
   }
   *reinterpret_cast<uint4*>(chunk + lane * 16) = make_uint4(w[0], w[1], w[2], w[3]);
 }
@@ -189,66 +248,10 @@ MXQ_DEV void write_chunk(uint8_t* chunk, const uint8_t* s, int64_t line, int64_t
 template <bool ALONG_K>
 __global__ void __launch_bounds__(256) experts_prepare(const PrepareArgs p) {
   __shared__ int32_t table[X_TABLE];
-  int32_t *off = table, *tile0 = off + p.experts + 1, *sf0 = tile0 + p.experts + 1;
+  const int32_t *off = table, *sf0 = off + 2 * (p.experts + 1);
   griddep_wait();
   griddep_launch_dependents();
-  const int lane = threadIdx.x & 31;
-  if (threadIdx.x < 32) {
-    // Offsets that fall, lie outside the rows or split an MMA's K are moved to the
-    // nearest that do not, so that no tile leaves the buffers, and reported.
-    bool bad = false;
-    auto placed = [&](int i) {
-      const int raw = p.offsets[i];
-      const int v = min(max(raw, 0), p.rows) / p.unit * p.unit;
-      bad |= v != raw;
-      return v;
-    };
-    int end = placed(0), tiles = 0, sfs = 0;
-    if (lane == 0) {
-      off[0] = end;
-      tile0[0] = sf0[0] = 0;
-    }
-    for (int i = lane; i - lane < p.experts; i += 32) {
-      const bool live = i < p.experts;
-      int v = live ? placed(i + 1) : 0;
-      const int own = v;
-#pragma unroll
-      for (int d = 1; d < 32; d <<= 1) {
-        const int o = __shfl_up_sync(~0u, v, d);
-        if (lane >= d) v = max(v, o);
-      }
-      v = max(v, end);
-      bad |= live && v != own;
-      int before = __shfl_up_sync(~0u, v, 1);
-      if (lane == 0) before = end;
-      const int len = v - before;
-      int nt, ns;
-      if (ALONG_K) {
-        nt = live ? p.tiles : 0;
-        ns = (len + p.stage_rows - 1) / p.stage_rows * p.stage_chunks;
-      } else {
-        nt = (len + p.tile_rows - 1) / p.tile_rows * p.n_nt;
-        ns = (len + p.chunk_rows - 1) / p.chunk_rows;
-      }
-#pragma unroll
-      for (int d = 1; d < 32; d <<= 1) {
-        const int a = __shfl_up_sync(~0u, nt, d), b = __shfl_up_sync(~0u, ns, d);
-        if (lane >= d) {
-          nt += a;
-          ns += b;
-        }
-      }
-      if (live) {
-        off[i + 1] = v;
-        tile0[i + 1] = tiles + nt;
-        sf0[i + 1] = sfs + ns;
-      }
-      end = __shfl_sync(~0u, v, 31);
-      tiles += __shfl_sync(~0u, nt, 31);
-      sfs += __shfl_sync(~0u, ns, 31);
-    }
-    if (bad && blockIdx.x == 0) record_error(&g_err_gemm, MXQ_ERR_ARG, SITE_EXPERT_OFFSETS);
-  }
+  if (threadIdx.x < 32) make_table<ALONG_K>(p, table, blockIdx.x == 0);
   __syncthreads();
   if (blockIdx.x == 0)
     for (int i = threadIdx.x; i < 3 * (p.experts + 1); i += blockDim.x) p.table[i] = table[i];
@@ -272,7 +275,7 @@ __global__ void __launch_bounds__(256) experts_prepare(const PrepareArgs p) {
     }
   } else {
     const int64_t tiles_b = (p.lines_b + 127) / 128;
-    const int64_t units_a = int64_t(sf) * p.kcs;
+    const int64_t units_a = p.sa ? int64_t(sf) * p.kcs : 0;   // few rows: B's chunks alone
     const int64_t units = units_a + (p.sb ? p.experts * tiles_b * p.kcs : 0);
     for (int64_t u = warp; u < units; u += warps) {
       const bool is_a = u < units_a;
@@ -314,17 +317,18 @@ constexpr int64_t X_LIM = int64_t(1) << 31;
 
 // The form of a rows product from its sizes; the device alone knows the experts' rows, so
 // it goes by their average over the experts that can have any.  Measured, 64 experts of
-// 4096x4096 E2M1 (2048x2048 E4M3), us at an average of 1 (of 8 experts), 8, 16, 32, 64:
-//   FEW16  20.5 (14.0)  92.7 (50.8)  115 (61.6)   186 (97.9)
-//   FEW64  25.1 (15.3)  91.2 (52.3)  96.2 (53.2)  102 (57.6)  128 (71.4)
-//   ROWS   27.2 (16.4)  97.3 (56.4)  102 (56.9)   105 (58.3)  108 (60.3)
+// 4096x4096 E2M1 (2048x2048 E4M3), us at an average of 1 (of 8 experts), 8, 16, 32, 64
+// (*: with the scales from a launch of their own, 3 us):
+//   FEW16  17.1 (12.2)   85.8 (45.2)   89.4 (47.4)   118* (63.7*)  184* (96.5*)
+//   FEW64  24.0* (16.6*) 90.7* (51.5*) 93.5* (52.5*) 101 (52.4)    108* (60.5*)
+//   ROWS   27.2 (16.4)   97.3 (56.4)   102 (56.9)    105 (58.3)    108 (60.3)
 // Through shared memory, the stores of a tile take less of the SM's memory path, and a
 // stage of the ring less: 9 stages to a tile, 1237 rows of 7 experts, 13.0 against 15.2
 // us; 16 stages, 62 against 58 us at an average of 32.
 Form rows_form(const mxq_experts_args& q, int64_t kbytes) {
   const int64_t average = q.rows / std::max<int64_t>(1, std::min<int64_t>(q.experts, q.rows));
-  if (average <= 8) return FEW16;
-  if (average <= 32) return FEW64;
+  if (average <= 16) return FEW16;
+  if (average <= 48) return FEW64;
   return kbytes <= 12 * G_BKB ? ROWS_STAGED : ROWS;
 }
 
@@ -364,7 +368,7 @@ bool expert_plan(const mxq_experts_args& q, bool wgrad, ExpertPlan& p) {
     p.items = (q.rows / tile_rows(p.form) + std::min<int64_t>(q.experts, q.rows)) * p.n_nt;
     p.ws_b = q.b_scale_layout == MXQ_SCALES_TC ? 0 : p.tiles_b * p.kcs * 512;
   }
-  p.ws_a = p.tiles_a * p.kcs * 512;
+  p.ws_a = is_few(p.form) ? 0 : p.tiles_a * p.kcs * 512;   // few rows: chunks are made in place
   // tile numbers and chunk numbers are 32-bit (up to two tiles past the last are named)
   return p.items < X_LIM && (p.tiles_a + 2) * p.kcs < X_LIM && (p.tiles_b + 2) * p.kcs < X_LIM;
 }
@@ -376,6 +380,7 @@ mxq_status experts_launch(const mxq_experts_args& q, void* stream) {
   if (!expert_plan(q, ALONG_K, p)) return MXQ_ERR_ARG;
   const bool fp4 = q.fmt == MXQ_E2M1, bf16 = q.out_dtype == MXQ_OUT_BF16;
   const bool tc = !ALONG_K && q.b_scale_layout == MXQ_SCALES_TC;
+  const bool few = is_few(p.form);
   if (tc && q.K % p.stage_rows != 0) return MXQ_ERR_ARG;
   if (q.N % (bf16 ? 8 : 4) != 0) return MXQ_ERR_ALIGN;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
@@ -430,7 +435,7 @@ mxq_status experts_launch(const mxq_experts_args& q, void* stream) {
                          CU_TENSOR_MAP_L2_PROMOTION_L2_256B) == CUDA_SUCCESS;
   };
   if (!codes(&g.ta, q.A, lines_a, chunk_rows(p.form)) || !codes(&g.tb, q.B, lines_b, G_BM) ||
-      !chunks(&g.tsa, r.ca, p.tiles_a) ||
+      (!few && !chunks(&g.tsa, r.ca, p.tiles_a)) ||
       !chunks(&g.tsb, tc ? static_cast<const void*>(q.sB) : r.cb, p.tiles_b))
     return MXQ_ERR_CUDA;
   if (ALONG_K) {
@@ -469,9 +474,14 @@ mxq_status experts_launch(const mxq_experts_args& q, void* stream) {
   g.experts = q.experts;
   g.b_tiles = static_cast<int32_t>((q.N + 127) / 128);
 
-  const int64_t units = (p.tiles_a + (tc ? 0 : p.tiles_b)) * p.kcs;
-  const unsigned grid = static_cast<unsigned>(std::min<int64_t>((units + 7) / 8, 4 * sm_count()));
-  if (!launch_early(experts_prepare<ALONG_K>, grid, 256, 0, st, r)) return MXQ_ERR_CUDA;
+  g.prep = r;
+  if (few) r.sa = nullptr;
+  if (!few || !tc) {
+    const int64_t units = ((few ? 0 : p.tiles_a) + (tc ? 0 : p.tiles_b)) * p.kcs;
+    const unsigned grid =
+        static_cast<unsigned>(std::min<int64_t>((units + 7) / 8, 4 * sm_count()));
+    if (!launch_early(experts_prepare<ALONG_K>, grid, 256, 0, st, r)) return MXQ_ERR_CUDA;
+  }
   if constexpr (ALONG_K) {
     return gemm_kernel_run<ExpertWork<WGRAD>>(g, p.items, stream);
   } else {

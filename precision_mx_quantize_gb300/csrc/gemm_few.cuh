@@ -5,13 +5,16 @@
 //   out[t][n] = sum_k w[n][k] x[t][k]
 // Two CTAs per SM walk the tiles (expert, 128 lines, T tokens), the tokens fastest, so
 // that CTAs that share a weight's lines run together.  Two, because a tensor-core
-// instruction costs the lane that issues it about 100 cycles, however few its columns:
-// one CTA with a ring as long issues five of them for 16 KB of weight
-// (FEW_NOTE).
-//   warp 0   TMA: 128 bytes of K of the lines and of the tokens, their scale chunks
+// instruction costs the lane that issues it about 100 cycles, however few its columns, and
+// 16 KB of weight take five of them (128 tokens of 8 experts of 64, 4096x4096 E2M1, T 16:
+// 93.5 us, 115 us with one CTA and a ring as long).
+//   warp 0   TMA: 128 bytes of K of the lines and of the tokens, the lines' scale chunks
 //   warp 1   tensor memory; one lane issues the MMAs into two accumulators in turn
 //   warps 2-5  epilogue: a line per lane, so that a token's 32 outputs are side by side
 //   warp 6   one lane copies each stage's scales into tensor memory
+//   warp 7   writes the tokens' scales of each stage where the copy reads them, out of
+//            the row-major ones: a launch before this one would cost a single token more
+//            than its scales do
 #pragma once
 
 #include "gemm_kernel.cuh"
@@ -19,7 +22,7 @@
 namespace mxq {
 namespace {
 
-constexpr int W_THREADS = 224;
+constexpr int W_THREADS = 256;
 constexpr int W_LINES = 128;
 constexpr int W_OPERAND = W_LINES * G_BKB;   // a stage's lines of the weight
 
@@ -61,6 +64,18 @@ MXQ_DEV void mma_mxf4(uint32_t d_tmem, uint64_t a, uint64_t b, uint32_t idesc, u
       : "memory");
 }
 
+// Four scales of a line from p on, the first in the lowest byte; the n that are left of the
+// line where they are fewer.  Any alignment.
+MXQ_DEV uint32_t scale_word(const uint8_t* p, int n) {
+  if (n >= 4 && (reinterpret_cast<uintptr_t>(p) & 3u) == 0)
+    return *reinterpret_cast<const uint32_t*>(p);
+  uint32_t w = 0;
+#pragma unroll
+  for (int u = 0; u < 4; ++u)
+    if (u < n) w |= static_cast<uint32_t>(p[u]) << (8 * u);
+  return w;
+}
+
 // Work is the expert table's walker with tiles of 128 lines by T tokens: at(t) gives an
 // Item whose mp counts token tiles and nt tiles of lines.
 template <typename Work, int T>
@@ -87,7 +102,7 @@ __global__ void __launch_bounds__(W_THREADS, 2)
   if (threadIdx.x == 0) {
     Work::prefetch(g);
     for (int s = 0; s < S; ++s) {
-      mbar_init(smem_u32(&full[s]), 1);
+      mbar_init(smem_u32(&full[s]), 2);   // the copies and the tokens' scales
       mbar_init(smem_u32(&empty[s]), 1);
       mbar_init(smem_u32(&sf_ready[s]), 1);
     }
@@ -132,12 +147,11 @@ __global__ void __launch_bounds__(W_THREADS, 2)
             break;
           }
           const uint32_t st = smem_u32(smem + s * F::STAGE), bar = smem_u32(&full[s]);
-          mbar_arrive_expect_tx(bar, W_OPERAND + T * G_BKB + 1024u * n_sf);
+          mbar_arrive_expect_tx(bar, W_OPERAND + T * G_BKB + 512u * n_sf);
           tma_load_2d(st, it.tb, bar, ks * G_BKB, it.by);
           tma_load_2d(st + W_OPERAND, it.ta, bar, ks * G_BKB, it.ay);
           const uint32_t sf = st + W_OPERAND + T * G_BKB;
           tma_load_2d(sf, it.tsb, bar, 0, it.sb + ks * n_sf);
-          tma_load_2d(sf + 1024, it.tsa, bar, 0, it.sa + ks * n_sf);
           ++issued;
           if (++s == S) { s = 0; phase ^= 1; }
         }
@@ -224,6 +238,67 @@ __global__ void __launch_bounds__(W_THREADS, 2)
       tc_commit(smem_u32(&drain[1]));
       if (!mbar_wait(smem_u32(&drain[1]), 0, tmo))
         record_error(&g_err_gemm, MXQ_ERR_TIMEOUT, SITE_GEMM_DRAIN);
+    }
+  } else if (warp == 7) {
+    // A chunk holds row r's four scales at (r % 32) * 16 + (r / 32) * 4; rows from T on
+    // are no columns of the MMAs.  The words of AHEAD stages are loaded together, those of
+    // the next ones while these are written.
+    constexpr int WORDS = T == 16 ? 1 : 4, AHEAD = T == 16 ? 8 : 4;
+    const auto& p = g.prep;
+    uint32_t s = 0, phase = 0;
+    bool ok = true;
+    Work work(g, table);
+    for (int t = blockIdx.x; t < n_tiles && ok; t += step) {
+      const Item it = work.at(t);
+      const int rows = min(it.rows - it.mp * T, T);
+      uint32_t next[AHEAD][WORDS], now[AHEAD][WORDS];
+      auto place = [&](int i, int& row, int& chunk) {
+        row = T == 16 ? lane & 15 : lane + 32 * (i & 1);
+        chunk = T == 16 ? lane >> 4 : i >> 1;
+      };
+      auto load = [&](int ks0) {
+#pragma unroll
+        for (int b = 0; b < AHEAD; ++b)
+#pragma unroll
+          for (int i = 0; i < WORDS; ++i) {
+            int row, chunk;
+            place(i, row, chunk);
+            const int block = ((ks0 + b) * n_sf + chunk) * 4;
+            next[b][i] = 0u;
+            if (row < rows && chunk < n_sf && ks0 + b < nk && block < p.kb)
+              next[b][i] = scale_word(p.sa + int64_t(it.ay + row) * p.kb + block, p.kb - block);
+          }
+      };
+      load(0);
+      for (int ks0 = 0; ks0 < nk && ok; ks0 += AHEAD) {
+#pragma unroll
+        for (int b = 0; b < AHEAD; ++b)
+#pragma unroll
+          for (int i = 0; i < WORDS; ++i) now[b][i] = next[b][i];
+        load(ks0 + AHEAD);
+#pragma unroll
+        for (int b = 0; b < AHEAD; ++b) {
+          if (ks0 + b >= nk || !ok) break;
+          ok = __all_sync(~0u, gwait(smem_u32(&empty[s]), phase ^ 1, tmo, abort_flag));
+          if (!ok) {
+            if (lane == 0 && !*abort_flag) gabort(abort_flag, SITE_GEMM_EMPTY);
+            break;
+          }
+          uint8_t* const sf = smem + s * F::STAGE + W_OPERAND + T * G_BKB + 1024;
+#pragma unroll
+          for (int i = 0; i < WORDS; ++i) {
+            int row, chunk;
+            place(i, row, chunk);
+            if (chunk < n_sf)
+              *reinterpret_cast<uint32_t*>(sf + chunk * 512 + (row & 31) * 16 + (row >> 5) * 4) =
+                  now[b][i];
+          }
+          asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+          __syncwarp();
+          if (lane == 0) mbar_arrive(smem_u32(&full[s]));
+          if (++s == S) { s = 0; phase ^= 1; }
+        }
+      }
     }
   } else {
     const int quad = warp & 3;   // tensor-memory lane quadrant

@@ -166,8 +166,8 @@ MXQ_DEV void prefetch_tmap(const CUtensorMap* map) {
 // sets up what needs no global memory (barriers, tensor memory, descriptor
 // prefetch), then waits for the previous grid to complete and its writes to
 // be visible before touching global memory, and lets the next kernel launch
-// early.  Every CTA of these grids is resident at once, so a dependent grid
-// waiting on free SMs can never hold up this one.
+// early.  A dependent grid can never hold up this one: it starts once every CTA
+// of this one has run that far (or left), so none still waits for an SM.
 MXQ_DEV void griddep_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 MXQ_DEV void griddep_launch_dependents() {
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");

@@ -208,7 +208,8 @@ PRODUCTS = [
     ([5, 127, 128, 129], 3, 0, 520, 512), ([300, 700], 0, 0, 256, 288), ([2] * 40, 1, 1, 24, 64),
     ([0] * 30 + [9] + [0] * 3, 0, 0, 1000, 1056), ([400, 0, 41], 0, 0, 264, 2208),
     ([70, 40, 100], 2, 1, 384, 4512), ([17, 0, 9, 70, 3], 0, 0, 136, 512),
-    ([30, 2, 65, 0], 1, 3, 264, 288), ([40] + [0] * 5 + [1], 0, 0, 200, 256)]
+    ([30, 2, 65, 0], 1, 3, 264, 288), ([40] + [0] * 5 + [1], 0, 0, 200, 256),
+    ([33, 1, 70, 20, 0, 90], 3, 0, 136, 1056)]
 
 
 @pytest.mark.parametrize("out", [BF, F32], ids=["bf16", "f32"])
