@@ -1247,14 +1247,30 @@ def adamw_state(param: torch.Tensor, bits: int = 32):
                   torch.full((blocks,), 2.0 ** -126, device=param.device)) for _ in range(2))
 
 
-def _overlap(buffers):
-    """The names of two of the (name, tensor) that share memory, or None."""
-    spans = sorted((t.data_ptr(), t.data_ptr() + t.numel() * t.element_size(), name)
-                   for name, t in buffers if t.numel())
-    for a, b in zip(spans, spans[1:]):
-        if b[0] < a[1]:
-            return a[2], b[2]
+def _overlap(names, places, tensors):
+    """The names of two of the tensors that share memory, or None."""
+    spans = sorted((a, a + t.numel() * t.element_size(), i)
+                   for i, (a, t) in enumerate(zip(places, tensors)))
+    end, last = 0, None
+    for a, b, i in spans:
+        if a == b:
+            continue
+        if a < end:
+            return names(last), names(i)
+        end, last = b, i
     return None
+
+
+def _plain_tensors(tensors, dtype, numels, dev):
+    """Whether all are contiguous CUDA tensors of dtype on device dev, each with at least
+    as many elements as its number in numels."""
+    try:
+        return (all([t.dtype is dtype for t in tensors]) and all(map(_on_gpu, tensors))
+                and all(map(torch.Tensor.is_contiguous, tensors))
+                and all([n >= m for n, m in zip(map(torch.Tensor.numel, tensors), numels)])
+                and set(map(torch.Tensor.get_device, tensors)) <= {dev})
+    except (AttributeError, TypeError):
+        return False
 
 
 class AdamWPlan:
@@ -1276,45 +1292,69 @@ class AdamWPlan:
                              "weight decays")
         self._check()
 
+    def _groups(self):
+        """[(name, dtype, tensors, elements that each must hold)] of everything written."""
+        numels = [p.numel() for p in self.params]
+        kinds = {isinstance(m, torch.Tensor) for m, _ in self.states}
+        if len(kinds) > 1:
+            raise ValueError("the states of a plan are all in 32 or all in 8 bits")
+        groups = [("params[%d]", torch.float32, self.params, [0] * len(numels))]
+        if True in kinds:
+            for k, name in enumerate(("m", "v")):
+                groups.append((f"states[%d].{name}", torch.float32, [s[k] for s in self.states],
+                               numels))
+        else:
+            blocks = [(n + 127) // 128 for n in numels]
+            for k, name in enumerate(("m", "v")):
+                groups.append((f"states[%d].{name}[0]", torch.uint8,
+                               [s[k][0] for s in self.states], numels))
+            for k, name in enumerate(("m", "v")):
+                groups.append((f"states[%d].{name}[1]", torch.float32,
+                               [s[k][1] for s in self.states], blocks))
+        self.bits = 32 if True in kinds else 8
+        return numels, groups
+
     def _check(self):
-        bits, dev, buffers, table = None, None, [], []
-        for i, (p, state, w) in enumerate(zip(self.params, self.states, self.weights)):
-            _need(p, f"params[{i}]", torch.float32, 0, dev)
-            dev, n = p.get_device(), p.numel()
-            m, v = state
-            b = 32 if isinstance(m, torch.Tensor) else 8
-            if bits is not None and b != bits:
-                raise ValueError("the states of a plan are all in 32 or all in 8 bits")
-            bits = b
-            parts = [(f"params[{i}]", p)]
-            if b == 32:
-                for name, t in (("m", m), ("v", v)):
-                    _need(t, f"states[{i}].{name}", torch.float32, n, dev)
-                    parts.append((f"states[{i}].{name}", t))
-                addresses = [m.data_ptr(), v.data_ptr(), 0, 0]
-            else:
-                for name, (codes, scales) in (("m", m), ("v", v)):
-                    _need(codes, f"states[{i}].{name}[0]", torch.uint8, n, dev)
-                    _need(scales, f"states[{i}].{name}[1]", torch.float32, (n + 127) // 128, dev)
-                    parts += [(f"states[{i}].{name}[0]", codes), (f"states[{i}].{name}[1]", scales)]
-                addresses = [m[0].data_ptr(), v[0].data_ptr(), m[1].data_ptr(), v[1].data_ptr()]
-            if w is not None:
-                _need(w, f"weights[{i}]", torch.bfloat16, n, dev)
-                parts.append((f"weights[{i}]", w))
-            buffers += parts
-            table.append(_ADAMW_TENSOR.pack(p.data_ptr(), *addresses, _ptr(w) or 0, n,
-                                            self.weight_decay[i]))
-        twice = _overlap(buffers)
+        for i, p in enumerate(self.params):
+            if not isinstance(p, torch.Tensor):
+                _need(p, f"params[{i}]", torch.float32, 0)
+        dev = self.params[0].get_device() if self.params else None
+        numels, groups = self._groups()
+        have = [i for i, w in enumerate(self.weights) if w is not None]
+        weights = [self.weights[i] for i in have]
+        for name, dtype, tensors, least in groups:
+            if not _plain_tensors(tensors, dtype, least, dev):
+                for i, t in enumerate(tensors):   # word the error
+                    _need(t, name % i, dtype, least[i], dev)
+        if not _plain_tensors(weights, torch.bfloat16, [numels[i] for i in have], dev):
+            for i in have:
+                _need(self.weights[i], f"weights[{i}]", torch.bfloat16, numels[i], dev)
+        columns = [list(map(torch.Tensor.data_ptr, g[2])) for g in groups]
+        copies = [0] * len(numels)
+        for i, a in zip(have, map(torch.Tensor.data_ptr, weights)):
+            copies[i] = a
+        every = [t for g in groups for t in g[2]] + weights
+        places = [a for c in columns for a in c] + [copies[i] for i in have]
+
+        def name(i):
+            k, n = divmod(i, max(len(numels), 1))
+            return groups[k][0] % n if i < len(numels) * len(groups) \
+                else f"weights[{have[i - len(numels) * len(groups)]}]"
+
+        twice = _overlap(name, places, every)
         if twice:
             raise ValueError(f"{twice[0]} and {twice[1]} share memory")
-        self.bits, self.device = bits or 32, dev
-        self.numels = [p.numel() for p in self.params]
-        self._movable = self.params + [w for w in self.weights if w is not None]
-        self._places = list(map(torch.Tensor.data_ptr, self._movable))
-        self._memory = [t.detach() for _, t in buffers]
-        self._table = b"".join(table)
-        self._written = {t.data_ptr() for _, t in buffers if t.numel()}
-        self._grads = struct.Struct(f"@{len(table)}P")
+        none = [0] * len(numels)
+        rows = zip(*columns, *([none] * (5 - len(columns))), copies, numels, self.weight_decay)
+        self.device, self.numels = dev, numels
+        # the moments' memory stays theirs while the plan lives; parameters and weights may
+        # move between steps
+        self._memory = [t.untyped_storage() for g in groups[1:] for t in g[2]]
+        self._movable = self.params + weights
+        self._places = columns[0] + [copies[i] for i in have]
+        self._table = b"".join([_ADAMW_TENSOR.pack(*row) for row in rows])
+        self._written = set(places) - {0}
+        self._grads = struct.Struct(f"@{len(numels)}P")
 
     def table(self):
         """The tensors' part of a launch; taken anew where one has moved."""

@@ -213,11 +213,12 @@ def test_grad_scale(bits):
     states = [mxq.adamw_state(params[0], bits)]
     grads = _grads([700], 9)
     plan = _step_and_check(params, grads, states, 1, scale=0.125)
-    before = [params[0].clone()] + [t.clone() for t in plan._memory]
+    flat = [params[0]] + [t for s in states[0] for t in (s if bits == 8 else [s])]
+    before = [t.clone() for t in flat]
     for bad in (float("nan"), float("inf"), -float("inf")):
         mxq.adamw_step(plan, grads, 2, 1e-3, grad_scale=torch.tensor([bad], device="cuda"))
     mxq.check()
-    for a, b in zip(before, [params[0]] + plan._memory):
+    for a, b in zip(before, flat):
         assert torch.equal(a, b)
 
 
