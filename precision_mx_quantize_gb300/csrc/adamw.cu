@@ -25,6 +25,7 @@ namespace {
 constexpr int A_THREADS = 256;
 constexpr int A_CHUNK = 8192;      // elements of a CTA, a multiple of A_THREADS * 4 and F_BLOCK
 constexpr float A_LEAST = 0.001953125f;   // 2^-9, the smallest code above zero
+constexpr int64_t A_CHUNKS = int64_t(1) << 31;   // of a launch, fewer than
 constexpr int A_MAX = 384;         // tensors of a launch (their table is a kernel argument)
 
 struct AdamTensor {
@@ -324,7 +325,8 @@ mxq_status adamw_launch(const mxq_adamw_tensor* t, const void* const* g, int cou
     for (; i < count && a.count < MAX; ++i) {
       if (t[i].n == 0) continue;
       const int64_t c = (t[i].n + A_CHUNK - 1) / A_CHUNK;
-      if (chunks + c >= (int64_t(1) << 31)) break;
+      if (c >= A_CHUNKS) return MXQ_ERR_ARG;
+      if (chunks + c >= A_CHUNKS) break;   // the next launch takes it
       AdamTensor& d = a.t[a.count];
       d.p = t[i].param;
       d.m = t[i].m;

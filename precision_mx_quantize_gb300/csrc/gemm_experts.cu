@@ -13,9 +13,10 @@
 // there is no first kernel: the product's makes the table and A's chunks itself.
 //
 // rows: rows of a tile past the expert's end are the next expert's; they are computed
-// and not stored.  Experts with few rows have tiles of their own (gemm_few.cuh).  wgrad: offsets are multiples of an MMA's K (32 elements, E2M1 64),
-// so the last stage of an expert issues one to four MMAs and none reads the next
-// expert's codes; an expert without rows gets zeros.
+// and not stored.  Experts with few rows have tiles of their own (gemm_few.cuh).
+// wgrad: offsets are multiples of an MMA's K (32 elements, E2M1 64), so the last stage of
+// an expert issues one to four MMAs and none reads the next expert's codes; an expert
+// without rows gets zeros.
 #include <string.h>
 
 #include "gemm_few.cuh"

@@ -163,6 +163,7 @@ def test_adamw_refusals():
     for kw in (dict(beta1=1.0), dict(beta1=-0.1), dict(beta2=nan), dict(eps=-1.0), dict(eps=nan),
                dict(step=0), dict(grad_dtype=2), dict(state_bits=16)):
         assert _adamw(**kw) == 1, kw
+    assert _adamw(dict(n=2 ** 45)) == 1          # more chunks than a launch has
     for t in (dict(n=-1), dict(param=None), dict(m=None), dict(v=None)):
         assert _adamw(t) == 1, t
     assert _adamw(grad=None) == 1
