@@ -237,11 +237,28 @@ MXQ_DEV void write_chunk(uint8_t* chunk, const uint8_t* s, int64_t line, int64_t
                          int64_t block, int n) {
   const int lane = threadIdx.x & 31;
   uint32_t w[4];
+  // Lines lie at any byte: a word is cut out of the two aligned ones around it, eight loads
+  // in flight per lane, unless those reach past the scales' ends or the line's.
+  const uintptr_t begin = reinterpret_cast<uintptr_t>(s), end = begin + lines * kb;
+  uint32_t lo[4], hi[4], shift[4];
+  bool fast[4];
 #pragma unroll
   for (int q = 0; q < 4; ++q) {
-    w[q] = 0u;
     const int64_t r = line + lane + 32 * q;
-    if (r < lines) w[q] = scale_word(s + r * kb + block, n);
+    const uintptr_t at = begin + r * kb + block, word = at & ~uintptr_t(3);
+    shift[q] = static_cast<uint32_t>(at & 3) * 8;
+    fast[q] = r < lines && n >= 4 && word >= begin && word + 8 <= end;
+    lo[q] = hi[q] = 0u;
+    if (fast[q]) {
+      lo[q] = reinterpret_cast<const uint32_t*>(word)[0];
+      hi[q] = reinterpret_cast<const uint32_t*>(word)[1];
+    }
+  }
+#pragma unroll
+  for (int q = 0; q < 4; ++q) {
+    const int64_t r = line + lane + 32 * q;
+    w[q] = __funnelshift_r(lo[q], hi[q], shift[q]);
+    if (!fast[q] && r < lines) w[q] = scale_word(s + r * kb + block, n);
   }
   *reinterpret_cast<uint4*>(chunk + lane * 16) = make_uint4(w[0], w[1], w[2], w[3]);
 }
@@ -480,7 +497,7 @@ mxq_status experts_launch(const mxq_experts_args& q, void* stream) {
   if (!few || !tc) {
     const int64_t units = ((few ? 0 : p.tiles_a) + (tc ? 0 : p.tiles_b)) * p.kcs;
     const unsigned grid =
-        static_cast<unsigned>(std::min<int64_t>((units + 7) / 8, 4 * sm_count()));
+        static_cast<unsigned>(std::min<int64_t>((units + 7) / 8, 8 * sm_count()));
     if (!launch_early(experts_prepare<ALONG_K>, grid, 256, 0, st, r)) return MXQ_ERR_CUDA;
   }
   if constexpr (ALONG_K) {

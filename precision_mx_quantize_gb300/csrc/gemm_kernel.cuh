@@ -633,7 +633,8 @@ __global__ void __launch_bounds__(G_THREADS, 1)
       MXQ_TMEM_LD32(taddr + 32, (v + 32));
       MXQ_TMEM_LD32(taddr + 64, (v + 64));
       MXQ_TMEM_LD32(taddr + 96, (v + 96));
-      tmem_ld_wait();
+#pragma unroll
+      for (int i = 0; i < 128; i += 16) MXQ_TMEM_WAIT16((v + i));
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive_cluster_relaxed(empty_leader);
