@@ -188,6 +188,7 @@ struct RowsArgs {
 };
 
 constexpr int R_THREADS = 256;
+constexpr int R_MOST = 8;   // choices handled together, at most
 
 // Rows of up to G choices of a token from j0 on and their weights.  ready() puts -1 and
 // weight 0 where a choice has no row, so that what follows needs no branches; a row
@@ -697,20 +698,28 @@ bool rows_launch_group(RowsOp op, int64_t ctas, cudaStream_t st, const RowsArgs&
     case GATHER:
       return launch_early(expert_gather<T, VEC, G>, static_cast<unsigned>(ctas), R_THREADS, 0, st,
                           a);
-    case COMBINE:
-      if constexpr (VEC) {
-        if (a.topk <= G)
-          return rows_launch_resident<expert_combine_ring<T, G>, (C_AHEAD + 1) * G * R_THREADS * 16>(
-              ctas, st, a);
+    case COMBINE: {
+      constexpr int SMEM = (C_AHEAD + 1) * G * R_THREADS * 16;
+      if constexpr (VEC && G < R_MOST) {   // no more choices than G
+        return rows_launch_resident<expert_combine_ring<T, G>, SMEM>(ctas, st, a);
+      } else {
+        if constexpr (VEC)
+          if (a.topk <= G)
+            return rows_launch_resident<expert_combine_ring<T, G>, SMEM>(ctas, st, a);
+        return rows_launch_resident<expert_combine<T, VEC, G>>(ctas, st, a);
       }
-      return rows_launch_resident<expert_combine<T, VEC, G>>(ctas, st, a);
-    default:
-      if constexpr (VEC && G > 4) {
-        if (a.topk <= G)
-          return rows_launch_resident<expert_combine_backward_ring<T, G>,
-                                      (C_AHEAD + 1) * (G + 1) * R_THREADS * 16>(ctas, st, a);
+    }
+    default: {
+      constexpr int SMEM = (C_AHEAD + 1) * (G + 1) * R_THREADS * 16;
+      if constexpr (VEC && G > 4 && G < R_MOST) {
+        return rows_launch_resident<expert_combine_backward_ring<T, G>, SMEM>(ctas, st, a);
+      } else {
+        if constexpr (VEC && G > 4)
+          if (a.topk <= G)
+            return rows_launch_resident<expert_combine_backward_ring<T, G>, SMEM>(ctas, st, a);
+        return rows_launch_resident<expert_combine_backward<T, VEC, G>>(ctas, st, a);
       }
-      return rows_launch_resident<expert_combine_backward<T, VEC, G>>(ctas, st, a);
+    }
   }
 }
 
@@ -722,7 +731,7 @@ bool rows_launch(RowsOp op, int64_t ctas, cudaStream_t st, const RowsArgs& a) {
   if (a.topk <= 2) return rows_launch_group<T, VEC, 2>(op, ctas, st, a);
   if (a.topk <= 4) return rows_launch_group<T, VEC, 4>(op, ctas, st, a);
   if (a.topk <= 6) return rows_launch_group<T, VEC, 6>(op, ctas, st, a);
-  return rows_launch_group<T, VEC, 8>(op, ctas, st, a);
+  return rows_launch_group<T, VEC, R_MOST>(op, ctas, st, a);
 }
 
 mxq_status rows_run(RowsOp op, const mxq_expert_rows_args* q, void* stream) {

@@ -73,7 +73,8 @@ def test_order_of_ids_past_32_bits():
 # ---- gather, combine ------------------------------------------------------------------
 
 ROWS = [(1, 1, 1, 1, 1), (1, 8, 64, 256, 1), (5, 3, 4, 33, 32), (40, 2, 3, 1001, 32),
-        (33, 9, 16, 64, 16), (64, 17, 5, 8, 1), (7, 4, 1024, 4096, 2), (3, 2, 2, 5000, 32)]
+        (33, 9, 16, 64, 16), (64, 17, 5, 8, 1), (7, 4, 1024, 4096, 2), (3, 2, 2, 5000, 32),
+        (20, 5, 8, 72, 1), (900, 6, 6, 128, 32), (12, 7, 9, 4104, 1), (700, 8, 20, 264, 64)]
 
 
 def _routing(tokens, topk, experts, align, seed):
