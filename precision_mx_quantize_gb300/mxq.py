@@ -1262,10 +1262,10 @@ def _overlap(names, places, tensors):
 
 
 def _plain_tensors(tensors, dtype, numels, dev):
-    """Whether all are contiguous CUDA tensors of dtype on device dev, each with at least
-    as many elements as its number in numels."""
+    """Whether all are contiguous CUDA tensors of dtype on device dev (host tensors have no
+    device index of a GPU), each with at least as many elements as its number in numels."""
     try:
-        return (all([t.dtype is dtype for t in tensors]) and all(map(_on_gpu, tensors))
+        return (all([t.dtype is dtype for t in tensors]) and all(map(_on_gpu, tensors[:1]))
                 and all(map(torch.Tensor.is_contiguous, tensors))
                 and all([n >= m for n, m in zip(map(torch.Tensor.numel, tensors), numels)])
                 and set(map(torch.Tensor.get_device, tensors)) <= {dev})
@@ -1370,7 +1370,7 @@ class AdamWPlan:
         try:
             dtypes = {g.dtype for g in grads}
             ok = (len(dtypes) == 1 and list(map(torch.Tensor.numel, grads)) == self.numels
-                  and all(map(torch.Tensor.is_contiguous, grads)) and all(map(_on_gpu, grads))
+                  and all(map(torch.Tensor.is_contiguous, grads))
                   and set(map(torch.Tensor.get_device, grads)) == {self.device})
         except (AttributeError, TypeError):
             ok = False
