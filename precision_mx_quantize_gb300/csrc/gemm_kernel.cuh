@@ -10,7 +10,7 @@
 // shared-memory traffic (TMA writes + tensor-core reads) within bandwidth.
 //   warp 0     (both CTAs) TMA producer: own A rows and own B half, 128 B of
 //              K per stage with 128-byte swizzle, plus the stage's scale
-//              chunks (own 128 A rows, all 256 B rows) into a 6-stage ring;
+//              chunks (own 128 A rows, all 256 B rows) into a ring of five or six;
 //   warp 1     (both CTAs) allocates the pair's tensor memory.  In the
 //              leader CTA one lane issues the four pair MMAs of each stage
 //              into the fp32 accumulators (each CTA: 128 lanes x 256
