@@ -1274,12 +1274,15 @@ def _plain_tensors(tensors, dtype, numels, dev):
 
 
 class AdamWPlan:
-    """The tensors that adamw_step updates, checked once.  It keeps them, and its own
-    reference to their memory; a parameter or weight that has moved since is looked up
-    anew at the next step (the moments stay where they are)."""
+    """The tensors that adamw_step updates, checked once.  It keeps them; where one of
+    them, a moment too, has moved since (its .data replaced, its storage resized), all
+    are checked and looked up anew at the next step.  A captured step goes on with the
+    memory that they had when it was captured."""
 
     def __init__(self, params, states, weights=None, weight_decay=0.0):
-        self.params, self.states = list(params), list(states)
+        self.params = list(params)
+        self.states = [tuple(x if isinstance(x, torch.Tensor) else tuple(x) for x in s)
+                       for s in states]
         self.weights = [None] * len(self.params) if weights is None else list(weights)
         try:
             self.weight_decay = [float(weight_decay)] * len(self.params)
@@ -1314,7 +1317,7 @@ class AdamWPlan:
         self.bits = 32 if True in kinds else 8
         return numels, groups
 
-    def _check(self):
+    def _check(self, moved=False):
         for i, p in enumerate(self.params):
             if not isinstance(p, torch.Tensor):
                 _need(p, f"params[{i}]", torch.float32, 0)
@@ -1341,25 +1344,26 @@ class AdamWPlan:
             return groups[k][0] % n if i < len(numels) * len(groups) \
                 else f"weights[{have[i - len(numels) * len(groups)]}]"
 
+        if moved or 0 in places:   # a resized storage may hold less than its tensor
+            for i, t in enumerate(every):
+                if t.untyped_storage().nbytes() < (t.storage_offset() + t.numel()) * t.element_size() \
+                        and t.numel():
+                    raise ValueError(f"the storage of {name(i)} holds less than the tensor")
         twice = _overlap(name, places, every)
         if twice:
             raise ValueError(f"{twice[0]} and {twice[1]} share memory")
         none = [0] * len(numels)
         rows = zip(*columns, *([none] * (5 - len(columns))), copies, numels, self.weight_decay)
         self.device, self.numels = dev, numels
-        # the moments' memory stays theirs while the plan lives; parameters and weights may
-        # move between steps
-        self._memory = [t.untyped_storage() for g in groups[1:] for t in g[2]]
-        self._movable = self.params + weights
-        self._places = columns[0] + [copies[i] for i in have]
+        self._written, self._places = every, places
         self._table = b"".join([_ADAMW_TENSOR.pack(*row) for row in rows])
-        self._written = set(places) - {0}
+        self._starts = set(places) - {0}
         self._grads = struct.Struct(f"@{len(numels)}P")
 
     def table(self):
         """The tensors' part of a launch; taken anew where one has moved."""
-        if list(map(torch.Tensor.data_ptr, self._movable)) != self._places:
-            self._check()
+        if list(map(torch.Tensor.data_ptr, self._written)) != self._places:
+            self._check(moved=True)
         return self._table
 
     def grads(self, grads):
@@ -1384,7 +1388,7 @@ class AdamWPlan:
                 if g.numel() != n:
                     raise ValueError(f"grads[{i}] holds {g.numel()} elements, its parameter {n}")
         places = list(map(torch.Tensor.data_ptr, grads))
-        if not self._written.isdisjoint(places):
+        if not self._starts.isdisjoint(places):
             raise ValueError("a gradient shares memory with a parameter or its state")
         return self._grads.pack(*places), code
 

@@ -398,6 +398,44 @@ def test_a_parameter_that_moved(fake):
         mxq.adamw_plan([p], [mxq.adamw_state(torch.zeros(100))])
 
 
+@pytest.mark.parametrize("bits", [32, 8])
+@pytest.mark.parametrize("how", ["data", "freed", "shrunk", "grown"])
+def test_a_moment_that_moved(fake, bits, how):
+    # no step writes where a moment was: its memory may be another tensor's by now
+    p = torch.zeros(300)
+    flat = lambda state: [t for x in state for t in (x if bits == 8 else (x,))]
+    for k in range(2 if bits == 32 else 4):
+        state = mxq.adamw_state(p, bits)
+        plan = mxq.adamw_plan([p], [state])
+        first = plan.table()
+        assert plan.table() is first
+        t = flat(state)[k]
+        if how == "data":
+            t.data = t.clone()
+        else:
+            t.untyped_storage().resize_(8 if how == "shrunk" else 0)
+            if how == "grown":
+                t.resize_(2000)
+        if how in ("freed", "shrunk"):
+            with pytest.raises(ValueError):
+                mxq.adamw_step(plan, [torch.zeros(300)], 1, 1e-3)
+            assert not fake
+            continue
+        row = mxq.AdamWTensor.from_buffer_copy(plan.table())
+        names = ("m", "v") if bits == 32 else ("m", "m_scale", "v", "r_scale")
+        assert [getattr(row, n) for n in names] == [x.data_ptr() for x in flat(state)]
+
+
+def test_a_plan_keeps_the_states_it_was_given(fake):
+    p, other = torch.zeros(300), torch.zeros(300)
+    m, v = mxq.adamw_state(p)
+    state = [m, v]
+    plan = mxq.adamw_plan([p], [state])
+    state[0] = other
+    p.data = torch.zeros(300)
+    assert mxq.AdamWTensor.from_buffer_copy(plan.table()).m == m.data_ptr()
+
+
 # ---- the oracle itself ---------------------------------------------------------------------
 
 def test_oracle_order_by_hand():
