@@ -1275,9 +1275,10 @@ def _plain_tensors(tensors, dtype, numels, dev):
 
 class AdamWPlan:
     """The tensors that adamw_step updates, checked once.  It keeps them; where one of
-    them, a moment too, has moved since (its .data replaced, its storage resized), all
-    are checked and looked up anew at the next step.  A captured step goes on with the
-    memory that they had when it was captured."""
+    them, a moment too, has moved since (its .data replaced, its storage resized), or a
+    parameter or weight has another size or order at the same place, all are checked
+    and looked up anew at the next step.  A captured step goes on with the memory that
+    they had when it was captured."""
 
     def __init__(self, params, states, weights=None, weight_decay=0.0):
         self.params = list(params)
@@ -1356,13 +1357,17 @@ class AdamWPlan:
         rows = zip(*columns, *([none] * (5 - len(columns))), copies, numels, self.weight_decay)
         self.device, self.numels = dev, numels
         self._written, self._places = every, places
+        # moments are their memory: elements at the parameter's places, whatever the view
+        self._viewed, self._sizes = self.params + weights, numels + [t.numel() for t in weights]
         self._table = b"".join([_ADAMW_TENSOR.pack(*row) for row in rows])
         self._starts = set(places) - {0}
         self._grads = struct.Struct(f"@{len(numels)}P")
 
     def table(self):
         """The tensors' part of a launch; taken anew where one has moved."""
-        if list(map(torch.Tensor.data_ptr, self._written)) != self._places:
+        if (list(map(torch.Tensor.data_ptr, self._written)) != self._places
+                or list(map(torch.Tensor.numel, self._viewed)) != self._sizes
+                or not all(map(torch.Tensor.is_contiguous, self._viewed))):
             self._check(moved=True)
         return self._table
 

@@ -426,6 +426,27 @@ def test_a_moment_that_moved(fake, bits, how):
         assert [getattr(row, n) for n in names] == [x.data_ptr() for x in flat(state)]
 
 
+def test_a_parameter_with_another_view_of_its_memory(fake):
+    # the same address, but other elements or another order than the plan's
+    for weight in (False, True):
+        p, w = torch.zeros(20, 15), torch.zeros(20, 15, dtype=BF)
+        plan = mxq.adamw_plan([p], [mxq.adamw_state(p)], [w])
+        t, whole = (w, w.data) if weight else (p, p.data)
+        grads = [torch.zeros(20, 15)]
+        t.data = whole.t()
+        _refused([lambda: mxq.adamw_step(plan, grads, 1, 1e-3)], ValueError)
+        t.data = whole[:10]
+        _refused([lambda: mxq.adamw_step(plan, grads, 1, 1e-3)], ValueError)
+        assert not fake
+        if not weight:      # a shorter parameter goes with gradients of its size
+            mxq.adamw_step(plan, [torch.zeros(10, 15)], 1, 1e-3)
+            assert mxq.AdamWTensor.from_buffer_copy(fake[-1][1][0]).n == 150
+        t.data = whole
+        mxq.adamw_step(plan, grads, 1, 1e-3)
+        assert mxq.AdamWTensor.from_buffer_copy(fake[-1][1][0]).n == 300
+        fake.clear()
+
+
 def test_a_plan_keeps_the_states_it_was_given(fake):
     p, other = torch.zeros(300), torch.zeros(300)
     m, v = mxq.adamw_state(p)
