@@ -25,6 +25,8 @@ import functools
 import os
 import struct
 import threading
+from bisect import bisect_left, bisect_right
+from itertools import repeat
 
 import torch
 
@@ -1360,7 +1362,12 @@ class AdamWPlan:
         # moments are their memory: elements at the parameter's places, whatever the view
         self._viewed, self._sizes = self.params + weights, numels + [t.numel() for t in weights]
         self._table = b"".join([_ADAMW_TENSOR.pack(*row) for row in rows])
-        self._starts = set(places) - {0}
+        # first and last byte of every written piece of memory, in order, and the gradients
+        # that were found apart from them
+        self._bounds = [b for span in sorted(
+            (a, a + t.numel() * t.element_size()) for a, t in zip(places, every) if t.numel())
+            for b in span]
+        self._apart = None
         self._grads = struct.Struct(f"@{len(numels)}P")
 
     def table(self):
@@ -1393,9 +1400,24 @@ class AdamWPlan:
                 if g.numel() != n:
                     raise ValueError(f"grads[{i}] holds {g.numel()} elements, its parameter {n}")
         places = list(map(torch.Tensor.data_ptr, grads))
-        if not self._starts.isdisjoint(places):
-            raise ValueError("a gradient shares memory with a parameter or its state")
-        return self._grads.pack(*places), code
+        packed = self._grads.pack(*places)
+        if self._apart != (packed, code):   # the same places of as many bytes: known
+            size = grads[0].element_size()
+            first = list(map(bisect_right, repeat(self._bounds), places))
+            last = list(map(bisect_left, repeat(self._bounds),
+                            [a + n * size for a, n in zip(places, self.numels)]))
+            if first != last or any([k & 1 for k in first]):
+                for i, g in enumerate(grads):
+                    self.need_apart(g, places[i], f"grads[{i}]")
+            self._apart = packed, code
+        return packed, code
+
+    def need_apart(self, t, at, name):
+        """t, at address `at`, shares no memory with what a step writes."""
+        end = at + t.numel() * t.element_size()
+        k = bisect_right(self._bounds, at)
+        if at < end and (k & 1 or k != bisect_left(self._bounds, end)):
+            raise ValueError(f"{name} shares memory with a parameter, its weight or its state")
 
 
 def adamw_plan(params, states, weights=None, weight_decay=0.0):
@@ -1406,12 +1428,14 @@ def adamw_plan(params, states, weights=None, weight_decay=0.0):
     return AdamWPlan(params, states, weights, weight_decay)
 
 
-def _scalar(value, name, dtype, dev):
+def _scalar(value, name, dtype, plan):
     """(number, device address or 0) of a number or a 1-element CUDA tensor."""
     if not isinstance(value, torch.Tensor):
         return value, 0
-    _need(value, name, dtype, 1, dev)
-    return 1, value.data_ptr()
+    _need(value, name, dtype, 1, plan.device)
+    at = value.data_ptr()
+    plan.need_apart(value, at, name)
+    return 1, at
 
 
 def adamw_step(plan: AdamWPlan, grads, step, lr, betas=(0.9, 0.999), eps=1e-8, grad_scale=None):
@@ -1423,11 +1447,11 @@ def adamw_step(plan: AdamWPlan, grads, step, lr, betas=(0.9, 0.999), eps=1e-8, g
         return
     table, dev = plan.table(), plan.device
     places, code = plan.grads(grads)
-    t, t_at = _scalar(step, "step", torch.int64, dev)
-    rate, rate_at = _scalar(lr, "lr", torch.float32, dev)
+    t, t_at = _scalar(step, "step", torch.int64, plan)
+    rate, rate_at = _scalar(lr, "lr", torch.float32, plan)
     scale_at = 0
     if grad_scale is not None:
         _need(grad_scale, "grad_scale", torch.float32, 1, dev)
-        scale_at = grad_scale.data_ptr()
+        _, scale_at = _scalar(grad_scale, "grad_scale", torch.float32, plan)
     a = _ADAMW_ARGS.pack(rate, betas[0], betas[1], eps, t, rate_at, t_at, scale_at, code, plan.bits)
     _ok(mxq_adamw(table, places, len(plan.params), a, _stream(dev)), "mxq_adamw")

@@ -447,6 +447,46 @@ def test_a_parameter_with_another_view_of_its_memory(fake):
         fake.clear()
 
 
+@pytest.mark.parametrize("bits", [32, 8])
+def test_a_gradient_that_overlaps_what_is_written(fake, bits):
+    # all of it from one buffer, 1200 bytes to a piece: parameter, gradient, weight, states
+    byte = torch.zeros(20000, dtype=U8)
+    cut = lambda at, n, dtype: byte[at:at + n * (torch.ones(1, dtype=dtype).element_size())].view(dtype)
+    p, w = cut(1200, 300, F32), cut(3600, 300, BF)
+    state = (cut(6000, 300, F32), cut(7200, 300, F32)) if bits == 32 else \
+        ((cut(6000, 300, U8), cut(7200, 3, F32)), (cut(8400, 300, U8), cut(9600, 3, F32)))
+    plan = mxq.adamw_plan([p], [state], [w])
+    grad = lambda at, dtype=F32: mxq.adamw_step(plan, [cut(at, 300, dtype)], 1, 1e-3)
+    for at in (0, 2400, 4800, 12000):      # between the pieces, up to their first bytes
+        grad(at)
+        grad(at)
+    grad(600, BF)
+    assert len(fake) == 9
+    fake.clear()
+    ends = (8396,) if bits == 32 else (6296, 7208, 8696, 9608)
+    starts = (6000, 7200) if bits == 32 else (6000, 7200, 8400, 9600)
+    _refused([lambda at=at: grad(at) for at in
+              (4, 1196, 1200, 1204, 2396, 2404, 3600, 4196) + starts + ends
+              + tuple(s - 1196 for s in starts)] + [lambda: grad(604, BF), lambda: grad(1796, BF)],
+             ValueError)
+    # numbers in device memory are read while the tensors are written
+    one, step = torch.ones(1), torch.ones(2, dtype=torch.int64)
+    g = [torch.zeros(300)]
+    _refused([lambda: mxq.adamw_step(plan, g, 1, p[299:]), lambda: mxq.adamw_step(plan, g, 1, 1e-3,
+                                                                              grad_scale=p[:1]),
+              lambda: mxq.adamw_step(plan, g, cut(7200, 1, torch.int64), 1e-3)], ValueError)
+    assert not fake
+    mxq.adamw_step(plan, g, step, one, grad_scale=one)
+    # an empty parameter's gradient is nowhere
+    empty = mxq.adamw_plan([p, torch.zeros(0)], [state, mxq.adamw_state(torch.zeros(0), bits)])
+    mxq.adamw_step(empty, [torch.zeros(300), p[:0]], 1, 1e-3)
+    # the parameter moves to where the gradient is
+    plan = mxq.adamw_plan([p], [state])
+    mxq.adamw_step(plan, g, 1, 1e-3)
+    p.data = g[0].data
+    _refused([lambda: mxq.adamw_step(plan, g, 1, 1e-3)], ValueError)
+
+
 def test_a_plan_keeps_the_states_it_was_given(fake):
     p, other = torch.zeros(300), torch.zeros(300)
     m, v = mxq.adamw_state(p)
