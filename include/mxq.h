@@ -27,8 +27,10 @@
  *  - All pointers named x, codes, scales, A, B, C, out, workspace are DEVICE
  *    pointers owned by the caller; the library never frees or keeps them.
  *  - `stream` is a cudaStream_t passed as void* (NULL = legacy default
- *    stream).  Every call only enqueues work on that stream and returns;
- *    argument errors are reported synchronously, device-side errors (a wait
+ *    stream) of the calling thread's current device, which must be the one
+ *    that holds the pointers (NULL names the current device's stream, so a
+ *    call cannot notice another).  Every call only enqueues work on that
+ *    stream and returns; argument errors are reported synchronously, device-side errors (a wait
  *    that timed out) by mxq_check().
  *  - Tensors are row-major.  A [rows, cols] bf16 tensor has row stride cols.
  *  - E4M3 and E5M2 codes take one byte per element.  E2M1 codes take half a

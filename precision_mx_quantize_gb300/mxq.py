@@ -203,19 +203,27 @@ def lib() -> ctypes.CDLL:
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+
+
 def _stream(device=None) -> int:
-    """The raw handle of the current CUDA stream of `device` (default: the
-    current device).  Uses torch's raw-handle accessor when it has one, which
-    skips building a Stream object on every call."""
-    if _raw_stream is not None:
-        if device is None:
+    """The raw handle of the current CUDA stream of `device`, which must be the
+    current device (the default): handle 0 is the default stream of whichever
+    device is current, and a launch there would take another device's memory.
+    Uses torch's raw-handle accessors when it has them, which skip building a
+    Stream object and torch's own set-up on every call."""
+    if device is None:
+        idx = torch.cuda.current_device()
+    else:
+        idx = device if isinstance(device, int) else torch.device(device).index
+        if idx is None:
             idx = torch.cuda.current_device()
-        elif isinstance(device, int):
-            idx = device
-        else:
-            idx = device.index if device.index is not None else torch.cuda.current_device()
+        elif idx != _current_device():
+            raise ValueError(f"the tensors are on CUDA device {idx}, the current device is "
+                             f"{_current_device()}: make the call inside torch.cuda.device({idx})")
+    if _raw_stream is not None:
         return _raw_stream(idx)
-    return torch.cuda.current_stream(device).cuda_stream
+    return torch.cuda.current_stream(idx).cuda_stream
 
 
 def _ok(status: int, where: str):
@@ -391,7 +399,8 @@ def mxq_check(stream=None):
 
 
 def check(device=None):
-    """Synchronize the current stream and raise on any recorded device error."""
+    """Synchronize the current stream and raise on any error recorded on the device (the
+    current one, which `device` must be where it is given)."""
     _ok(mxq_check(_stream(device)), "mxq_check")
 
 
@@ -566,11 +575,11 @@ def mx_quantize_dual(x: torch.Tensor, fmt_r="e4m3", had_r=False, fmt_c="e2m1", h
     if SCALE_LAYOUTS[scale_layout] == SCALES_ROWMAJOR:
         _ok(mxq_quantize_dual(x.data_ptr(), x.shape[0], x.shape[1], FMTS[fmt_r], int(had_r),
                               cr.data_ptr(), sr.data_ptr(), FMTS[fmt_c], int(had_c), cc.data_ptr(),
-                              sc.data_ptr(), _stream(x.device)), "mxq_quantize_dual")
+                              sc.data_ptr(), _stream(x.get_device())), "mxq_quantize_dual")
     else:
         _ok(mxq_quantize_dual_ex(x.data_ptr(), x.shape[0], x.shape[1], FMTS[fmt_r], int(had_r),
                                  cr.data_ptr(), sr.data_ptr(), FMTS[fmt_c], int(had_c),
-                                 cc.data_ptr(), sc.data_ptr(), SCALES_TC, _stream(x.device)),
+                                 cc.data_ptr(), sc.data_ptr(), SCALES_TC, _stream(x.get_device())),
             "mxq_quantize_dual_ex")
     return cr, sr, cc, sc
 
@@ -586,7 +595,7 @@ def mx_quantize_ablation(x: torch.Tensor, axis="col", fmt="e2m1", hadamard=True,
     _ok(mxq_quantize_ablation(x.data_ptr(), x.shape[0], x.shape[1], AXES[axis], FMTS[fmt],
                               int(hadamard), int(sign_mask) & 0xFFFFFFFF, int(stochastic),
                               int(seed) & 0xFFFFFFFFFFFFFFFF, codes.data_ptr(), scales.data_ptr(),
-                              _stream(x.device)), "mxq_quantize_ablation")
+                              _stream(x.get_device())), "mxq_quantize_ablation")
     return codes, scales
 
 
@@ -622,7 +631,7 @@ def mx_gemm(A, sA, B, sB, fmt, M, N, K, out_dtype=torch.float32, out=None, works
     _need(out, "out", out_dtype, M * N, dev)
     if SCALE_LAYOUTS[scale_layout] == SCALES_TC:
         _ok(mxq_gemm_ex(A.data_ptr(), sA.data_ptr(), B.data_ptr(), sB.data_ptr(), FMTS[fmt], M, N,
-                        K, out.data_ptr(), od, SCALES_TC, None, 0, _stream(A.device)),
+                        K, out.data_ptr(), od, SCALES_TC, None, 0, _stream(A.get_device())),
             "mxq_gemm_ex")
         return out
     if workspace is None:
@@ -630,7 +639,7 @@ def mx_gemm(A, sA, B, sB, fmt, M, N, K, out_dtype=torch.float32, out=None, works
     _need(workspace, "workspace", torch.uint8, 0, dev)   # its size is checked by the library
     _ok(mxq_gemm(A.data_ptr(), sA.data_ptr(), B.data_ptr(), sB.data_ptr(), FMTS[fmt], M, N, K,
                  out.data_ptr(), od, workspace.data_ptr(), workspace.numel(),
-                 _stream(A.device)), "mxq_gemm")
+                 _stream(A.get_device())), "mxq_gemm")
     return out
 
 
@@ -686,7 +695,7 @@ def mx_gemm_quantize(A, sA, B, sB, fmt, M, N, K, out_fmt="e4m3", out=None, works
             workspace = gemm_workspace(M, N, K, fmt, A.device)
         _ok(mxq_gemm_quantize(A.data_ptr(), sA.data_ptr(), B.data_ptr(), sB.data_ptr(), FMTS[fmt], M,
                               N, K, FMTS[out_fmt], codes.data_ptr(), scales.data_ptr(),
-                              workspace.data_ptr(), workspace.numel(), _stream(A.device)),
+                              workspace.data_ptr(), workspace.numel(), _stream(A.get_device())),
             "mxq_gemm_quantize")
         return codes, scales
     if not in_tc and workspace is None:
@@ -695,7 +704,7 @@ def mx_gemm_quantize(A, sA, B, sB, fmt, M, N, K, out_fmt="e4m3", out=None, works
     _ok(mxq_gemm_quantize_ex(A.data_ptr(), sA.data_ptr(), B.data_ptr(), sB.data_ptr(), FMTS[fmt], M,
                              N, K, SCALE_LAYOUTS[scale_layout], FMTS[out_fmt], codes.data_ptr(),
                              scales.data_ptr(), SCALE_LAYOUTS[out_scale_layout], ws_ptr, ws_n,
-                             _stream(A.device)), "mxq_gemm_quantize_ex")
+                             _stream(A.get_device())), "mxq_gemm_quantize_ex")
     return codes, scales
 
 
