@@ -30,8 +30,8 @@
  *    stream) of the calling thread's current device, which must be the one
  *    that holds the pointers (NULL names the current device's stream, so a
  *    call cannot notice another).  Every call only enqueues work on that
- *    stream and returns; argument errors are reported synchronously, device-side errors (a wait
- *    that timed out) by mxq_check().
+ *    stream and returns; argument errors are reported synchronously,
+ *    device-side errors (a wait that timed out) by mxq_check().
  *  - Tensors are row-major.  A [rows, cols] bf16 tensor has row stride cols.
  *  - E4M3 and E5M2 codes take one byte per element.  E2M1 codes take half a
  *    byte: two per byte along the blocked axis, the even element in the low
@@ -607,7 +607,8 @@ size_t mxq_gemm_experts_wgrad_workspace_size(int64_t rows, int64_t M, int64_t N,
  *   m = beta1 m + (1 - beta1) g,   v = beta2 v + (1 - beta2) g^2
  *   p = p - lr weight_decay p
  *         - lr / (1 - beta1^t) * m / (sqrt(v / (1 - beta2^t)) + eps)
- * in fp32, one rounding per operation of m and v.  state_bits 32: m and v in fp32.
+ * in fp32, one rounding per operation of m and v, for sqrt(v), and for the quotient.
+ * state_bits 32: m and v in fp32.
  * state_bits 8: m and r = sqrt(v) as E4M3 codes with one fp32 scale per 128 elements
  * (the last block of a tensor shorter):
  *   scale = max(amax * RN(1 / 448), 2^-126),   code = RN_sat(value * (1 / scale))

@@ -250,3 +250,26 @@ def test_a_tensor_that_moved_is_looked_up_anew():
     mxq.adamw_step(plan, g, 2, 1e-2)
     mxq.check()
     assert torch.equal(old, was) and params[0].lt(5.0).all() and params[0].gt(4.9).all()
+
+
+@pytest.mark.parametrize("bits", [32, 8])
+def test_the_step_is_a_rounded_quotient(bits):
+    # betas of 1/2 and 3/4 and a rate of 1/2 make every factor of the first step a power of
+    # two, so that from p = 0 the step is m / (2 sqrt(v)) with one rounding: numpy's, bit for bit
+    n, f = 6000, np.float32
+    state = mxq.adamw_state(torch.zeros(n, device="cuda"), bits)
+    start = mxq.adamw_plan([torch.zeros(n, device="cuda")], [state])
+    for seed in (1, 2):        # moments of unlike gradients
+        mxq.adamw_step(start, _grads([n], seed), seed, 1e-3)
+    from oracle import mx_oracle as O
+    table = O.decode_table("e4m3").astype(f)
+    decode = lambda c, s: table[to_np(c)] * np.repeat(to_np(s), 128)[:n]
+    m, v = (to_np(state[0]), to_np(state[1])) if bits == 32 else \
+        (decode(*state[0]), decode(*state[1]) ** 2)
+    p, g = torch.zeros(n, device="cuda"), _grads([n], 3)
+    d = to_np(g[0])
+    mxq.adamw_step(mxq.adamw_plan([p], [state]), g, 1, 0.5, betas=(0.5, 0.75), eps=0.0)
+    mxq.check()
+    m = m * f(0.5) + d * f(0.5)
+    v = v * f(0.75) + d * d * f(0.25)
+    assert np.array_equal(to_np(p), -(m / (np.sqrt(v) * f(2))))
