@@ -185,6 +185,8 @@ struct RowsArgs {
   float* dweights;           // [tokens][topk]
   int64_t tokens, rows, cols;
   int32_t topk, experts, team;
+  int32_t parts;             // teams that clear an expert's padding
+  int64_t units;             // tokens and experts' parts
 };
 
 constexpr int R_THREADS = 256;
@@ -289,22 +291,23 @@ struct Piece<T, false> {
 };
 
 // Zeros in the rows between an expert's choices and the next expert's rows, by the
-// teams behind the tokens'.
+// teams behind the tokens': team `u` of them takes every parts-th row of an expert's.
 template <typename T, bool VEC>
-MXQ_DEV void clear_padding(const RowsArgs& a, int64_t e, int at) {
+MXQ_DEV void clear_padding(const RowsArgs& a, int64_t u, int at) {
   using P = Piece<T, VEC>;
-  if (e >= a.experts) return;
+  if (u >= a.units - a.tokens) return;
   P zero;
   zero.clear();
+  const int e = static_cast<int>(u) % a.experts, part = static_cast<int>(u) / a.experts;
   const int64_t lo = max(int64_t(a.offsets[e]) + a.counts[e], int64_t(0));
   const int64_t hi = min(int64_t(a.offsets[e + 1]), a.rows);
-  for (int64_t r = lo; r < hi; ++r)
+  for (int64_t r = lo + part; r < hi; r += a.parts)
     for (int64_t c = int64_t(at) * P::REACH; c < a.cols; c += int64_t(a.team) * P::N)
       zero.store(static_cast<T*>(a.out) + r * a.cols + c, a.team, a.cols - c);
 }
 
-// Teams walk the tokens (and, past them, the experts whose padding they clear) a grid
-// apart, and load a token's choices while the one before is on its way.
+// Teams walk the tokens (and, past them, the padding that they clear) a grid apart, and
+// load a token's choices while the one before is on its way.
 struct Team {
   int at, threads;   // place in the team, its size
   int64_t t, step;   // first token, tokens from one to the next
@@ -372,7 +375,7 @@ __global__ void __launch_bounds__(R_THREADS) expert_gather(const RowsArgs a) {
       }
     }
   }
-  for (; t < a.tokens + a.experts; t += team.step) clear_padding<T, VEC>(a, t - a.tokens, team.at);
+  for (; t < a.units; t += team.step) clear_padding<T, VEC>(a, t - a.tokens, team.at);
 }
 
 // out[t] = sum_j w[t][j] y[row of (t, j)], in the order of j, in fp32.  The loads of all
@@ -560,7 +563,7 @@ __global__ void __launch_bounds__(R_THREADS) expert_combine_backward(const RowsA
       }
     }
   }
-  for (; t < a.tokens + a.experts; t += team.step) clear_padding<T, VEC>(a, t - a.tokens, team.at);
+  for (; t < a.units; t += team.step) clear_padding<T, VEC>(a, t - a.tokens, team.at);
 }
 
 // The same for aligned rows and more than four choices, with the pieces two units ahead as
@@ -660,7 +663,7 @@ __global__ void __launch_bounds__(R_THREADS) expert_combine_backward_ring(const 
       a.dweights[t * a.topk + team.at] = s;
     }
   }
-  for (; t < a.tokens + a.experts; t += team.step) clear_padding<T, true>(a, t - a.tokens, team.at);
+  for (; t < a.units; t += team.step) clear_padding<T, true>(a, t - a.tokens, team.at);
 }
 
 enum RowsOp { GATHER, COMBINE, BACKWARD };
@@ -784,8 +787,14 @@ mxq_status rows_run(RowsOp op, const mxq_expert_rows_args* q, void* stream) {
   a.team = 32;
   while (a.team < R_THREADS && a.team * 2 <= pieces) a.team *= 2;
   const int per = R_THREADS / a.team;
-  const int64_t teams = a.tokens + a.experts;
-  const int64_t grid = (teams + per - 1) / per;
+  // The buffer says how long an expert's padding may be; only the device knows how long it
+  // is.  A team has about 32 rows (gather, 8192x8 of 64 x 4096 bf16: at an align of 4096
+  // 307 us, 898 us with one team an expert; at 256 106 and 147 us; at 32 it is one team).
+  const int64_t choices = a.tokens * a.topk;
+  const int64_t padding = a.experts ? (a.rows - choices) / std::min<int64_t>(a.experts, choices) : 0;
+  a.parts = static_cast<int32_t>(std::min<int64_t>(std::max<int64_t>((padding + 31) / 32, 1), 128));
+  a.units = a.tokens + int64_t(a.experts) * a.parts;
+  const int64_t grid = (a.units + per - 1) / per;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   using B = __nv_bfloat16;
   const bool ok = bf16 ? (vec ? rows_launch<B, true>(op, grid, st, a)

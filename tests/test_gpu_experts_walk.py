@@ -116,6 +116,34 @@ def test_rows_of_many_tokens(case, dtype):
     assert torch.equal(buf[off[-1]:], y[off[-1]:])
 
 
+@pytest.mark.parametrize("dtype", [BF, F32], ids=["bf16", "f32"])
+@pytest.mark.parametrize("case", [(50, 2, 5, 264, 4096, 0), (3000, 8, 20, 72, 1000, 0), (40, 1, 9, 33, 511, 7),
+                                  (700, 6, 30, 136, 2048, -3), (1, 1, 1024, 8, 64, 5000)], ids=str)
+def test_long_padding(case, dtype):
+    # several teams to an expert's padding, in buffers of the exact size, shorter or longer ones
+    tokens, topk, experts, cols, align, more = case
+    g = _gen(tokens)
+    ids = torch.randint(-1, experts, (tokens, topk), device="cuda", generator=g)
+    dev = row_of, offsets, counts = mxq.expert_order(ids, experts, align)
+    off, n = offsets.tolist(), counts.tolist()
+    end = off[-1]
+    rows = max(end + more, 1)
+    x = torch.randn(tokens, cols, device="cuda", generator=g).to(dtype)
+    y = torch.randn(rows, cols, device="cuda", generator=g).to(dtype)
+    want = torch.full((rows + 4, cols), 7.0, dtype=dtype, device="cuda")
+    want[:min(end, rows)] = 0.0
+    for j in range(topk):
+        h = (row_of[:, j] >= 0) & (row_of[:, j] < rows)
+        want[row_of[h, j].long()] = x[h]
+    out = torch.full((rows + 4, cols), 7.0, dtype=dtype, device="cuda")
+    mxq.expert_gather(x, *dev, rows, out=out)
+    assert torch.equal(out, want)
+    out.fill_(7.0)
+    mxq.expert_combine_backward(x, y, *dev, out=out)
+    assert torch.equal(out, want)
+    mxq.check()
+
+
 # ---- products -------------------------------------------------------------------------
 
 BAD = {"e4m3": [0x7F, 0xFF], "e5m2": [c | s for c in (0x7C, 0x7D, 0x7E, 0x7F) for s in (0, 0x80)],
