@@ -343,14 +343,18 @@ __global__ void __launch_bounds__(W_THREADS, 2)
   if (warp == 1) tmem_dealloc(tmem, F::TMEM);
 }
 
-// Launches the kernel on two CTAs per SM, at most `items`.
+// Launches the kernel on as many CTAs as the device holds, at most `items`.
 template <typename Work, int T>
 mxq_status gemm_few_run(const typename Work::Params& g, int64_t items, void* stream) {
   // the table takes what this launch's experts need
   const int smem = Few<T>::FIXED + (Work::table_bytes(g) + 15) / 16 * 16;
   if (!ensure_dynamic_smem(reinterpret_cast<const void*>(mx_gemm_few<Work, T>), smem))
     return MXQ_ERR_CUDA;
-  const unsigned grid = static_cast<unsigned>(std::min<int64_t>(items, 2 * sm_count()));
+  // Of an SM's 228 KB a CTA takes its own and 1 KB: the table of 640 experts (T 64; T 16:
+  // 981) and more leaves room for one.  A second half of the grid that waited for the first
+  // to end took 339 us where one takes 281 (1024 experts of 8 rows, 1024x1024 E4M3).
+  const int per_sm = 2 * (smem + 1024) <= 228 * 1024 ? 2 : 1;
+  const unsigned grid = static_cast<unsigned>(std::min<int64_t>(items, per_sm * sm_count()));
   if (!launch_early(mx_gemm_few<Work, T>, grid, W_THREADS, smem, static_cast<cudaStream_t>(stream),
                     g))
     return MXQ_ERR_CUDA;
