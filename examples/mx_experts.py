@@ -49,9 +49,8 @@ def main(tokens=600, experts=6, topk=2, in_f=256, out_f=384, steps=40, lr=0.02, 
         layer.requantize()
     # one token: its rows alone, without padding
     one, w1 = route(x[:1], router, topk)
-    r1, o1, c1 = mxq.expert_order(one, experts)
-    served = layer.infer(mxq.expert_gather(x[:1].contiguous(), r1, o1, c1, topk), o1)
-    served = mxq.expert_combine(served, r1, w1)
+    rows1, (r1, o1, _) = layer.dispatch(x[:1], one, padded=False)
+    served = mxq.expert_combine(layer.infer(rows1, o1), r1, w1)
     trained = mxq.expert_combine(layer.forward(rows, offsets)[0], row_of, weights)[:1]
     gap = (served.float() - trained.float()).norm() / trained.float().norm()
     mxq.check()

@@ -10,7 +10,7 @@ use them:
   the columns wait for the weight gradient), the product grouped by expert;
 * backward(): both layouts of dy, the input gradient against the transposed codes, and
   one weight gradient per expert in fp32;
-* infer(): the rows alone, for a server's tokens.
+* infer(): the rows alone, for a server's tokens, dispatched without padding.
 
 The offsets of the experts' rows stay on the device.  Host code only: every operation is
 one of mxq's calls on the current stream.
@@ -61,11 +61,14 @@ class MxExpertLinear:
             mxq.mx_quantize_dual(self.weight[i], self.fmt, False, self.fmt, False,
                                  out=tuple(t[i] for t in self.operands), scale_layout=self.layout)
 
-    def dispatch(self, x, ids):
+    def dispatch(self, x, ids, padded=True):
         """x [tokens, in] bf16, ids [tokens, topk] -> (rows [capacity, in], routing): what
-        forward() and backward() take, and the places to gather from and combine into."""
-        routing = mxq.expert_order(ids, self.experts, self.align)
-        rows = mxq.expert_rows(ids.numel(), self.experts, self.align)
+        forward() and backward() take, and the places to gather from and combine into.
+        padded False: the choices' rows alone, for infer() (backward() needs the padding;
+        a token of eight experts has 8 rows then, and 256 with it)."""
+        align = self.align if padded else 1
+        routing = mxq.expert_order(ids, self.experts, align)
+        rows = mxq.expert_rows(ids.numel(), self.experts, align)
         return mxq.expert_gather(x, *routing, rows), routing
 
     def forward(self, rows, offsets):

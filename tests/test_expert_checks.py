@@ -335,6 +335,15 @@ def test_layer_makes_the_operands_it_needs(fake):
     assert MxExpertLinear(torch.zeros(1, 32, 32, dtype=BF), wgrad_fmt="e2m1").align == 64
 
 
+def test_layer_dispatches_a_servers_tokens_without_padding(fake):
+    layer = MxExpertLinear(torch.zeros(64, 128, 256, dtype=BF))
+    x, ids = torch.zeros(1, 256, dtype=BF), torch.zeros(1, 8, dtype=torch.int64)
+    rows, (row_of, offsets, counts) = layer.dispatch(x, ids, padded=False)
+    assert rows.shape == (8, 256) and fake[-2][0] == "mxq_expert_order" and fake[-2][1][4] == 1
+    assert layer.infer(rows, offsets).shape == (8, 128)
+    assert layer.dispatch(x, ids)[0].shape == (256, 256) and fake[-2][1][4] == 32
+
+
 def test_adamw_bindings(fake):
     params = [torch.zeros(5, 7), torch.zeros(300), torch.zeros(0)]
     for bits in (32, 8):

@@ -146,6 +146,25 @@ def test_a_step_in_a_graph():
         assert not torch.equal(m2, before[0])
 
 
+@pytest.mark.parametrize("shape", [(1, 64, 8, 64, 256), (13, 9, 4, 96, 160)], ids=str)
+def test_a_servers_tokens_without_padding(shape):
+    tokens, experts, topk, out_f, in_f = shape
+    layer = _layer(experts, out_f, in_f)
+    x, ids = synth.normal((tokens, in_f), 1).cuda(), _ids(tokens, topk, experts, 2)
+    rows, (row_of, offsets, counts) = layer.dispatch(x, ids, padded=False)
+    assert rows.shape == (tokens * topk, in_f)
+    for t, j in np.ndindex(tokens, topk):
+        assert torch.equal(rows[int(row_of[t, j])], x[t])
+    y = layer.infer(rows, offsets)
+    mxq.check()
+    w = _f(layer.weight)
+    q = [O.quantize_any(w[e].astype(np.float32), "row", "e4m3", False) for e in range(experts)]
+    A, sA = O.quantize_any(_f(rows).astype(np.float32), "row", "e4m3", False)
+    ref, S = E.experts_product(A, sA, [v[0] for v in q], [v[1] for v in q],
+                               to_np(offsets).astype(np.int64), "e4m3", np.zeros((rows.shape[0], out_f)))
+    _near(y, ref, S, in_f)
+
+
 def test_requantize_follows_the_weights():
     layer = _layer(3, 64, 128)
     rows = synth.normal((32, 128), 1).cuda()
