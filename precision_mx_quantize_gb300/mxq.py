@@ -1258,14 +1258,17 @@ def adamw_state(param: torch.Tensor, bits: int = 32):
                   torch.full((blocks,), 2.0 ** -126, device=param.device)) for _ in range(2))
 
 
-def _overlap(names, places, tensors):
-    """The names of two of the tensors that share memory, or None."""
-    spans = sorted((a, a + t.numel() * t.element_size(), i)
-                   for i, (a, t) in enumerate(zip(places, tensors)))
+def _spans(places, tensors):
+    """[(first byte, end, index)] of the tensors' memory, in order."""
+    sizes = [n * z for n, z in zip(map(torch.Tensor.numel, tensors),
+                                   map(torch.Tensor.element_size, tensors))]
+    return sorted([(a, a + n, i) for i, (a, n) in enumerate(zip(places, sizes)) if n])
+
+
+def _overlap(names, spans):
+    """The names of two of the spans' tensors that share memory, or None."""
     end, last = 0, None
     for a, b, i in spans:
-        if a == b:
-            continue
         if a < end:
             return names(last), names(i)
         end, last = b, i
@@ -1361,7 +1364,8 @@ class AdamWPlan:
                 if t.untyped_storage().nbytes() < (t.storage_offset() + t.numel()) * t.element_size() \
                         and t.numel():
                     raise ValueError(f"the storage of {name(i)} holds less than the tensor")
-        twice = _overlap(name, places, every)
+        spans = _spans(places, every)
+        twice = _overlap(name, spans)
         if twice:
             raise ValueError(f"{twice[0]} and {twice[1]} share memory")
         none = [0] * len(numels)
@@ -1373,9 +1377,7 @@ class AdamWPlan:
         self._table = b"".join([_ADAMW_TENSOR.pack(*row) for row in rows])
         # first and last byte of every written piece of memory, in order, and the gradients
         # that were found apart from them
-        self._bounds = [b for span in sorted(
-            (a, a + t.numel() * t.element_size()) for a, t in zip(places, every) if t.numel())
-            for b in span]
+        self._bounds = [at for span in spans for at in span[:2]]
         self._apart = None
         self._grads = struct.Struct(f"@{len(numels)}P")
 
