@@ -1296,8 +1296,8 @@ class AdamWPlan:
 
     def __init__(self, params, states, weights=None, weight_decay=0.0):
         self.params = list(params)
-        self.states = [tuple(x if isinstance(x, torch.Tensor) else tuple(x) for x in s)
-                       for s in states]
+        self.states = [(m, v) if isinstance(m, torch.Tensor) else (tuple(m), tuple(v))
+                       for m, v in states]
         self.weights = [None] * len(self.params) if weights is None else list(weights)
         try:
             self.weight_decay = [float(weight_decay)] * len(self.params)

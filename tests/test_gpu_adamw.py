@@ -273,3 +273,32 @@ def test_the_step_is_a_rounded_quotient(bits):
     m = m * f(0.5) + d * f(0.5)
     v = v * f(0.75) + d * d * f(0.25)
     assert np.array_equal(to_np(p), -(m / (np.sqrt(v) * f(2))))
+
+
+@pytest.mark.parametrize("bits", [32, 8])
+def test_moments_that_moved_are_looked_up_anew(bits):
+    # replaced as a checkpoint's are, or given back and allocated anew: what a new plan does
+    params, grads = _params([700, 129], 1), _grads([700, 129], 2)
+    states = [mxq.adamw_state(p, bits) for p in params]
+    flat = lambda st: [t for s in st for x in s for t in (x if bits == 8 else (x,))]
+    plan = mxq.adamw_plan(params, states)
+    mxq.adamw_step(plan, grads, 1, 1e-3)
+    for step, how in ((2, "data"), (3, "storage")):
+        saved = [t.clone() for t in flat(states)]
+        for t, old in zip(flat(states), saved):
+            if how == "data":
+                t.data = old.clone()
+            else:
+                size = t.untyped_storage().nbytes()
+                t.untyped_storage().resize_(0)
+                with pytest.raises(ValueError, match="storage"):
+                    plan.table()
+                t.untyped_storage().resize_(size + 4096)
+                t.copy_(old)
+        other = [p.clone() for p in params]
+        copy = [tuple(tuple(t.clone() for t in x) if bits == 8 else x.clone() for x in s) for s in states]
+        mxq.adamw_step(plan, grads, step, 1e-3)
+        mxq.adamw_step(mxq.adamw_plan(other, copy), grads, step, 1e-3)
+        mxq.check()
+        for a, b in zip(params + flat(states), other + flat(copy)):
+            assert torch.equal(a, b)
