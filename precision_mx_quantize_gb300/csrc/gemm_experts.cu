@@ -340,9 +340,17 @@ constexpr int64_t X_LIM = int64_t(1) << 31;
 //   FEW16  17.1 (12.2)   85.8 (45.2)   89.4 (47.4)   118* (63.7*)  184* (96.5*)
 //   FEW64  24.0* (16.6*) 90.7* (51.5*) 93.5* (52.5*) 101 (52.4)    108* (60.5*)
 //   ROWS   27.2 (16.4)   97.3 (56.4)   102 (56.9)    105 (58.3)    108 (60.3)
+// With one expert that has half or nine tenths of the rows instead (512 to 8192 rows of 64
+// experts, 2048x2048 E4M3), the chosen form takes up to 1.2 times as long, and a buffer four
+// times as long as its rows, which the average counts, changes that by 8 % at most.
 // Through shared memory, the stores of a tile take less of the SM's memory path, and a
-// stage of the ring less: 9 stages to a tile, 1237 rows of 7 experts, 13.0 against 15.2
-// us; 16 stages, 62 against 58 us at an average of 32.
+// stage of the ring less.  16 experts of 512 rows, N 2048, E4M3, us staged (direct):
+//   stages of a tile      4           9            12           16           32
+//   bf16                  21.8 (24.3) 31.2 (32.3)  36.4 (36.8)  44.7 (43.7)  75.9 (71.4)
+//   fp32                  27.9 (32.1) 35.7 (40.0)  41.0 (44.2)  49.3 (51.6)  80.8 (78.4)
+// E2M1 turns between 6 and 9 stages in bf16 (3 % at 12) and at 16 in fp32.  1233 rows of 7
+// experts, N 1004, with less than a tile for every cluster, E4M3 fp32: 12 stages 13.3
+// (15.6), 16 stages 14.9 (17.2).
 Form rows_form(const mxq_experts_args& q, int64_t kbytes) {
   const int64_t average = q.rows / std::max<int64_t>(1, std::min<int64_t>(q.experts, q.rows));
   if (average <= 16) return FEW16;

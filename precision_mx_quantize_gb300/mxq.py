@@ -1435,7 +1435,8 @@ def adamw_plan(params, states, weights=None, weight_decay=0.0):
     """A plan of adamw_step: contiguous fp32 CUDA tensors `params`, for each what
     adamw_state returned, and for each a bf16 tensor of its size that receives the
     rounded parameter (the quantizers' input), or None.  weight_decay: one number, or one
-    per tensor.  No two of them may share memory."""
+    per tensor.  No two of them may share memory.  A step finds tensors that have moved
+    since, a captured one does not (AdamWPlan)."""
     return AdamWPlan(params, states, weights, weight_decay)
 
 
@@ -1453,7 +1454,8 @@ def adamw_step(plan: AdamWPlan, grads, step, lr, betas=(0.9, 0.999), eps=1e-8, g
     """One AdamW step of the plan's tensors, in place.  grads: one contiguous tensor per
     parameter, all fp32 or all bf16; step: 1 at the first step.  step (int64), lr (fp32)
     and grad_scale (fp32; a factor of the gradients, NaN or infinity to leave everything
-    as it is) may be 1-element CUDA tensors, which a captured launch reads anew."""
+    as it is) may be 1-element CUDA tensors, which a captured launch reads anew.  None of
+    what it reads may overlap what it writes."""
     if not plan.params:
         return
     table, dev = plan.table(), plan.device
